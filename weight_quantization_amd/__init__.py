@@ -33,3 +33,11 @@ from .binding import (  # noqa: F401
     load_library,
     packed_shape,
 )
+from .paged import (  # noqa: F401
+    KvPagePlan,
+    hlwq_kv_page_plan,
+    hlwq_kv_paged_append,
+    hlwq_kv_paged_attention,
+    hlwq_kv_paged_attention_workspace,
+    hlwq_prompt_attention,
+)

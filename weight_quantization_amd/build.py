@@ -3,8 +3,8 @@
 Steps:
 1. compile and run the host table generator (Lloyd-Max codebooks and the
    bucket-search tables, verified by brute force while generating);
-2. compile the kernels and the C ABI with hipcc into ``libhlwq.so`` next to
-   this file;
+2. compile the kernels and the C ABI with hipcc, one process per source, and
+   link them into ``libhlwq.so`` next to this file;
 3. compile the streaming-bandwidth probe that bench.py uses as its HBM ceiling
    into ``libhlwq_stream.so`` (include/hlwq_stream.h).
 
@@ -16,6 +16,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -26,6 +28,10 @@ LIB = os.path.join(HERE, "libhlwq.so")
 STREAM_LIB = os.path.join(HERE, "libhlwq_stream.so")
 
 ARCH = "gfx950"
+
+# the paged KV cache and attention (include/hlwq_attention.h), linked into
+# libhlwq.so with hlwq.hip
+SERVING_SOURCES = ("kv_paged.hip", "attention.hip")
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -73,10 +79,14 @@ def generate_tables() -> str:
 
 def build_library(extra_flags=(), out: str = LIB, source: str | None = None) -> str:
     generate_tables()
-    src = source or os.path.join(CSRC, "hlwq.hip")
+    sources = [source or os.path.join(CSRC, "hlwq.hip"), *(os.path.join(CSRC, s) for s in SERVING_SOURCES)]
     tmp = out + ".tmp"
-    cmd = [_hipcc(), *HIPCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", BUILD, src, "-o", tmp]
-    _run(cmd)
+    with tempfile.TemporaryDirectory(dir=BUILD) as objs, ThreadPoolExecutor(len(sources)) as ex:
+        objects = [os.path.join(objs, f"{i}.o") for i in range(len(sources))]
+        compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+        list(ex.map(lambda so: _run([_hipcc(), *compile_flags, *extra_flags, "-I", INCLUDE, "-I", BUILD, "-c", so[0],
+                                     "-o", so[1]]), zip(sources, objects)))
+        _run([_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *extra_flags, *objects, "-o", tmp])
     os.replace(tmp, out)
     return out
 

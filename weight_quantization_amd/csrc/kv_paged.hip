@@ -1,0 +1,448 @@
+// kv_paged.hip — the paged KV cache's bookkeeping and writes: page planning and
+// the append of a step's tokens (include/hlwq_attention.h).  Compiled with
+// -ffp-contract=off, so the encoder follows the operation order documented in
+// include/hlwq.h bit for bit.
+
+#include "kv_common.h"
+
+namespace hlwq_kv {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Page plan.  One workgroup plans the tables (the prefix sums over the
+// requests, the stack and the block table are one dependent chain), then a
+// grid over the rows fills the maps.
+// ---------------------------------------------------------------------------
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kRowThreads = 256;
+
+struct PlanArgs {
+  const int32_t* tokens;
+  const int32_t* n_new;
+  const uint8_t* reset;
+  const int32_t* n_free;
+  int32_t* free_pages;
+  int32_t* table;
+  int32_t* cu;
+  int32_t* lens;
+  int32_t* row_request;
+  int32_t* positions;
+  int32_t* slots;
+  int32_t* n_free_after;
+  int32_t* status;
+  int32_t requests, rows, width, n_pages, page_shift;
+  int64_t n_res;
+};
+
+// What one request asks of a step.
+struct Need {
+  int64_t held, n;    // tokens before (0 after a reset) and new
+  int64_t back;       // pages given back
+  int64_t had, want;  // pages before and after
+  bool bad;
+};
+__device__ __forceinline__ int64_t pages_of(const PlanArgs& a, int64_t tokens) {
+  const int64_t e = tokens - a.n_res;
+  return e > 0 ? (e + (int64_t{1} << a.page_shift) - 1) >> a.page_shift : 0;
+}
+__device__ __forceinline__ Need need_of(const PlanArgs& a, int32_t b) {
+  Need d;
+  const int32_t t = a.tokens[b], n = a.n_new[b];
+  const bool ended = a.reset && a.reset[b];
+  const int64_t before = pages_of(a, t);
+  d.held = ended ? 0 : t;
+  d.n = n;
+  d.back = ended ? before : 0;
+  d.had = ended ? 0 : before;
+  d.want = pages_of(a, d.held + n);
+  d.bad = t < 0 || n < 0 || before > a.width || d.want > a.width || d.held + n > 0x7fffffff;
+  if (d.bad) d.n = d.back = d.had = d.want = 0;
+  return d;
+}
+
+__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t u = __shfl_up(v, d, 64);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) hlwq_kv_plan_tables_kernel(const PlanArgs a) {
+  __shared__ int64_t sums[3][kPlanWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t per = (a.requests + kPlanThreads - 1) / kPlanThreads;
+  const int32_t b0 = static_cast<int32_t>(min(static_cast<int64_t>(threadIdx.x) * per, static_cast<int64_t>(a.requests)));
+  const int32_t b1 = min(b0 + per, a.requests);
+  const int32_t nf = a.n_free[0];
+
+  // totals and exclusive prefixes of new rows, pages given back, pages taken
+  int64_t own[3] = {0, 0, 0};
+  bool bad = nf < 0 || nf > a.n_pages;
+  for (int32_t b = b0; b < b1; ++b) {
+    const Need d = need_of(a, b);
+    bad |= d.bad;
+    own[0] += d.n;
+    own[1] += d.back;
+    own[2] += d.want - d.had;
+  }
+  int64_t pre[3], total[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int64_t s = wave_scan(own[k], lane);
+    pre[k] = s - own[k];
+    if (lane == 63) sums[k][wave] = s;
+  }
+  bad = __syncthreads_or(bad);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    total[k] = 0;
+    for (int w = 0; w < kPlanWaves; ++w) {
+      if (w == wave) pre[k] += total[k];
+      total[k] += sums[k][w];
+    }
+  }
+  bad |= total[0] > a.rows || nf + total[1] > a.n_pages;
+
+  // pages given back: where each request's begin on the stack, kept in lens
+  // until the lengths are written
+  if (!bad && total[1] > 0) {
+    int64_t at = pre[1];
+    for (int32_t b = b0; b < b1; ++b) {
+      a.lens[b] = static_cast<int32_t>(at);
+      at += need_of(a, b).back;
+    }
+    __syncthreads();
+    bool off = false;
+    for (int32_t b = wave; b < a.requests; b += kPlanWaves) {
+      if (!a.reset[b]) continue;
+      const int64_t n = pages_of(a, a.tokens[b]);
+      for (int64_t p = lane; p < n; p += 64) {
+        const int32_t id = a.table[static_cast<int64_t>(b) * a.width + p];
+        off |= id < 0 || id >= a.n_pages;
+      }
+    }
+    bad = __syncthreads_or(off);
+  }
+  const int64_t top = nf + total[1];
+  const int64_t missing = total[2] - top;
+  if (bad || missing > 0) {
+    for (int32_t b = b0; b < b1; ++b) {
+      a.cu[b] = 0;
+      a.lens[b] = a.tokens[b];
+    }
+    if (threadIdx.x == 0) {
+      a.cu[a.requests] = 0;
+      *a.n_free_after = nf;
+      *a.status = bad ? -1 : static_cast<int32_t>(min(missing, int64_t{0x7fffffff}));
+    }
+    return;
+  }
+  if (total[1] > 0) {
+    for (int32_t b = wave; b < a.requests; b += kPlanWaves) {
+      if (!a.reset[b]) continue;
+      const int64_t n = pages_of(a, a.tokens[b]);
+      int32_t* to = a.free_pages + nf + a.lens[b];
+      for (int64_t p = lane; p < n; p += 64) to[p] = a.table[static_cast<int64_t>(b) * a.width + p];
+    }
+    __syncthreads();
+  }
+  int64_t row = pre[0], taken = pre[2];
+  for (int32_t b = b0; b < b1; ++b) {
+    const Need d = need_of(a, b);
+    a.cu[b] = static_cast<int32_t>(row);
+    a.lens[b] = static_cast<int32_t>(d.held + d.n);
+    for (int64_t p = d.had; p < d.want; ++p)
+      a.table[static_cast<int64_t>(b) * a.width + p] = a.free_pages[top - 1 - taken++];
+    row += d.n;
+  }
+  if (threadIdx.x == 0) {
+    a.cu[a.requests] = static_cast<int32_t>(total[0]);
+    *a.n_free_after = static_cast<int32_t>(top - total[2]);
+    *a.status = 0;
+  }
+}
+
+__global__ void __launch_bounds__(kRowThreads) hlwq_kv_plan_rows_kernel(const PlanArgs a) {
+  const int64_t i64 = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
+  if (i64 >= a.rows) return;
+  const int32_t i = static_cast<int32_t>(i64);
+  int32_t req = -1, pos = -1, slot = -1;
+  if (i < a.cu[a.requests]) {
+    // the last request that begins at or before row i (empty ones begin where
+    // the next one does, so the last is the one that owns it)
+    int32_t lo = 0, hi = a.requests - 1;
+    while (lo < hi) {
+      const int32_t mid = (lo + hi + 1) >> 1;
+      if (a.cu[mid] <= i)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    req = lo;
+    pos = a.lens[lo] - (a.cu[lo + 1] - i);
+    const int64_t old = pos - a.n_res;
+    if (old >= 0) {
+      const int32_t id = a.table[static_cast<int64_t>(lo) * a.width + (old >> a.page_shift)];
+      if (id >= 0 && id < a.n_pages)
+        slot = static_cast<int32_t>((static_cast<int64_t>(id) << a.page_shift) + (old & ((1 << a.page_shift) - 1)));
+    }
+  }
+  a.row_request[i] = req;
+  a.positions[i] = pos;
+  a.slots[i] = slot;
+}
+
+// ---------------------------------------------------------------------------
+// Append.  One wave takes one head vector of one row, K or V: it encodes the
+// token that the row pushes out of the window (from the ring, or from the
+// step's own row n_residual before it) into its slot, and puts a new token
+// that stays into the ring.  A ring slot that is read and rewritten in the
+// same call has one wave do both, in that order, so no wave waits for another.
+// ---------------------------------------------------------------------------
+
+struct AppendArgs {
+  const uint16_t* src[2];
+  int64_t stride[2];
+  uint8_t* packed[2];
+  uint16_t* norms[2];
+  uint16_t* window[2];
+  const int32_t* cu;
+  const int32_t* lens;
+  const int32_t* row_request;
+  const int32_t* slots;
+  int64_t n_slots;  // n_pages * page_size
+  int32_t requests, rows, heads, page_shift;
+  int64_t n_res, ring;
+};
+
+__device__ __forceinline__ int64_t floor_mod(int64_t a, int64_t m) {
+  const int64_t r = a % m;
+  return r < 0 ? r + m : r;
+}
+
+// Codes and norm of the vector whose values 4 lane .. 4 lane + 3 are in w, to
+// packed[vec] and norms[vec].
+template <int BITS>
+__device__ __forceinline__ void encode_wave(uint2 w, uint8_t* packed, uint16_t* norms, int64_t vec, int lane) {
+  constexpr int K = 1 << BITS;
+  constexpr float thr3[7] = HLWQ_THRESHOLDS_3;
+  constexpr float thr2[3] = HLWQ_THRESHOLDS_2;
+  float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+  float s = __builtin_fmaf(x[0], x[0], x[1] * x[1]) + __builtin_fmaf(x[2], x[2], x[3] * x[3]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s = s + lane_xor(s, d);
+  const float n = sqrtf(s);
+  const float r = n >= FLT_MIN ? 1.0f / n : 0.0f;
+  wave_fwht(x, lane);
+  uint32_t f = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float y = x[j] * r;
+    uint32_t c = 0;
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) c += (y > (BITS == 3 ? thr3[k] : thr2[k])) ? 1u : 0u;
+    f |= c << (BITS * j);
+  }
+  uint8_t* dst = packed + vec * (32 * BITS);
+  if constexpr (BITS == 2) {
+    dst[lane] = static_cast<uint8_t>(f);
+  } else {
+    // 8 lanes hold 32 codes = 96 bits = 3 words
+    const int i = lane & 7, bit = 12 * i;
+    const uint64_t v = static_cast<uint64_t>(f) << (bit & 31);
+    uint32_t wd[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      wd[k] = ((bit >> 5) == k ? static_cast<uint32_t>(v) : 0u) | ((bit >> 5) + 1 == k ? static_cast<uint32_t>(v >> 32) : 0u);
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) wd[k] |= lane_xor(wd[k], d);
+    if (i == 0) {
+      uint32_t* out = reinterpret_cast<uint32_t*>(dst + 12 * (lane >> 3));
+      out[0] = wd[0];
+      out[1] = wd[1];
+      out[2] = wd[2];
+    }
+  }
+  if (lane == 0) norms[vec] = f16_bits(n);
+}
+
+constexpr int kAppendThreads = 256;
+
+template <int BITS>
+__global__ void __launch_bounds__(kAppendThreads) hlwq_kv_paged_append_kernel(const AppendArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int side = blockIdx.y;
+  const int64_t row64 = unit / a.heads;
+  if (row64 >= a.rows) return;
+  const int32_t row = static_cast<int32_t>(row64), head = static_cast<int32_t>(unit - row64 * a.heads);
+  const int32_t b = a.row_request[row];
+  if (b < 0 || b >= a.requests) return;
+  const RowRange rr = row_range(a.cu, b, a.rows);
+  if (row < rr.begin || row >= rr.end) return;
+  const int64_t n = rr.end - rr.begin;
+  const int64_t total = max(static_cast<int64_t>(a.lens[b]), n), held = total - n;
+  const int64_t t = held + (row - rr.begin), old = t - a.n_res;
+  const uint16_t* src = a.src[side] + head * kDim + 4 * lane;
+  uint16_t* ring = a.window[side] + (static_cast<int64_t>(b) * a.heads + head) * a.ring * kDim + 4 * lane;
+  const int64_t stay = max(held, total - a.n_res);  // first new token that stays in the window
+
+  if (old >= 0) {
+    const bool ringed = old < held;
+    const int64_t slot = a.slots[row];
+    if (slot >= 0 && slot < a.n_slots) {
+      const uint16_t* p = ringed ? ring + old % a.ring * kDim : src + (row - a.n_res) * a.stride[side];
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      const int64_t vec = (((slot >> a.page_shift) * a.heads + head) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
+      encode_wave<BITS>(w, a.packed[side], a.norms[side], vec, lane);
+    }
+    if (ringed) {
+      // the token that stays in the slot just read, if one does
+      const int64_t t2 = stay + floor_mod(old - stay, a.ring);
+      if (t2 < total) {
+        const uint2 v = *reinterpret_cast<const uint2*>(src + (rr.begin + (t2 - held)) * a.stride[side]);
+        *reinterpret_cast<uint2*>(ring + old % a.ring * kDim) = v;
+      }
+    }
+  }
+  if (t >= stay) {
+    // its slot's last token before the step; if that one leaves the window
+    // now, the row that encodes it writes this one
+    const int64_t u = held - 1 - floor_mod(held - 1 - t, a.ring);
+    const bool other = u >= 0 && u >= held - a.n_res && u < total - a.n_res;
+    if (!other) {
+      const uint2 v = *reinterpret_cast<const uint2*>(src + row * a.stride[side]);
+      *reinterpret_cast<uint2*>(ring + t % a.ring * kDim) = v;
+    }
+  }
+}
+
+int run_plan(const hlwq_kv_plan* p, hipStream_t stream) {
+  if (!p) return HLWQ_ERR_NULL;
+  if (p->requests < 0 || p->rows < 0 || p->max_pages < 0 || p->n_pages < 0 || p->n_residual < 0) return HLWQ_ERR_SHAPE;
+  if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1))) return HLWQ_ERR_SHAPE;
+  if (p->requests > kMaxRequests || p->max_pages > kMaxTable || p->rows > 0x7fffffff ||
+      p->n_pages > 0x7fffffff / p->page_size)
+    return HLWQ_ERR_LIMIT;
+  const int64_t table = p->requests * p->max_pages;
+  if (!p->n_free || !p->cu_new || !p->n_free_after || !p->status ||
+      (p->requests > 0 && (!p->tokens || !p->n_new || !p->lens)) ||
+      (p->rows > 0 && (!p->row_request || !p->positions || !p->slots)) || (p->n_pages > 0 && !p->free_pages) ||
+      (table > 0 && !p->block_table))
+    return HLWQ_ERR_NULL;
+  std::vector<Span> spans;
+  const struct {
+    const void* p;
+    int64_t count;
+    bool written;
+  } words[] = {{p->tokens, p->requests, false},      {p->n_new, p->requests, false},  {p->n_free, 1, false},
+               {p->free_pages, p->n_pages, true},    {p->block_table, table, true},   {p->cu_new, p->requests + 1, true},
+               {p->lens, p->requests, true},         {p->row_request, p->rows, true}, {p->positions, p->rows, true},
+               {p->slots, p->rows, true},            {p->n_free_after, 1, true},      {p->status, 1, true}};
+  for (const auto& w : words) {
+    if (misaligned(w.p, 4)) return HLWQ_ERR_ALIGN;
+    add_span(spans, w.p, w.count, 4, w.written);
+  }
+  add_span(spans, p->reset, p->requests, 1, false);
+  if (check_disjoint(spans) != HLWQ_OK) return HLWQ_ERR_OVERLAP;
+  PlanArgs a;
+  a.tokens = p->tokens;
+  a.n_new = p->n_new;
+  a.reset = p->reset;
+  a.n_free = p->n_free;
+  a.free_pages = p->free_pages;
+  a.table = p->block_table;
+  a.cu = p->cu_new;
+  a.lens = p->lens;
+  a.row_request = p->row_request;
+  a.positions = p->positions;
+  a.slots = p->slots;
+  a.n_free_after = p->n_free_after;
+  a.status = p->status;
+  a.requests = static_cast<int32_t>(p->requests);
+  a.rows = static_cast<int32_t>(p->rows);
+  a.width = static_cast<int32_t>(p->max_pages);
+  a.n_pages = static_cast<int32_t>(p->n_pages);
+  a.page_shift = __builtin_ctzll(static_cast<uint64_t>(p->page_size));
+  a.n_res = p->n_residual;
+  const int st = launch(hlwq_kv_plan_tables_kernel, dim3(1), dim3(kPlanThreads), stream, a);
+  if (st != HLWQ_OK || p->rows == 0) return st;
+  return launch(hlwq_kv_plan_rows_kernel, dim3(static_cast<uint32_t>(ceil_div(p->rows, kRowThreads))), dim3(kRowThreads),
+                stream, a);
+}
+
+int run_append(const hlwq_kv_cache* c, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+               const int32_t* cu, const int32_t* lens, const int32_t* row_request, const int32_t* slots, int64_t rows,
+               hipStream_t stream) {
+  if (!c) return HLWQ_ERR_NULL;
+  std::vector<Span> spans;
+  int st = check_cache(*c, true, spans);
+  if (st != HLWQ_OK) return st;
+  if (rows < 0) return HLWQ_ERR_SHAPE;
+  if (rows == 0 || c->requests == 0 || c->kv_heads == 0) return HLWQ_OK;
+  int64_t units;
+  if (rows > 0x7fffffff || !mul_ok(rows, c->kv_heads, &units) || ceil_div(units, kAppendThreads / 64) > 0x7fffff)
+    return HLWQ_ERR_LIMIT;
+  int64_t ke, ve;
+  if ((st = check_rows(k, k_stride, rows, c->kv_heads, &ke)) != HLWQ_OK ||
+      (st = check_rows(v, v_stride, rows, c->kv_heads, &ve)) != HLWQ_OK)
+    return st;
+  if (!cu || !lens || !row_request || !slots) return HLWQ_ERR_NULL;
+  if (misaligned(cu, 4) || misaligned(lens, 4) || misaligned(row_request, 4) || misaligned(slots, 4)) return HLWQ_ERR_ALIGN;
+  add_span(spans, k, ke, 2, false);
+  add_span(spans, v, ve, 2, false);
+  add_span(spans, cu, c->requests + 1, 4, false);
+  add_span(spans, lens, c->requests, 4, false);
+  add_span(spans, row_request, rows, 4, false);
+  add_span(spans, slots, rows, 4, false);
+  if (check_disjoint(spans) != HLWQ_OK) return HLWQ_ERR_OVERLAP;
+  AppendArgs a;
+  const hlwq_kv_store* s[2] = {&c->k, &c->v};
+  const void* src[2] = {k, v};
+  const int64_t stride[2] = {k_stride, v_stride};
+  for (int i = 0; i < 2; ++i) {
+    a.src[i] = static_cast<const uint16_t*>(src[i]);
+    a.stride[i] = stride[i];
+    a.packed[i] = static_cast<uint8_t*>(s[i]->packed);
+    a.norms[i] = static_cast<uint16_t*>(s[i]->norms);
+    a.window[i] = static_cast<uint16_t*>(s[i]->window);
+  }
+  a.cu = cu;
+  a.lens = lens;
+  a.row_request = row_request;
+  a.slots = slots;
+  a.n_slots = c->n_pages * c->page_size;
+  a.requests = static_cast<int32_t>(c->requests);
+  a.rows = static_cast<int32_t>(rows);
+  a.heads = static_cast<int32_t>(c->kv_heads);
+  a.page_shift = __builtin_ctzll(static_cast<uint64_t>(c->page_size));
+  a.n_res = c->n_residual;
+  a.ring = c->ring;
+  const dim3 grid(static_cast<uint32_t>(ceil_div(units, kAppendThreads / 64)), 2);
+  return launch(c->bits == 3 ? hlwq_kv_paged_append_kernel<3> : hlwq_kv_paged_append_kernel<2>, grid, dim3(kAppendThreads),
+                stream, a);
+}
+
+}  // namespace
+}  // namespace hlwq_kv
+
+extern "C" {
+
+int hlwq_kv_page_plan(const hlwq_kv_plan* plan, void* hip_stream) {
+  return hlwq_kv::run_plan(plan, static_cast<hipStream_t>(hip_stream));
+}
+
+int hlwq_kv_paged_append(const hlwq_kv_cache* cache, const void* k_new_bf16, int64_t k_stride, const void* v_new_bf16,
+                         int64_t v_stride, const int32_t* cu_new, const int32_t* lens, const int32_t* row_request,
+                         const int32_t* slots, int64_t rows, void* hip_stream) {
+  return hlwq_kv::run_append(cache, k_new_bf16, k_stride, v_new_bf16, v_stride, cu_new, lens, row_request, slots, rows,
+                             static_cast<hipStream_t>(hip_stream));
+}
+
+}  // extern "C"
