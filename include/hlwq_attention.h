@@ -117,7 +117,7 @@ int hlwq_kv_page_plan(const hlwq_kv_plan* plan, void* hip_stream);
 
 /* Put the step's keys and values k_new, v_new (bf16 [rows][kv_heads][256],
  * consecutive rows k_stride / v_stride elements apart: a multiple of 8, at
- * least 256 * kv_heads) into the cache: row i, at position t of its request,
+ * least 256 * kv_heads, at most 2^22) into the cache: row i, at position t of its request,
  * pushes out token t - n_residual, whose codes and norm go to slots[i]; the new
  * tokens that stay among the newest n_residual go to their ring slots.
  * cu_new, lens, row_request and slots as hlwq_kv_page_plan wrote them.  Rows

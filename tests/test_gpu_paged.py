@@ -512,9 +512,9 @@ def test_a_serving_loop(wq, bits, page, residual, ring):
         torch.cuda.synchronize()
         assert p.status.item() == 0
         got, cu = out.cpu().double().numpy(), np.concatenate([[0], np.cumsum(new)])
+        whole = None
         if step == 0:  # nothing cached: the same as whole prompts
-            whole = wq.hlwq_prompt_attention(dev16(q), dev16(k), dev16(v), p.cu_new)
-            assert torch.allclose(whole[:cu[-1]].float(), out[:cu[-1]].float(), rtol=2 ** -7, atol=2 ** -9)
+            whole = wq.hlwq_prompt_attention(dev16(q), dev16(k), dev16(v), p.cu_new).cpu().double().numpy()
         for b in range(slots):
             if reset[b]:
                 history[b] = [[], []]
@@ -531,6 +531,8 @@ def test_a_serving_loop(wq, bits, page, residual, ring):
                 history[b][i].extend(x[r])
             if new[b]:
                 pr.check_attention(got[r], f64(q[r]), *both, enc, held, hk)
+                if whole is not None:
+                    pr.check_attention(whole[r], f64(q[r]), *both, enc, held, hk)
         s.tokens, s.n_free = p.lens, p.n_free
     assert s.tokens.tolist() == [len(h[0]) for h in history]
 

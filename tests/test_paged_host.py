@@ -83,7 +83,7 @@ def test_append_argument_errors(lib):
     assert append(lib, c, slots=None) == ENULL
     assert append(lib, c, ks=1016) == ESHAPE
     assert append(lib, c, vs=1028) == ESHAPE
-    assert append(lib, c, ks=2 ** 62) == ESHAPE
+    assert append(lib, c, ks=2 ** 22 + 8) == ELIMIT
     assert append(lib, c, rows=-1) == ESHAPE
     assert append(lib, c, rows=2 ** 31) == ELIMIT
     assert append(lib, c, k=at(6) + 8) == EALIGN

@@ -1,7 +1,7 @@
 // attention.hip — attention over the paged cache of HLWQ codes and over whole
 // prompts (include/hlwq_attention.h).
 
-#include "kv_common.h"
+#include "attention_tile.h"
 
 #include <cmath>
 
@@ -9,27 +9,6 @@ namespace hlwq_kv {
 namespace {
 
 constexpr int kThreads = 256;
-
-struct AttnArgs {
-  const uint16_t* q;
-  int64_t q_stride;
-  const uint16_t* k_new;
-  const uint16_t* v_new;
-  int64_t k_stride, v_stride;
-  const uint8_t* k_packed;
-  const uint8_t* v_packed;
-  const uint16_t* k_norms;
-  const uint16_t* v_norms;
-  const uint16_t* k_window;
-  const uint16_t* v_window;
-  const int32_t* cu;
-  const int32_t* lens;   // null: nothing is cached
-  const int32_t* table;
-  uint16_t* out;
-  int64_t n_res, ring, width;
-  int32_t requests, rows, q_heads, kv_heads, n_pages, page_shift;
-  float scale;
-};
 
 __device__ __forceinline__ float wave_sum(float s) {
 #pragma unroll
@@ -183,6 +162,21 @@ int launch_attention(int bits, const AttnArgs& a, hipStream_t stream) {
                 dim3(static_cast<uint32_t>(groups)), dim3(kThreads), stream, a);
 }
 
+// Workgroups of a prompt call with `tile` rows to each: at most one tile more
+// per sequence than whole ones.
+int64_t prompt_groups(const AttnArgs& a, int64_t tile) {
+  const int64_t rows = static_cast<int64_t>(a.rows) * a.group;
+  return std::min(rows / tile + a.requests, rows) * a.kv_heads;
+}
+
+int launch_prompt(const AttnArgs& a, hipStream_t stream) {
+  const bool wide = prompt_groups(a, 256) >= 512;
+  const int64_t groups = prompt_groups(a, wide ? 256 : 128);
+  if (groups > 0x7fffff) return HLWQ_ERR_LIMIT;
+  return launch(wide ? hlwq_prompt_attention_kernel<8, 64> : hlwq_prompt_attention_kernel<4, 32>,
+                dim3(static_cast<uint32_t>(groups)), dim3(wide ? 512 : 256), stream, a);
+}
+
 size_t workspace_bytes_of(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
   bool nothing;
   if (requests <= 0 || requests > kMaxRequests || check_heads(rows, q_heads, kv_heads, &nothing) != HLWQ_OK || nothing) return 0;
@@ -287,8 +281,9 @@ int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
   a.rows = static_cast<int32_t>(rows);
   a.q_heads = static_cast<int32_t>(q_heads);
   a.kv_heads = static_cast<int32_t>(kv_heads);
+  a.group = static_cast<int32_t>(q_heads / kv_heads);
   a.scale = scale;
-  return launch_attention(0, a, stream);
+  return launch_prompt(a, stream);
 }
 
 }  // namespace

@@ -1,0 +1,199 @@
+// attention_common.h — what the attention kernels share: arguments, the
+// requests' extents, the matrix-core fragments and the unpacking of codes.
+//
+// Every kernel computes S^T = K Q^T and O^T = V^T P^T, so that a query row is
+// a column of both results: its softmax statistics are one register of the
+// lanes that hold the column, the probabilities come out of the first product
+// in the layout that the second takes them in (up to an order of the keys,
+// which V's operand follows), and nothing is exchanged across lanes but the
+// row maximum.
+#pragma once
+
+#include "kv_common.h"
+
+namespace hlwq_kv {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+typedef __attribute__((address_space(3))) float lds_f32;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+// A row's running maximum is raised, and its sums rescaled, only once a score
+// passes it by this much (in powers of two): probabilities then reach 2^8,
+// far inside the range of bf16, fp16 and fp32, and the rescale of 256 sums is
+// paid a few times per row instead of once per tile.
+constexpr float kLazy = 8.0f;
+
+struct AttnArgs {
+  const uint16_t* q;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  int64_t q_stride, k_stride, v_stride;
+  const uint8_t* k_packed;
+  const uint8_t* v_packed;
+  const uint16_t* k_norms;
+  const uint16_t* v_norms;
+  const uint16_t* k_window;
+  const uint16_t* v_window;
+  const int32_t* cu;
+  const int32_t* lens;  // null: nothing is cached
+  const int32_t* table;
+  uint16_t* out;
+  float* partial;  // workspace: partial sums, then their statistics
+  int64_t n_res, ring;
+  int32_t requests, rows, q_heads, kv_heads, group, n_pages, page_shift, width;
+  int32_t workers;  // workgroups that share the work
+  int32_t least, most;  // requests with rows * group in [least, most] are this kernel's
+  float scale;
+};
+
+// One request's part of a step.
+struct Extent {
+  int32_t begin, n;   // rows
+  int64_t held, enc;  // tokens before the step, those of them encoded
+  int64_t paged;      // encoded tokens that have a table entry
+};
+__device__ __forceinline__ Extent extent_of(const AttnArgs& a, int32_t b) {
+  Extent e;
+  const RowRange r = row_range(a.cu, b, a.rows);
+  e.begin = r.begin;
+  e.n = r.end - r.begin;
+  e.held = a.lens ? max(static_cast<int64_t>(a.lens[b]) - e.n, int64_t{0}) : 0;
+  e.enc = a.lens ? max(e.held - a.n_res, int64_t{0}) : 0;
+  e.paged = a.n_pages > 0 ? min(e.enc, static_cast<int64_t>(a.width) << a.page_shift) : 0;
+  return e;
+}
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Value of lane l ^ 32.
+__device__ __forceinline__ float half_swap(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// Two floats rounded to a pair of fp16, to nearest.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const f16x2 v = {static_cast<_Float16>(lo), static_cast<_Float16>(hi)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// The pair of bf16 with infinities and NaN replaced by zero; `any` gets a bit
+// set if there was one.  (Adding one to an exponent of all ones carries into
+// the sign's place.)
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w, uint32_t& any) {
+  const uint32_t m = ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+  any |= m;
+  return w & ~(m | (m - (m >> 15)));
+}
+
+// ---------------------------------------------------------------------------
+// Codes to centroids.  The centroids enter the products as fp16; their bytes
+// are looked up by v_perm_b32, which picks each byte of its result from eight
+// bytes in two registers: one permute gives the high bytes of four centroids,
+// one the low bytes, and two more interleave them to four fp16.
+// ---------------------------------------------------------------------------
+
+constexpr uint16_t f16_of(float f) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f)); }
+template <int BITS>
+struct Book {
+  static constexpr float c3[8] = HLWQ_CENTROIDS_3;
+  static constexpr float c2[4] = HLWQ_CENTROIDS_2;
+  static constexpr uint32_t word(int first, int shift) {
+    uint32_t w = 0;
+    for (int i = 0; i < 4; ++i) {
+      const uint16_t h = BITS == 3 ? f16_of(c3[(first + i) & 7]) : f16_of(c2[i]);
+      w |= static_cast<uint32_t>((h >> shift) & 0xff) << (8 * i);
+    }
+    return w;
+  }
+  static constexpr uint32_t hi0 = word(0, 8), hi1 = word(4, 8), lo0 = word(0, 0), lo1 = word(4, 0);
+};
+
+// Four codes, one a byte, to four fp16 centroids.
+template <int BITS>
+__device__ __forceinline__ u32x2 look_up(uint32_t c) {
+  const uint32_t hi = __builtin_amdgcn_perm(Book<BITS>::hi1, Book<BITS>::hi0, c);
+  const uint32_t lo = __builtin_amdgcn_perm(Book<BITS>::lo1, Book<BITS>::lo0, c);
+  return u32x2{__builtin_amdgcn_perm(hi, lo, 0x05010400u), __builtin_amdgcn_perm(hi, lo, 0x07030602u)};
+}
+
+// ---------------------------------------------------------------------------
+// Finding work.  The requests' lengths are on the device, so every workgroup
+// sums what the requests ask for and finds its own share of it.
+// ---------------------------------------------------------------------------
+
+// The prefix sum of a quantity over the requests: thread i of NT holds the sum
+// `own` of requests [b0, b1) and the sum `pre` of all before them.
+struct Prefix {
+  int64_t own, pre, total;
+  int32_t b0, b1;
+};
+template <int NT, class F>
+__device__ __forceinline__ Prefix prefix_of(int32_t requests, F of, int64_t* lds) {
+  Prefix p;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t per = (requests + NT - 1) / NT;
+  p.b0 = min(static_cast<int32_t>(threadIdx.x) * per, requests);
+  p.b1 = min(p.b0 + per, requests);
+  p.own = 0;
+  for (int32_t b = p.b0; b < p.b1; ++b) p.own += of(b);
+  int64_t v = p.own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t u = __shfl_up(v, d, 64);
+    if (lane >= d) v += u;
+  }
+  if (lane == 63) lds[wave] = v;
+  __syncthreads();
+  p.pre = v - p.own;
+  p.total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) {
+    if (w < wave) p.pre += lds[w];
+    p.total += lds[w];
+  }
+  __syncthreads();
+  return p;
+}
+
+// The request that holds unit x of the quantity, and x's place in it; -1 if
+// there is none.  lds: 2 words.
+struct Found {
+  int32_t b;
+  int64_t rest;
+};
+template <class F>
+__device__ __forceinline__ Found find(const Prefix& p, int64_t x, F of, int64_t* lds) {
+  if (threadIdx.x == 0) lds[0] = -1;
+  __syncthreads();
+  if (x >= p.pre && x < p.pre + p.own) {
+    int64_t at = p.pre;
+    for (int32_t b = p.b0; b < p.b1; ++b) {
+      const int64_t n = of(b);
+      if (x < at + n) {
+        lds[0] = b;
+        lds[1] = x - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  Found f;
+  f.b = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(lds[0]));
+  const int64_t rest = lds[1];
+  f.rest = static_cast<int64_t>((static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(rest) >> 32))) << 32) |
+                                static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(rest))));
+  __syncthreads();
+  return f;
+}
+
+}  // namespace hlwq_kv

@@ -1,0 +1,360 @@
+// attention_tile.h — the matrix-core attention for many query rows: a
+// workgroup takes 32 rows a wave and streams keys and values through LDS.
+//
+// A row is a (token, query head) pair of one KV head, row r of a request being
+// token r / group, head r % group, so that grouped heads fill the same tile and
+// share every key and value that is read.  Per 32 keys and wave: 16 products of
+// 32x32x16 for S^T, the softmax of 16 scores a lane, 16 products for O^T.  The
+// sums O^T stay in 128 registers, Q in 64.
+//
+// What bounds it: per 32 keys a wave's products take 1024 cycles of its SIMD's
+// matrix core and it reads 32 KB from LDS, two waves a SIMD share both.  With
+// eight waves to a workgroup the CU reads 256 KB in 2048 matrix cycles, half
+// of what LDS gives (K as b128, V transposed on the way by ds_read_tr16);
+// softmax and address arithmetic (about 500 cycles a wave) run beside the
+// other wave's products.
+#pragma once
+
+#include "attention_common.h"
+
+namespace hlwq_kv {
+
+// A buffer resource over `bytes` bytes at p (uniform): reads past them give 0.
+__device__ __forceinline__ u32x4 buffer_of(const void* p, int64_t bytes) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  return u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u))),
+               static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32) & 0xffffu)),
+               static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(bytes, int64_t{0x7fffffff})))),
+               0x00020000u};
+}
+
+// 16 bytes a lane from memory straight to LDS: lane l's land at lds + 16 l.
+// The compiler does not see these loads; a wait on the vector-memory counter
+// stands before the barrier that publishes them (wait_staged).  M0, which
+// holds the LDS address, is used by nothing else in these kernels.
+__device__ __forceinline__ void stage16(u32x4 buffer, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer)
+               : "memory");
+}
+__device__ __forceinline__ void stage16(const void* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+__device__ __forceinline__ void wait_staged() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// LDS tile of keys (or values): key k's 256 values in 32 chunks of 16 bytes at
+// 512 k, chunk c in place c ^ swizzle(k).  Sixteen lanes that read the same
+// chunk of sixteen keys then hit different banks, and so do the four keys by
+// 64 bytes of a transposed read of V.
+__device__ __forceinline__ int swizzle(int key) { return ((key & 3) << 2) | ((key >> 2) & 3); }
+
+// One wave's 32 rows.
+struct Rows {
+  f32x16 o[8];  // o[t][i]: value 32 t + 8 (i / 4) + 4 (lane / 32) + i % 4 of row lane % 32
+  float m, l;   // running maximum (of scores times log2 e) and this lane's share of the sum
+  uint32_t left;  // nonzero: infinite or NaN values were left out of the sums
+};
+
+__device__ __forceinline__ void clear(Rows& r) {
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r.o[t][i] = 0;
+}
+
+__device__ __forceinline__ void scale_rows(Rows& r, float f) {
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r.o[t][i] *= f;
+}
+
+template <bool ENC>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (ENC)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Lane constants of the LDS reads.
+struct TileLane {
+  uint32_t k;  // chunk 0 (or 1, upper half) of key lane % 32
+  uint32_t v;  // transposed read of value block 0, keys 0 .. 3 (4 .. 7, upper half)
+};
+__device__ __forceinline__ TileLane tile_lane(int lane) {
+  const int col = lane & 31, h = lane >> 5, l16 = lane & 15, g2 = (lane >> 4) & 1;
+  TileLane t;
+  t.k = col * 512 + ((h ^ swizzle(col)) * 16);
+  t.v = (4 * h + (l16 >> 2)) * 512 + ((((2 * g2 + ((l16 >> 1) & 1)) ^ h) + ((l16 >> 2) << 2)) * 16) + 8 * (l16 & 1);
+  return t;
+}
+
+// Fragment x = 2 t + s of V^T for O^T's rows 32 t .. and keys 16 s .. of the 32
+// at `v`: ds_read_tr16_b64 gives lane i of sixteen the element i % 4 of the
+// four lanes i / 4 + 4 j, so with lane r pointing at key r / 4, values 4 (r %
+// 4) .. the lane gets value i of four keys.
+__device__ __forceinline__ u32x4 v_fragment(uint32_t v, int x) {
+  const int t = x >> 1, s = x & 1;
+  const uint32_t ad = (v ^ ((t & 3) << 6)) + (t >> 2) * 256 + s * 8192;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)static_cast<uintptr_t>(ad));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)static_cast<uintptr_t>((ad ^ 32) + 4096));
+  return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// One step of 32 keys whose K and V lie in LDS at k and v (lane addresses), for
+// rows that see keys 0 .. lim of them.
+//   ENC: centroids in fp16; kn, vn: LDS addresses of the 32 keys' norms (kn < 0
+//   where a key is not there; vn over the tile's scale), masked: some key is
+//   not.
+//   otherwise bf16, masked: some row does not see some key.
+// factor turns a product into a score times log2 e.
+template <bool ENC>
+__device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t k, uint32_t v, float factor,
+                                         int lim, bool masked, uint32_t kn, uint32_t vn, int lane) {
+  constexpr int PK = 3, PV = 2;  // fragments in flight: what fits the registers beside the sums
+  const int h = lane >> 5;
+  f32x16 s;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = 0;
+  u32x4 kf[PK];
+  const auto k_read = [&](int x) {
+    kf[x % PK] = *reinterpret_cast<const lds_u32x4*>(static_cast<uintptr_t>((k ^ ((x & 7) * 32)) + (x >> 3) * 256));
+  };
+#pragma unroll
+  for (int x = 0; x < PK; ++x) k_read(x);
+  __builtin_amdgcn_sched_group_barrier(0x100, PK, 0);
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    s = mfma32<ENC>(kf[x % PK], q[x], s);
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    if (x + PK < 16) {
+      k_read(x + PK);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+  }
+  u32x4 vf[PV];
+  if constexpr (ENC) {
+#pragma unroll
+    for (int x = 0; x < PV; ++x) vf[x] = v_fragment(v, x);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * PV, 0);
+  }
+  // score i of a lane is key 8 (i / 4) + 4 h + i % 4
+  if constexpr (ENC) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 n = *reinterpret_cast<const lds_f32x4*>(static_cast<uintptr_t>(kn + 32 * i + 16 * h));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[4 * i + j] *= n[j];
+        if (masked) s[4 * i + j] = n[j] < 0 ? -FLT_MAX : s[4 * i + j];
+      }
+    }
+  } else if (masked) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + 4 * h + i % 4 > lim ? -FLT_MAX : s[i];
+  }
+  float mx = s[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+  mx = fmaxf(mx, half_swap(mx)) * factor;
+  if (__any(mx - r.m > kLazy)) {
+    const float mn = fmaxf(r.m, mx);
+    const float f = fast_exp2(r.m - mn);
+    r.m = mn;
+    r.l *= f;
+    scale_rows(r, f);
+  }
+  float p[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) p[i] = fast_exp2(__builtin_fmaf(s[i], factor, -r.m));
+  if constexpr (!ENC) {
+    // a score of -FLT_MAX is no 0 where the factor is 0 or the maximum too
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[i] = 8 * (i / 4) + 4 * h + i % 4 > lim ? 0.0f : p[i];
+    }
+  }
+  if constexpr (ENC) {
+    u32x4 pf[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (masked) {
+        const f32x4 n = *reinterpret_cast<const lds_f32x4*>(static_cast<uintptr_t>(kn + 32 * i + 16 * h));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[4 * i + j] = n[j] < 0 ? 0.0f : p[4 * i + j];
+      }
+      const f32x4 n = *reinterpret_cast<const lds_f32x4*>(static_cast<uintptr_t>(vn + 32 * i + 16 * h));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.l += p[4 * i + j];
+      pf[i >> 1][2 * (i & 1)] = pack_f16x2(p[4 * i] * n[0], p[4 * i + 1] * n[1]);
+      pf[i >> 1][2 * (i & 1) + 1] = pack_f16x2(p[4 * i + 2] * n[2], p[4 * i + 3] * n[3]);
+    }
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      r.o[x >> 1] = mfma32<true>(vf[x % PV], pf[x & 1], r.o[x >> 1]);
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 1);
+      if (x + PV < 16) {
+        vf[x % PV] = v_fragment(v, x + PV);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
+      }
+    }
+  } else {
+    u32x4 pf[2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r.l += p[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pf[i >> 2][i & 3] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+#pragma unroll
+    for (int x = 0; x < PV; ++x) vf[x] = v_fragment(v, x);
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      u32x4 f = vf[x % PV];
+      if (x + PV < 16) vf[x % PV] = v_fragment(v, x + PV);
+      // a masked key's value times its probability 0 is NaN where the value is
+      // infinite or NaN: in these steps such values are left out, and added at
+      // the end to the rows that see them (add_nonfinite)
+      if (masked) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = finite_pair(f[j], r.left);
+      }
+      r.o[x >> 1] = mfma32<false>(f, pf[x & 1], r.o[x >> 1]);
+    }
+  }
+}
+
+// The infinite and NaN values that the masked steps left out, of keys [from,
+// to]: added to the row if it sees their key (key <= lim).  value(key): the
+// key's 256 values in memory.
+template <class F>
+__device__ __forceinline__ void add_nonfinite(Rows& r, int from, int to, int lim, int h, F value) {
+  if (!__any(r.left != 0)) return;
+  for (int key = from; key <= to; ++key) {
+    const uint16_t* p = value(key);
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p + 32 * t + 8 * i + 4 * h);
+        const float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.o[t][4 * i + j] += key <= lim && !__builtin_isfinite(x[j]) ? x[j] : 0.0f;
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Whole prompts.  A workgroup takes one tile of one KV head's rows, the tiles
+// of a sequence from its end on (a causal tile costs as many keys as its last
+// token has before it, so the long ones start first), consecutive workgroups
+// on different KV heads, so that an XCD's L2 serves as few heads as there are.
+// ---------------------------------------------------------------------------
+
+template <int NW, int KT>
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) hlwq_prompt_attention_kernel(const AttnArgs a) {
+  constexpr int kRows = 32 * NW;
+  constexpr uint32_t kStage = KT * 1024;  // K and V of one stage
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, h = lane >> 5;
+  const int head = blockIdx.x % a.kv_heads;
+  const int g = a.group;
+
+  const auto tiles = [&](int32_t b) {
+    const RowRange r = row_range(a.cu, b, a.rows);
+    return ceil_div(static_cast<int64_t>(r.end - r.begin) * g, kRows);
+  };
+  int64_t* scratch = reinterpret_cast<int64_t*>(lds);
+  const Prefix pre = prefix_of<64 * NW>(a.requests, tiles, scratch);
+  const Found f = find(pre, blockIdx.x / a.kv_heads, tiles, scratch);
+  if (f.b < 0) return;
+  const RowRange rr = row_range(a.cu, f.b, a.rows);
+  const int32_t n = rr.end - rr.begin;
+  const int64_t rows = static_cast<int64_t>(n) * g;
+  const int64_t r0 = (tiles(f.b) - 1 - f.rest) * kRows;  // the tile's first row
+  const int64_t w0 = r0 + 32 * wave;                      // the wave's
+  // tokens of the lane's row, of the wave's first and last, of the tile's last
+  const int64_t row = min(w0 + col, rows - 1);
+  const int32_t tok = static_cast<int32_t>(row / g);
+  const auto q_head = [&]() { return head * static_cast<int64_t>(g) + (min(w0 + col, rows - 1) - static_cast<int64_t>(tok) * g); };
+  const int32_t first = static_cast<int32_t>(min(w0, rows - 1) / g), last = w0 < rows ? static_cast<int32_t>(min(w0 + 31, rows - 1) / g) : -1;
+  const int32_t end = static_cast<int32_t>(min(r0 + kRows - 1, rows - 1) / g) + 1;
+
+  u32x4 q[16];
+  {
+    const uint16_t* qp = a.q + (rr.begin + static_cast<int64_t>(tok)) * a.q_stride + q_head() * kDim + 8 * h;
+#pragma unroll
+    for (int s = 0; s < 16; ++s) q[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
+  }
+  Rows r;
+  clear(r);
+  r.m = -FLT_MAX;
+  r.l = 0;
+  r.left = 0;
+  const float factor = fabsf(a.scale) * kLog2e;
+
+  // Stage i of a wave's KT / (2 NW): keys 2 NW i + 2 wave and the one after,
+  // 512 bytes each, lane l the chunk that belongs in place l % 32.  Rows past
+  // the sequence read as zeros.
+  const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+  const uint32_t place = (col ^ swizzle(2 * wave + h)) * 16;
+  uint32_t ko = (2 * wave + h) * static_cast<uint32_t>(a.k_stride) * 2, vo = (2 * wave + h) * static_cast<uint32_t>(a.v_stride) * 2;
+  const auto stage = [&](int buf, int32_t t0) {
+    const int64_t at = rr.begin + static_cast<int64_t>(t0);
+    const u32x4 kb = buffer_of(a.k_new + at * a.k_stride + head * kDim, ((n - t0 - 1) * a.k_stride + kDim) * 2);
+    const u32x4 vb = buffer_of(a.v_new + at * a.v_stride + head * kDim, ((n - t0 - 1) * a.v_stride + kDim) * 2);
+    asm volatile("" : "+v"(ko), "+v"(vo));  // the sums below are made each time, not kept in registers
+#pragma unroll
+    for (int i = 0; i < KT / (2 * NW); ++i) {
+      const int pair = 2 * NW * i + 2 * wave;
+      // 8 keys on, the swizzle differs in one bit; 16 keys on, it is the same
+      const uint32_t c = place ^ (swizzle(2 * NW * i) * 16);
+      stage16(kb, ko + 2 * NW * i * static_cast<uint32_t>(a.k_stride) * 2 + c, base + buf * kStage + pair * 512);
+      stage16(vb, vo + 2 * NW * i * static_cast<uint32_t>(a.v_stride) * 2 + c, base + buf * kStage + KT * 512 + pair * 512);
+    }
+  };
+  const TileLane at = tile_lane(lane);
+  stage(0, 0);
+  // settle Q before the loop (and turn it round for a negative scale), so that
+  // no wait on its loads stands inside
+#pragma unroll
+  for (int s = 0; s < 16; ++s) {
+    if (a.scale < 0) q[s] ^= 0x80008000u;
+    asm volatile("" : "+v"(q[s]));
+  }
+  for (int32_t t0 = 0, buf = 0; t0 < end; t0 += KT, buf ^= 1) {
+    wait_staged();
+    barrier();
+    if (t0 + KT < end) stage(buf ^ 1, t0 + KT);
+#pragma unroll
+    for (int u = 0; u < KT / 32; ++u) {
+      const int32_t k0 = t0 + 32 * u;
+      if (k0 > last) continue;
+      const uint32_t kb = base + buf * kStage + u * 16384, vb = kb + KT * 512;
+      key_step<false>(r, q, kb + at.k, vb + at.v, factor, tok - k0, k0 + 31 > first, 0, 0, lane);
+    }
+  }
+  add_nonfinite(r, (first + 1) / 32 * 32, last, tok, h, [&](int key) {
+    return a.v_new + (rr.begin + static_cast<int64_t>(key)) * a.v_stride + head * kDim;
+  });
+  r.l += half_swap(r.l);
+  const float inv = 1.0f / r.l;
+  if (w0 + col < rows) {
+    uint16_t* op = a.out + ((rr.begin + static_cast<int64_t>(tok)) * a.q_heads + q_head()) * kDim;
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint2 w = {pack_bf16x2(r.o[t][4 * i] * inv, r.o[t][4 * i + 1] * inv),
+                         pack_bf16x2(r.o[t][4 * i + 2] * inv, r.o[t][4 * i + 3] * inv)};
+        *reinterpret_cast<uint2*>(op + 32 * t + 8 * i + 4 * h) = w;
+      }
+  }
+}
+
+}  // namespace hlwq_kv

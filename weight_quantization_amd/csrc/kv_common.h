@@ -89,7 +89,7 @@ __device__ __forceinline__ RowRange row_range(const int32_t* __restrict__ cu, in
 // ---------------------------------------------------------------------------
 
 inline bool mul_ok(int64_t a, int64_t b, int64_t* r) { return !__builtin_mul_overflow(a, b, r); }
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 // One buffer of a call: its bytes [lo, hi), and whether the call writes it (a
@@ -138,11 +138,13 @@ int launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t stream, type
 constexpr int64_t kMaxRequests = 1 << 20;
 constexpr int64_t kMaxTable = 1 << 20;
 constexpr int64_t kMaxHeads = 1 << 12;
+constexpr int64_t kMaxStride = 1 << 22;  // elements: 64 rows stay below 2^31 bytes
 
 // Rows of `heads` 256-vectors, `stride` elements apart: the extent in
 // elements, or a status.
 inline int check_rows(const void* p, int64_t stride, int64_t rows, int64_t heads, int64_t* extent) {
   if (stride < heads * kDim || (stride & 7)) return HLWQ_ERR_SHAPE;
+  if (stride > kMaxStride) return HLWQ_ERR_LIMIT;
   int64_t bytes;
   if (!mul_ok(rows - 1, stride, extent) || __builtin_add_overflow(*extent, heads * kDim, extent) ||
       !mul_ok(*extent, 2, &bytes))
