@@ -58,7 +58,7 @@ extern "C" {
 /* Keys or values of a paged cache. */
 typedef struct hlwq_kv_store {
   void* packed; /* u8   [n_pages][kv_heads][page_size][32 * bits], 16-byte aligned */
-  void* norms;  /* fp16 [n_pages][kv_heads][page_size] */
+  void* norms;  /* fp16 [n_pages][kv_heads][page_size], 16-byte aligned */
   void* window; /* bf16 [requests][kv_heads][ring][256], 16-byte aligned; may be NULL when ring = 0 */
 } hlwq_kv_store;
 

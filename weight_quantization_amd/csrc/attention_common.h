@@ -196,4 +196,107 @@ __device__ __forceinline__ Found find(const Prefix& p, int64_t x, F of, int64_t*
   return f;
 }
 
+// How the paged kernels share their work out.  A tile is M consecutive rows of
+// one request and KV head; it costs its key blocks of KT tokens: those of the
+// pages, then those of the window and of the step's own tokens up to the
+// tile's last row.  The tiles lie one after the other, by request, KV head and
+// row, and every workgroup takes an equal stretch of their cost, so that
+// requests of any lengths load the workgroups alike; a tile that several
+// workgroups share is joined from their partial sums afterwards.
+template <int M, int KT>
+struct Work {
+  Extent e;
+  int64_t tiles, base, step, page_blocks;
+  __device__ __forceinline__ Work(const AttnArgs& a, int32_t b) {
+    e = extent_of(a, b);
+    const int64_t rows = static_cast<int64_t>(e.n) * a.group;
+    tiles = rows >= a.least && rows <= a.most ? ceil_div(rows, M) : 0;
+    page_blocks = ceil_div(e.paged, KT);
+    base = page_blocks + ceil_div(e.held - e.enc + 1, KT);
+    step = ceil_div(ceil_div(M, a.group), KT);  // at least the blocks by which a tile's tokens pass the one before it
+  }
+  // of one KV head
+  __device__ __forceinline__ int64_t cost_before(int64_t j) const { return j * base + step * (j * (j + 1) / 2); }
+  __device__ __forceinline__ int64_t cost(int64_t j) const { return base + step * (j + 1); }
+  __device__ __forceinline__ int64_t head_cost() const { return cost_before(tiles); }
+  // the tile that holds place x of a KV head's cost
+  __device__ __forceinline__ int64_t tile_at(int64_t x) const {
+    const double b = 2.0 * base + step, s = step;
+    int64_t j = static_cast<int64_t>((sqrt(b * b + 8.0 * s * x) - b) / (2.0 * s));
+    j = max(min(j, tiles - 1), int64_t{0});
+    while (j > 0 && cost_before(j) > x) --j;
+    while (j + 1 < tiles && cost_before(j + 1) <= x) ++j;
+    return j;
+  }
+  // tokens (of the step) of the tile's first row and last row
+  __device__ __forceinline__ int32_t first_token(const AttnArgs& a, int64_t j) const { return static_cast<int32_t>(j * M / a.group); }
+  __device__ __forceinline__ int32_t last_token(const AttnArgs& a, int64_t j) const {
+    return static_cast<int32_t>(min((j + 1) * M, static_cast<int64_t>(e.n) * a.group) - 1) / a.group;
+  }
+  // key blocks of tile j: the pages', then the others
+  __device__ __forceinline__ int64_t blocks(const AttnArgs& a, int64_t j) const {
+    return page_blocks + ceil_div(e.held - e.enc + last_token(a, j) + 1, KT);
+  }
+};
+
+// The stretches: worker w of `workers` takes cost [bound(w), bound(w + 1)).
+// Fewer workgroups than there are share a small total, at least kLeastBlocks
+// blocks to each.
+struct Share {
+  int64_t total;
+  int64_t workers;
+  __device__ __forceinline__ Share(int64_t t, int64_t most, int64_t least_blocks) {
+    total = t;
+    workers = max(min(most, t / least_blocks), int64_t{1});
+  }
+  __device__ __forceinline__ int64_t bound(int64_t w) const { return w * total / workers; }
+  // the worker whose stretch holds x
+  __device__ __forceinline__ int64_t worker_at(int64_t x) const {
+    int64_t w = x * workers / total;
+    while (w > 0 && bound(w) > x) --w;
+    while (bound(w + 1) <= x) ++w;
+    return w;
+  }
+};
+
+// A worker's partial sums of a tile: slot 0 if its stretch begins inside the
+// tile, 1 if it begins with or before it.  M rows of 256 floats to a slot, then for
+// all slots the rows' maxima and sums.
+template <int M>
+__device__ __forceinline__ float* partial_row(const AttnArgs& a, int64_t worker, int slot, int row) {
+  return a.partial + ((worker * 2 + slot) * M + row) * kDim;
+}
+template <int M>
+__device__ __forceinline__ float2* partial_stat(const AttnArgs& a, int64_t worker, int slot, int row) {
+  return reinterpret_cast<float2*>(a.partial + static_cast<int64_t>(a.workers) * 2 * M * kDim) + (worker * 2 + slot) * M + row;
+}
+constexpr int64_t partial_floats(int64_t workers, int64_t m) { return workers * 2 * m * (kDim + 2); }
+
+// One worker's segments, one after the other.
+struct Segment {
+  int32_t b, head;
+  int64_t tile, from, to, cost;  // places [from, to) of the tile's cost
+};
+template <int M, int KT, class F>
+__device__ __forceinline__ void for_segments(const AttnArgs& a, const Share& s, const Found& first, int64_t worker, F run) {
+  int64_t left = s.bound(worker + 1) - s.bound(worker);
+  int64_t rest = first.rest;
+  for (int32_t b = first.b; left > 0 && b < a.requests; ++b, rest = 0) {
+    const Work<M, KT> w(a, b);
+    if (w.tiles == 0) continue;
+    const int64_t head_cost = w.head_cost();
+    int32_t head = static_cast<int32_t>(rest / head_cost);
+    rest -= head * head_cost;
+    for (; head < a.kv_heads && left > 0; ++head, rest = 0) {
+      int64_t j = w.tile_at(rest);
+      rest -= w.cost_before(j);
+      for (; j < w.tiles && left > 0; ++j, rest = 0) {
+        Segment g{b, head, j, rest, min(rest + left, w.cost(j)), w.cost(j)};
+        left -= g.to - g.from;
+        run(w, g);
+      }
+    }
+  }
+}
+
 }  // namespace hlwq_kv

@@ -169,7 +169,7 @@ inline int check_cache(const hlwq_kv_cache& c, bool written, std::vector<Span>& 
     return HLWQ_ERR_SHAPE;
   for (const hlwq_kv_store* s : {&c.k, &c.v}) {
     if ((vecs > 0 && (!s->packed || !s->norms)) || (ring > 0 && !s->window)) return HLWQ_ERR_NULL;
-    if (misaligned(s->packed, 16) || misaligned(s->norms, 2) || misaligned(s->window, 16)) return HLWQ_ERR_ALIGN;
+    if (misaligned(s->packed, 16) || misaligned(s->norms, 16) || misaligned(s->window, 16)) return HLWQ_ERR_ALIGN;
     add_span(spans, s->packed, vecs, 32 * c.bits, written);
     add_span(spans, s->norms, vecs, 2, written);
     add_span(spans, s->window, ring, 2 * kDim, written);
