@@ -1,8 +1,7 @@
 // attention.hip — attention over the paged cache of HLWQ codes and over whole
 // prompts (include/hlwq_attention.h).
 
-#include "attention_split.h"
-#include "attention_tile.h"
+#include "attention_chunk.h"
 
 #include <cmath>
 
@@ -34,37 +33,74 @@ int launch_prompt(const AttnArgs& a, hipStream_t stream) {
                 dim3(static_cast<uint32_t>(groups)), dim3(wide ? 512 : 256), stream, a);
 }
 
-// Workgroups of the split kernel, and the rows to its tiles: sixteen where
-// the requests' mean fits (or nearly), else 32.
-constexpr int64_t kSplitWorkers = 512;
-bool split_wide(int64_t requests, int64_t rows, int64_t group) { return rows * group > 16 * requests; }
-int64_t split_workers(bool wide) { return wide ? kSplitWorkers / 2 : kSplitWorkers; }
+// How a paged call is shared among the kernels: requests with at most kFewRows
+// query rows to a KV head go to the split kernel (in tiles of sixteen or 32),
+// the others to the chunk kernel.  The lengths are on the device, so the host
+// goes by the mean: where it is few rows the split kernel takes every request,
+// and a single request goes to one of the two.
+constexpr int64_t kFewRows = 32;
+constexpr int64_t kSplitWorkers = 512, kChunkWorkers = 256;
+struct PagedPlan {
+  int split_rows;      // rows to a tile of the split kernel; 0: it is not called
+  bool chunk;          // whether the chunk kernel is called
+  int64_t split_workers;
+  size_t split_bytes, chunk_bytes;  // of workspace, each its own
+};
+PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t group) {
+  PagedPlan p;
+  p.chunk = rows * group > kFewRows * requests;
+  p.split_rows = p.chunk && requests == 1 ? 0 : p.chunk || rows * group > 16 * requests ? 32 : 16;
+  p.split_workers = p.split_rows == 32 ? kSplitWorkers / 2 : kSplitWorkers;
+  p.split_bytes = p.split_rows ? partial_floats(p.split_workers, p.split_rows) * sizeof(float) : 0;
+  p.chunk_bytes = p.chunk ? partial_floats(kChunkWorkers, kChunkRows) * sizeof(float) : 0;
+  return p;
+}
 
 size_t workspace_bytes_of(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
   bool nothing;
   if (requests <= 0 || requests > kMaxRequests || check_heads(rows, q_heads, kv_heads, &nothing) != HLWQ_OK || nothing) return 0;
-  const bool wide = split_wide(requests, rows, q_heads / kv_heads);
-  return static_cast<size_t>(partial_floats(split_workers(wide), wide ? 32 : 16)) * sizeof(float);
+  const PagedPlan p = paged_plan(requests, rows, q_heads / kv_heads);
+  return p.split_bytes + p.chunk_bytes;
+}
+
+// Workgroups that join rows of tiles of m rows: at most one tile more per
+// request than whole ones, every tile holding a row.
+int64_t join_groups(const AttnArgs& a, int64_t m) {
+  const int64_t rows = static_cast<int64_t>(a.rows) * a.group;
+  return std::min(rows / m + a.requests, rows) * a.kv_heads * m;
 }
 
 template <int BITS, int NR>
-int launch_split(AttnArgs a, hipStream_t stream) {
-  constexpr int M = 16 * NR;
-  a.workers = static_cast<int32_t>(split_workers(NR == 2));
-  a.least = 1;
-  a.most = 0x7fffffff;
-  const int64_t rows = static_cast<int64_t>(a.rows) * a.group;
-  const int64_t tiles = std::min(rows / M + a.requests, rows) * a.kv_heads;
-  if (tiles * M > 0x7fffff) return HLWQ_ERR_LIMIT;
+int launch_split(const AttnArgs& a, hipStream_t stream) {
   const int st = launch(hlwq_split_attention_kernel<BITS, NR>, dim3(static_cast<uint32_t>(a.workers)), dim3(kSplitThreads), stream, a);
   if (st != HLWQ_OK) return st;
-  return launch(hlwq_join_attention_kernel<M, kSplitBlock, kSplitLeast>, dim3(static_cast<uint32_t>(tiles * M)),
+  return launch(hlwq_join_attention_kernel<16 * NR, kSplitBlock, kSplitLeast>, dim3(static_cast<uint32_t>(join_groups(a, 16 * NR))),
                 dim3(kSplitThreads), stream, a);
 }
 
-int launch_paged(int bits, const AttnArgs& a, hipStream_t stream) {
-  if (split_wide(a.requests, a.rows, a.group)) return bits == 3 ? launch_split<3, 2>(a, stream) : launch_split<2, 2>(a, stream);
-  return bits == 3 ? launch_split<3, 1>(a, stream) : launch_split<2, 1>(a, stream);
+int launch_paged(int bits, AttnArgs a, void* ws, hipStream_t stream) {
+  const PagedPlan p = paged_plan(a.requests, a.rows, a.group);
+  if ((p.split_rows && join_groups(a, p.split_rows) > 0xffffff) || (p.chunk && join_groups(a, kChunkRows) > 0xffffff))
+    return HLWQ_ERR_LIMIT;
+  if (p.split_rows) {
+    a.partial = static_cast<float*>(ws);
+    a.workers = static_cast<int32_t>(p.split_workers);
+    a.least = 1;
+    a.most = p.chunk ? kFewRows : 0x7fffffff;
+    const int st = p.split_rows == 16 ? (bits == 3 ? launch_split<3, 1>(a, stream) : launch_split<2, 1>(a, stream))
+                                      : (bits == 3 ? launch_split<3, 2>(a, stream) : launch_split<2, 2>(a, stream));
+    if (st != HLWQ_OK) return st;
+  }
+  if (!p.chunk) return HLWQ_OK;
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.split_bytes);
+  a.workers = kChunkWorkers;
+  a.least = p.split_rows ? kFewRows + 1 : 1;
+  a.most = 0x7fffffff;
+  const int st = launch(bits == 3 ? hlwq_chunk_attention_kernel<3> : hlwq_chunk_attention_kernel<2>,
+                        dim3(static_cast<uint32_t>(a.workers)), dim3(512), stream, a);
+  if (st != HLWQ_OK) return st;
+  return launch(hlwq_join_attention_kernel<kChunkRows, kChunkBlock, kChunkLeast>,
+                dim3(static_cast<uint32_t>(join_groups(a, kChunkRows))), dim3(kSplitThreads), stream, a);
 }
 
 int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q_heads, const void* k, int64_t k_stride,
@@ -123,11 +159,10 @@ int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q
   a.q_heads = static_cast<int32_t>(q_heads);
   a.kv_heads = static_cast<int32_t>(c->kv_heads);
   a.group = static_cast<int32_t>(q_heads / c->kv_heads);
-  a.partial = static_cast<float*>(ws);
   a.n_pages = static_cast<int32_t>(c->n_pages);
   a.page_shift = __builtin_ctzll(static_cast<uint64_t>(c->page_size));
   a.scale = scale;
-  return launch_paged(c->bits, a, stream);
+  return launch_paged(c->bits, a, ws, stream);
 }
 
 int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,

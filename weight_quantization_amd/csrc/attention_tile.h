@@ -232,9 +232,9 @@ __device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t
 // to]: added to the row if it sees their key (key <= lim).  value(key): the
 // key's 256 values in memory.
 template <class F>
-__device__ __forceinline__ void add_nonfinite(Rows& r, int from, int to, int lim, int h, F value) {
+__device__ __forceinline__ void add_nonfinite(Rows& r, int64_t from, int64_t to, int64_t lim, int h, F value) {
   if (!__any(r.left != 0)) return;
-  for (int key = from; key <= to; ++key) {
+  for (int64_t key = from; key <= to; ++key) {
     const uint16_t* p = value(key);
 #pragma unroll
     for (int t = 0; t < 8; ++t)
@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
       key_step<false>(r, q, kb + at.k, vb + at.v, factor, tok - k0, k0 + 31 > first, 0, 0, lane);
     }
   }
-  add_nonfinite(r, (first + 1) / 32 * 32, last, tok, h, [&](int key) {
-    return a.v_new + (rr.begin + static_cast<int64_t>(key)) * a.v_stride + head * kDim;
+  add_nonfinite(r, (first + 1) / 32 * 32, last, tok, h, [&](int64_t key) {
+    return a.v_new + (rr.begin + key) * a.v_stride + head * kDim;
   });
   r.l += half_swap(r.l);
   const float inv = 1.0f / r.l;
