@@ -129,7 +129,7 @@ def test_workspace_helper():
     w = wq.hlwq_kv_paged_attention_workspace
     assert w(0, 5, 24, 4) == 0 and w(2, 0, 24, 4) == 0 and w(2, 5, 23, 4) == 0 and w(2, 5, 24, 0) == 0
     assert w(-1, 5, 24, 4) == 0 and w(2 ** 21, 5, 24, 4) == 0
-    assert w(1, 1, 24, 4) > 0 and w(2 ** 20, 2 ** 31 - 1, 4096, 1) > 0
+    assert w(1, 1, 24, 4) > 0 and w(2 ** 20, 2 ** 31 // 4096 - 1, 4096, 1) > 0 and w(1, 2 ** 31 // 4096, 4096, 1) == 0
 
 
 def prompt(lib, q=at(0), qs=6144, k=at(1), ks=1024, v=at(2), vs=1024, cu=at(3), n=2, rows=5, hq=24, hk=4, d=256,

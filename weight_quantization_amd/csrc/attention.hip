@@ -14,7 +14,8 @@ int check_heads(int64_t rows, int64_t q_heads, int64_t kv_heads, bool* nothing) 
   *nothing = rows == 0 || q_heads == 0;
   if (*nothing) return HLWQ_OK;
   if (kv_heads == 0 || q_heads % kv_heads) return HLWQ_ERR_SHAPE;
-  if (q_heads > kMaxHeads || rows > 0x7fffffff) return HLWQ_ERR_LIMIT;
+  // (out alone would pass the memory there is)
+  if (q_heads > kMaxHeads || rows > 0x7fffffff / q_heads) return HLWQ_ERR_LIMIT;
   return HLWQ_OK;
 }
 
@@ -63,24 +64,25 @@ size_t workspace_bytes_of(int64_t requests, int64_t rows, int64_t q_heads, int64
   return p.split_bytes + p.chunk_bytes;
 }
 
-// Workgroups that join rows of tiles of m rows: at most one tile more per
-// request than whole ones, every tile holding a row.
-int64_t join_groups(const AttnArgs& a, int64_t m) {
+// Workgroups that join tiles of m rows, `each` rows to a workgroup: at most one
+// tile more per request than whole ones, every tile holding a row.
+constexpr int kJoinWaveRows = 4;  // of wide tiles
+int64_t join_groups(const AttnArgs& a, int64_t m, int64_t each) {
   const int64_t rows = static_cast<int64_t>(a.rows) * a.group;
-  return std::min(rows / m + a.requests, rows) * a.kv_heads * m;
+  return std::min(rows / m + a.requests, rows) * a.kv_heads * (m / each);
 }
 
 template <int BITS, int NR>
 int launch_split(const AttnArgs& a, hipStream_t stream) {
   const int st = launch(hlwq_split_attention_kernel<BITS, NR>, dim3(static_cast<uint32_t>(a.workers)), dim3(kSplitThreads), stream, a);
   if (st != HLWQ_OK) return st;
-  return launch(hlwq_join_attention_kernel<16 * NR, kSplitBlock, kSplitLeast>, dim3(static_cast<uint32_t>(join_groups(a, 16 * NR))),
+  return launch(hlwq_join_attention_kernel<16 * NR, kSplitBlock, kSplitLeast, 0>, dim3(static_cast<uint32_t>(join_groups(a, 16 * NR, 1))),
                 dim3(kSplitThreads), stream, a);
 }
 
 int launch_paged(int bits, AttnArgs a, void* ws, hipStream_t stream) {
   const PagedPlan p = paged_plan(a.requests, a.rows, a.group);
-  if ((p.split_rows && join_groups(a, p.split_rows) > 0xffffff) || (p.chunk && join_groups(a, kChunkRows) > 0xffffff))
+  if ((p.split_rows && join_groups(a, p.split_rows, 1) > 0xffffff) || (p.chunk && join_groups(a, kChunkRows, 4 * kJoinWaveRows) > 0xffffff))
     return HLWQ_ERR_LIMIT;
   if (p.split_rows) {
     a.partial = static_cast<float*>(ws);
@@ -99,8 +101,8 @@ int launch_paged(int bits, AttnArgs a, void* ws, hipStream_t stream) {
   const int st = launch(bits == 3 ? hlwq_chunk_attention_kernel<3> : hlwq_chunk_attention_kernel<2>,
                         dim3(static_cast<uint32_t>(a.workers)), dim3(512), stream, a);
   if (st != HLWQ_OK) return st;
-  return launch(hlwq_join_attention_kernel<kChunkRows, kChunkBlock, kChunkLeast>,
-                dim3(static_cast<uint32_t>(join_groups(a, kChunkRows))), dim3(kSplitThreads), stream, a);
+  return launch(hlwq_join_attention_kernel<kChunkRows, kChunkBlock, kChunkLeast, kJoinWaveRows>,
+                dim3(static_cast<uint32_t>(join_groups(a, kChunkRows, 4 * kJoinWaveRows))), dim3(kSplitThreads), stream, a);
 }
 
 int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q_heads, const void* k, int64_t k_stride,

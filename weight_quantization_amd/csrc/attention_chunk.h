@@ -87,25 +87,22 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
     const Work<M, KT> w(a, b);
     return w.head_cost() * a.kv_heads;
   };
-  int64_t* scratch = reinterpret_cast<int64_t*>(lds);
-  const Prefix pre = prefix_of<512>(a.requests, cost, scratch);
-  if (pre.total == 0) return;
-  const Share share(pre.total, a.workers, kChunkLeast);
+  const int64_t total = sum_over(a.requests, cost);
+  const Share share(total, a.workers, kChunkLeast);
+  if (total == 0 || blockIdx.x >= share.workers) return;
   // Workgroups of one XCD (every eighth) take neighbouring stretches, which
   // share a KV head's keys in its L2.
   const int64_t worker = share.workers % 8 == 0 ? (blockIdx.x % 8) * (share.workers / 8) + blockIdx.x / 8 : blockIdx.x;
-  if (blockIdx.x >= share.workers) return;
-  const Found first = find(pre, share.bound(worker), cost, scratch);
-  if (first.b < 0) return;
+  const Found first = find(a.requests, share.bound(worker), cost, [](int32_t) { return int64_t{0}; });
 
   for_segments<M, KT>(a, share, first, worker, [&](const Work<M, KT>& w, const Segment& g) {
     const Extent& e = w.e;
-    const int64_t rows = static_cast<int64_t>(e.n) * a.group, w0 = g.tile * M + 32 * wave;
+    const int32_t rows = w.rows(a), w0 = static_cast<int32_t>(g.tile * M) + 32 * wave;
     const int64_t blocks = w.blocks(a, g.tile);
-    const int64_t u0 = g.from * blocks / g.cost, u1 = g.to * blocks / g.cost;
+    const int64_t u0 = w.block_at(g.from, blocks, g.cost), u1 = w.block_at(g.to, blocks, g.cost);
     const int64_t near = e.held - e.enc;
-    const int32_t tok = static_cast<int32_t>(min(w0 + col, rows - 1) / a.group);
-    const auto q_head = [&]() { return g.head * static_cast<int64_t>(a.group) + (min(w0 + col, rows - 1) - static_cast<int64_t>(tok) * a.group); };
+    const int32_t tok = token_of(min(w0 + col, rows - 1), a.group);
+    const auto q_head = [&]() { return g.head * a.group + (min(w0 + col, rows - 1) - tok * a.group); };
     const auto q_ptr = [&]() { return a.q + (e.begin + static_cast<int64_t>(tok)) * a.q_stride + q_head() * kDim + 8 * h; };
     Rows r;
     r.m = -FLT_MAX;
@@ -253,8 +250,8 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
 
     if (u1 > w.page_blocks) {
       const int64_t from = max(u0, w.page_blocks) - w.page_blocks, to = u1 - w.page_blocks;
-      const int64_t first_key = near + min(w0, rows - 1) / a.group;               // the last that the wave's first row sees
-      const int64_t last_key = idle ? -1 : near + min(w0 + 31, rows - 1) / a.group;  // and its last
+      const int64_t first_key = near + token_of(min(w0, rows - 1), a.group);               // the last that the wave's first row sees
+      const int64_t last_key = idle ? -1 : near + token_of(min(w0 + 31, rows - 1), a.group);  // and its last
       const int64_t end_key = near + w.last_token(a, g.tile);                      // and the tile's last
       const int64_t ring0 = a.ring > 0 ? e.enc % a.ring : 0;
       const auto row = [&](int side, int64_t k) {

@@ -71,6 +71,11 @@ __device__ __forceinline__ Extent extent_of(const AttnArgs& a, int32_t b) {
   return e;
 }
 
+// The token that row r of a request belongs to.
+__device__ __forceinline__ int32_t token_of(int32_t r, int32_t group) {
+  return static_cast<int32_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(group));
+}
+
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Value of lane l ^ 32.
@@ -126,73 +131,67 @@ __device__ __forceinline__ u32x2 look_up(uint32_t c) {
 }
 
 // ---------------------------------------------------------------------------
-// Finding work.  The requests' lengths are on the device, so every workgroup
-// sums what the requests ask for and finds its own share of it.
+// Finding work.  The requests' lengths are on the device, so every wave sums
+// what the requests ask for and finds its workgroup's share of it, without
+// LDS or a barrier: lane i takes requests i, i + 64, ..
 // ---------------------------------------------------------------------------
 
-// The prefix sum of a quantity over the requests: thread i of NT holds the sum
-// `own` of requests [b0, b1) and the sum `pre` of all before them.
-struct Prefix {
-  int64_t own, pre, total;
-  int32_t b0, b1;
-};
-template <int NT, class F>
-__device__ __forceinline__ Prefix prefix_of(int32_t requests, F of, int64_t* lds) {
-  Prefix p;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int32_t per = (requests + NT - 1) / NT;
-  p.b0 = min(static_cast<int32_t>(threadIdx.x) * per, requests);
-  p.b1 = min(p.b0 + per, requests);
-  p.own = 0;
-  for (int32_t b = p.b0; b < p.b1; ++b) p.own += of(b);
-  int64_t v = p.own;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
-  if (lane == 63) lds[wave] = v;
-  __syncthreads();
-  p.pre = v - p.own;
-  p.total = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 64; ++w) {
-    if (w < wave) p.pre += lds[w];
-    p.total += lds[w];
-  }
-  __syncthreads();
-  return p;
+// a / b for a, b >= 0, in 32 bits where they fit (64 take ten times as long).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
-// The request that holds unit x of the quantity, and x's place in it; -1 if
-// there is none.  lds: 2 words.
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(v) >> 32));
+  return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// The sum of a quantity over the requests.
+template <class F>
+__device__ __forceinline__ int64_t sum_over(int32_t requests, F of) {
+  int64_t v = 0;
+  for (int32_t b = threadIdx.x & 63; b < requests; b += 64) v += of(b);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  return uniform64(v);
+}
+
+// The request that holds unit x of the quantity (0 <= x < its sum), x's place
+// in it, and the sum of `also` over the requests before it.
 struct Found {
   int32_t b;
-  int64_t rest;
+  int64_t rest, also;
 };
-template <class F>
-__device__ __forceinline__ Found find(const Prefix& p, int64_t x, F of, int64_t* lds) {
-  if (threadIdx.x == 0) lds[0] = -1;
-  __syncthreads();
-  if (x >= p.pre && x < p.pre + p.own) {
-    int64_t at = p.pre;
-    for (int32_t b = p.b0; b < p.b1; ++b) {
-      const int64_t n = of(b);
-      if (x < at + n) {
-        lds[0] = b;
-        lds[1] = x - at;
-        break;
+template <class F, class G>
+__device__ __forceinline__ Found find(int32_t requests, int64_t x, F of, G also) {
+  const int lane = threadIdx.x & 63;
+  Found f{0, 0, 0};
+  for (int32_t b0 = 0; b0 < requests; b0 += 64) {
+    const bool in = b0 + lane < requests;
+    const int64_t own = in ? of(b0 + lane) : 0, other = in ? also(b0 + lane) : 0;
+    int64_t v = own, w = other;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t p = __shfl_up(v, d, 64), q = __shfl_up(w, d, 64);
+      if (lane >= d) {
+        v += p;
+        w += q;
       }
-      at += n;
     }
+    const uint64_t past = __ballot(x < v);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      f.b = b0 + at;
+      f.rest = uniform64(x - __shfl(v - own, at, 64));
+      f.also += uniform64(__shfl(w - other, at, 64));
+      return f;
+    }
+    x -= uniform64(__shfl(v, 63, 64));
+    f.also += uniform64(__shfl(w, 63, 64));
   }
-  __syncthreads();
-  Found f;
-  f.b = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(lds[0]));
-  const int64_t rest = lds[1];
-  f.rest = static_cast<int64_t>((static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(rest) >> 32))) << 32) |
-                                static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(rest))));
-  __syncthreads();
+  f.b = -1;
   return f;
 }
 
@@ -209,53 +208,60 @@ struct Work {
   int64_t tiles, base, step, page_blocks;
   __device__ __forceinline__ Work(const AttnArgs& a, int32_t b) {
     e = extent_of(a, b);
-    const int64_t rows = static_cast<int64_t>(e.n) * a.group;
+    const int32_t rows = e.n * a.group;
     tiles = rows >= a.least && rows <= a.most ? ceil_div(rows, M) : 0;
     page_blocks = ceil_div(e.paged, KT);
     base = page_blocks + ceil_div(e.held - e.enc + 1, KT);
-    step = ceil_div(ceil_div(M, a.group), KT);  // at least the blocks by which a tile's tokens pass the one before it
+    // at least the blocks by which a tile's tokens pass those of the one before
+    step = M <= KT ? 1 : (static_cast<uint32_t>(M - 1) / static_cast<uint32_t>(a.group) + KT) / KT;
   }
   // of one KV head
-  __device__ __forceinline__ int64_t cost_before(int64_t j) const { return j * base + step * (j * (j + 1) / 2); }
-  __device__ __forceinline__ int64_t cost(int64_t j) const { return base + step * (j + 1); }
+  __device__ __forceinline__ int64_t cost_before(int64_t j) const { return j * base + step * (j * (j - 1) / 2); }
+  __device__ __forceinline__ int64_t cost(int64_t j) const { return base + step * j; }
   __device__ __forceinline__ int64_t head_cost() const { return cost_before(tiles); }
   // the tile that holds place x of a KV head's cost
   __device__ __forceinline__ int64_t tile_at(int64_t x) const {
-    const double b = 2.0 * base + step, s = step;
+    if (tiles == 1) return 0;
+    const double b = 2.0 * base - step, s = step;
     int64_t j = static_cast<int64_t>((sqrt(b * b + 8.0 * s * x) - b) / (2.0 * s));
     j = max(min(j, tiles - 1), int64_t{0});
     while (j > 0 && cost_before(j) > x) --j;
     while (j + 1 < tiles && cost_before(j + 1) <= x) ++j;
     return j;
   }
+  __device__ __forceinline__ int32_t rows(const AttnArgs& a) const { return e.n * a.group; }
   // tokens (of the step) of the tile's first row and last row
-  __device__ __forceinline__ int32_t first_token(const AttnArgs& a, int64_t j) const { return static_cast<int32_t>(j * M / a.group); }
+  __device__ __forceinline__ int32_t first_token(const AttnArgs& a, int64_t j) const {
+    return static_cast<uint32_t>(j * M) / static_cast<uint32_t>(a.group);
+  }
   __device__ __forceinline__ int32_t last_token(const AttnArgs& a, int64_t j) const {
-    return static_cast<int32_t>(min((j + 1) * M, static_cast<int64_t>(e.n) * a.group) - 1) / a.group;
+    return static_cast<uint32_t>(min((j + 1) * M, static_cast<int64_t>(rows(a))) - 1) / static_cast<uint32_t>(a.group);
   }
   // key blocks of tile j: the pages', then the others
   __device__ __forceinline__ int64_t blocks(const AttnArgs& a, int64_t j) const {
     return page_blocks + ceil_div(e.held - e.enc + last_token(a, j) + 1, KT);
   }
+  // the block at place x of a tile's cost: its blocks spread evenly over it
+  __device__ __forceinline__ static int64_t block_at(int64_t x, int64_t blocks, int64_t cost) {
+    return blocks == cost ? x : quotient(x * blocks, cost);
+  }
 };
 
-// The stretches: worker w of `workers` takes cost [bound(w), bound(w + 1)).
-// Fewer workgroups than there are share a small total, at least kLeastBlocks
-// blocks to each.
+// The stretches: worker w of `workers` takes cost [bound(w), bound(w + 1)),
+// the first `more` one unit more than the others.  Fewer workgroups than there
+// are share a small total, at least least_blocks to each.
 struct Share {
-  int64_t total;
-  int64_t workers;
-  __device__ __forceinline__ Share(int64_t t, int64_t most, int64_t least_blocks) {
-    total = t;
-    workers = max(min(most, t / least_blocks), int64_t{1});
+  int64_t workers, each, more;
+  __device__ __forceinline__ Share(int64_t total, int64_t most, int64_t least_blocks) {
+    workers = max(min(most, total / least_blocks), int64_t{1});
+    each = quotient(total, workers);
+    more = total - each * workers;
   }
-  __device__ __forceinline__ int64_t bound(int64_t w) const { return w * total / workers; }
+  __device__ __forceinline__ int64_t bound(int64_t w) const { return w * each + min(w, more); }
   // the worker whose stretch holds x
   __device__ __forceinline__ int64_t worker_at(int64_t x) const {
-    int64_t w = x * workers / total;
-    while (w > 0 && bound(w) > x) --w;
-    while (bound(w + 1) <= x) ++w;
-    return w;
+    const int64_t cut = more * (each + 1);
+    return x < cut ? quotient(x, each + 1) : more + quotient(x - cut, each);
   }
 };
 
@@ -285,7 +291,7 @@ __device__ __forceinline__ void for_segments(const AttnArgs& a, const Share& s, 
     const Work<M, KT> w(a, b);
     if (w.tiles == 0) continue;
     const int64_t head_cost = w.head_cost();
-    int32_t head = static_cast<int32_t>(rest / head_cost);
+    int32_t head = static_cast<int32_t>(quotient(rest, head_cost));
     rest -= head * head_cost;
     for (; head < a.kv_heads && left > 0; ++head, rest = 0) {
       int64_t j = w.tile_at(rest);

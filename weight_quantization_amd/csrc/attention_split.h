@@ -437,20 +437,17 @@ hlwq_split_attention_kernel(const AttnArgs a) {
     const Work<M, kSplitBlock> w(a, b);
     return w.head_cost() * a.kv_heads;
   };
-  int64_t* scratch = reinterpret_cast<int64_t*>(lds);
-  const Prefix pre = prefix_of<kSplitThreads>(a.requests, cost, scratch);
-  if (pre.total == 0) return;
-  const Share share(pre.total, a.workers, kSplitLeast);
+  const int64_t total = sum_over(a.requests, cost);
+  const Share share(total, a.workers, kSplitLeast);
   const int64_t worker = blockIdx.x;
-  if (worker >= share.workers) return;
-  const Found first = find(pre, share.bound(worker), cost, scratch);
-  if (first.b < 0) return;
+  if (total == 0 || worker >= share.workers) return;
+  const Found first = find(a.requests, share.bound(worker), cost, [](int32_t) { return int64_t{0}; });
 
   for_segments<M, kSplitBlock>(a, share, first, worker, [&](const Work<M, kSplitBlock>& w, const Segment& g) {
     const Extent& e = w.e;
-    const int64_t r0 = g.tile * M, rows = static_cast<int64_t>(e.n) * a.group;
+    const int32_t r0 = static_cast<int32_t>(g.tile * M), rows = w.rows(a);
     const int64_t blocks = w.blocks(a, g.tile);
-    const int64_t u0 = g.from * blocks / g.cost, u1 = g.to * blocks / g.cost;
+    const int64_t u0 = w.block_at(g.from, blocks, g.cost), u1 = w.block_at(g.to, blocks, g.cost);
     const int64_t near = e.held - e.enc;  // tokens in the window
     Joined<NR> all;
 #pragma unroll
@@ -463,39 +460,39 @@ hlwq_split_attention_kernel(const AttnArgs a) {
         for (int x = 0; x < 4; ++x) all.o[n][k][x] = 0;
       }
     // token (of the step) and q vector of a row of the tile
-    const auto q_row = [&](int64_t row, int32_t& token) {
-      token = static_cast<int32_t>(row / a.group);
-      return a.q + (e.begin + static_cast<int64_t>(token)) * a.q_stride +
-             (static_cast<int64_t>(g.head) * a.group + (row - static_cast<int64_t>(token) * a.group)) * kDim;
+    const auto q_row = [&](int32_t row, int32_t& token) {
+      token = token_of(row, a.group);
+      return a.q + (e.begin + static_cast<int64_t>(token)) * a.q_stride + (g.head * a.group + (row - token * a.group)) * kDim;
     };
 
     if (u0 < w.page_blocks && u0 < u1) {
       const int64_t end = min(u1, w.page_blocks);
-      // pages of the block's sixteens; tokens of it that exist
-      int32_t id[2], next_id[2];
-      const auto pages = [&](int64_t u, int32_t (&p)[2]) {
+      // Pages: lane 2 i + s holds that of sixteen s of the wave's 32 tokens of
+      // block u0 + i, for 32 blocks at a time and the next 32 ahead.
+      const auto pages = [&](int64_t u) {
+        const int64_t t = (u + (lane >> 1)) * kSplitBlock + 32 * wave + 16 * (lane & 1);
+        const int32_t id = t < e.paged ? a.table[static_cast<int64_t>(g.b) * a.width + (t >> a.page_shift)] : -1;
+        return id < a.n_pages ? id : -1;
+      };
+      int32_t ids = pages(u0), ids_ahead = u0 + 32 < end ? pages(u0 + 32) : -1;
+      const auto fetch = [&](int64_t u, Codes<BITS>& to, int (&there)[2]) {
+        const int at = static_cast<int>(u - u0) & 31;
+        if (at == 0 && u > u0) {
+          ids = ids_ahead;
+          if (u + 32 < end) ids_ahead = pages(u + 32);
+        }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int64_t t = u * kSplitBlock + 32 * wave + 16 * s;
-          p[s] = t < e.paged ? a.table[static_cast<int64_t>(g.b) * a.width + (t >> a.page_shift)] : -1;
+          const int32_t id = __builtin_amdgcn_readlane(ids, 2 * at + s);
+          there[s] = id < 0 ? 0 : static_cast<int>(min(e.paged - t, int64_t{16}));
+          const int64_t vec = ((static_cast<int64_t>(max(id, 0)) * a.kv_heads + g.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+          load_codes<BITS>(to, a, s, vec, lane);
         }
       };
-      const auto there = [&](int64_t u, int s, const int32_t (&p)[2]) {
-        const int64_t left = e.paged - (u * kSplitBlock + 32 * wave + 16 * s);
-        return p[s] < 0 || p[s] >= a.n_pages ? 0 : static_cast<int>(min(max(left, int64_t{0}), int64_t{16}));
-      };
-      const auto fetch = [&](int64_t u, const int32_t (&p)[2], Codes<BITS>& to) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int64_t t = u * kSplitBlock + 32 * wave + 16 * s;
-          const int64_t page = p[s] < 0 || p[s] >= a.n_pages ? 0 : p[s];
-          load_codes<BITS>(to, a, s, ((page * a.kv_heads + g.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1)), lane);
-        }
-      };
-      pages(u0, id);
       Codes<BITS> cur, next;
-      fetch(u0, id, cur);
-      if (u0 + 1 < end) pages(u0 + 1, next_id);
+      int there[2], there_next[2] = {0, 0};
+      fetch(u0, cur, there);
 
       // q rotated, each row over a power of two that brings its largest value
       // to [1, 2), as fp16
@@ -539,15 +536,11 @@ hlwq_split_attention_kernel(const AttnArgs a) {
       SplitRows<NR> r;
       clear(r);
       for (int64_t u = u0; u < end; ++u) {
-        const int na = there(u, 0, id), nb = there(u, 1, id);
-        if (u + 1 < end) {
-          fetch(u + 1, next_id, next);
-          id[0] = next_id[0];
-          id[1] = next_id[1];
-          if (u + 2 < end) pages(u + 2, next_id);
-        }
-        if (na + nb > 0) code_step<BITS, NR>(r, q, factor, cur, na, nb, lane);
+        if (u + 1 < end) fetch(u + 1, next, there_next);
+        if (there[0] + there[1] > 0) code_step<BITS, NR>(r, q, factor, cur, there[0], there[1], lane);
         cur = next;
+        there[0] = there_next[0];
+        there[1] = there_next[1];
       }
       join<NR>(all, r, true, lds, lane, wave);
       __syncthreads();
@@ -599,9 +592,8 @@ hlwq_split_attention_kernel(const AttnArgs a) {
         if (r0 + row >= rows) continue;
         if (whole) {
           const float inv = 1.0f / all.l[n][k];
-          const int32_t token = static_cast<int32_t>((r0 + row) / a.group);
-          const int64_t at = (e.begin + static_cast<int64_t>(token)) * a.q_heads + static_cast<int64_t>(g.head) * a.group +
-                             (r0 + row - static_cast<int64_t>(token) * a.group);
+          const int32_t token = token_of(r0 + row, a.group);
+          const int64_t at = (e.begin + static_cast<int64_t>(token)) * a.q_heads + g.head * a.group + (r0 + row - token * a.group);
           *reinterpret_cast<uint2*>(a.out + at * kDim + 4 * lane) =
               uint2{pack_bf16x2(all.o[n][k][0] * inv, all.o[n][k][1] * inv), pack_bf16x2(all.o[n][k][2] * inv, all.o[n][k][3] * inv)};
         } else {
@@ -614,15 +606,17 @@ hlwq_split_attention_kernel(const AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiles that several workgroups shared: a workgroup joins one row of a tile,
-// each wave every fourth partial sum.
+// Tiles that several workgroups shared.  Where tiles are narrow and many
+// workgroups share one (few rows over a long cache), a workgroup joins one row
+// and each wave every fourth partial sum; where they are wide (WAVE_ROWS > 0)
+// a wave joins that many rows by itself.
 // ---------------------------------------------------------------------------
 
-template <int M, int KT, int LEAST>
+template <int M, int KT, int LEAST, int WAVE_ROWS>
 __global__ void __launch_bounds__(kSplitThreads) hlwq_join_attention_kernel(const AttnArgs a) {
+  constexpr int kRows = WAVE_ROWS ? 4 * WAVE_ROWS : 1;  // of a workgroup
   __shared__ __attribute__((aligned(16))) float lds[4 * (kDim + 4)];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t* scratch = reinterpret_cast<int64_t*>(lds);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const auto cost = [&](int32_t b) {
     const Work<M, KT> w(a, b);
     return w.head_cost() * a.kv_heads;
@@ -631,34 +625,27 @@ __global__ void __launch_bounds__(kSplitThreads) hlwq_join_attention_kernel(cons
     const Work<M, KT> w(a, b);
     return w.tiles * a.kv_heads;
   };
-  const Prefix costs = prefix_of<kSplitThreads>(a.requests, cost, scratch);
-  if (costs.total == 0) return;
-  const Prefix pre = prefix_of<kSplitThreads>(a.requests, tiles, scratch);
-  const int64_t x = blockIdx.x / M;
-  const int row = blockIdx.x % M;
-  const Found f = find(pre, x, tiles, scratch);
+  const int64_t total = sum_over(a.requests, cost);
+  if (total == 0) return;
+  const Found f = find(a.requests, blockIdx.x / (M / kRows), tiles, cost);
   if (f.b < 0) return;
-  // the cost before the request, from the thread that holds it
-  if (f.b >= costs.b0 && f.b < costs.b1) {
-    int64_t at = costs.pre;
-    for (int32_t b = costs.b0; b < f.b; ++b) at += cost(b);
-    scratch[0] = at;
-  }
-  __syncthreads();
-  const int64_t before = scratch[0];
-  __syncthreads();
   const Work<M, KT> w(a, f.b);
-  const int32_t head = static_cast<int32_t>(f.rest / w.tiles);
+  const int32_t head = static_cast<int32_t>(quotient(f.rest, w.tiles));
   const int64_t tile = f.rest - head * w.tiles;
-  const int64_t at_row = tile * M + row, rows = static_cast<int64_t>(w.e.n) * a.group;
-  if (at_row >= rows) return;
-  const int64_t x0 = before + head * w.head_cost() + w.cost_before(tile), x1 = x0 + w.cost(tile);
-  const Share share(costs.total, a.workers, LEAST);
+  const int32_t row0 = (blockIdx.x % (M / kRows)) * kRows, r0 = static_cast<int32_t>(tile * M), rows = w.rows(a);
+  if (r0 + row0 >= rows) return;
+  const int64_t x0 = f.also + head * w.head_cost() + w.cost_before(tile), x1 = x0 + w.cost(tile);
+  const Share share(total, a.workers, LEAST);
   const int64_t w0 = share.worker_at(x0), w1 = share.worker_at(x1 - 1);
   if (w0 == w1) return;  // one workgroup did it all
-  float m = -FLT_MAX, l = 0;
-  f32x4 o = {0, 0, 0, 0};
-  for (int64_t k = w0 + wave; k <= w1; k += 4) {
+
+  const auto write = [&](int32_t at_row, f32x4 o, float l) {
+    const float inv = 1.0f / l;
+    const int32_t token = token_of(at_row, a.group);
+    const int64_t at = (w.e.begin + static_cast<int64_t>(token)) * a.q_heads + head * a.group + (at_row - token * a.group);
+    *reinterpret_cast<uint2*>(a.out + at * kDim + 4 * lane) = uint2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+  };
+  const auto add = [&](int64_t k, int row, f32x4& o, float& m, float& l) {
     const int slot = k == w0 ? 1 : 0;
     const float2 s = *partial_stat<M>(a, k, slot, row);
     const f32x4 v = *reinterpret_cast<const f32x4*>(partial_row<M>(a, k, slot, row) + 4 * lane);
@@ -667,30 +654,48 @@ __global__ void __launch_bounds__(kSplitThreads) hlwq_join_attention_kernel(cons
     m = mn;
     l = l * f0 + s.y * f1;
     o = o * f0 + v * f1;
-  }
-  *reinterpret_cast<f32x4*>(lds + wave * (kDim + 4) + 4 * lane) = o;
-  if (lane == 0) {
-    lds[wave * (kDim + 4) + kDim] = m;
-    lds[wave * (kDim + 4) + kDim + 1] = l;
-  }
-  __syncthreads();
-  if (wave != 0) return;
-  float mx = -FLT_MAX;
+  };
+  if constexpr (WAVE_ROWS > 0) {
+    float m[WAVE_ROWS], l[WAVE_ROWS];
+    f32x4 o[WAVE_ROWS];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) mx = fmaxf(mx, lds[k * (kDim + 4) + kDim]);
-  l = 0;
-  o = f32x4{0, 0, 0, 0};
+    for (int i = 0; i < WAVE_ROWS; ++i) {
+      m[i] = -FLT_MAX;
+      l[i] = 0;
+      o[i] = f32x4{0, 0, 0, 0};
+    }
+    const int row = row0 + wave * WAVE_ROWS;
+    for (int64_t k = w0; k <= w1; ++k)
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float g = fast_exp2(lds[k * (kDim + 4) + kDim] - mx);
-    l += lds[k * (kDim + 4) + kDim + 1] * g;
-    o += *reinterpret_cast<const f32x4*>(lds + k * (kDim + 4) + 4 * lane) * g;
+      for (int i = 0; i < WAVE_ROWS; ++i)
+        if (r0 + row + i < rows) add(k, row + i, o[i], m[i], l[i]);
+#pragma unroll
+    for (int i = 0; i < WAVE_ROWS; ++i)
+      if (r0 + row + i < rows) write(r0 + row + i, o[i], l[i]);
+  } else {
+    float m = -FLT_MAX, l = 0;
+    f32x4 o = {0, 0, 0, 0};
+    for (int64_t k = w0 + wave; k <= w1; k += 4) add(k, row0, o, m, l);
+    *reinterpret_cast<f32x4*>(lds + wave * (kDim + 4) + 4 * lane) = o;
+    if (lane == 0) {
+      lds[wave * (kDim + 4) + kDim] = m;
+      lds[wave * (kDim + 4) + kDim + 1] = l;
+    }
+    __syncthreads();
+    if (wave != 0) return;
+    float mx = -FLT_MAX;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, lds[k * (kDim + 4) + kDim]);
+    l = 0;
+    o = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float g = fast_exp2(lds[k * (kDim + 4) + kDim] - mx);
+      l += lds[k * (kDim + 4) + kDim + 1] * g;
+      o += *reinterpret_cast<const f32x4*>(lds + k * (kDim + 4) + 4 * lane) * g;
+    }
+    write(r0 + row0, o, l);
   }
-  const float inv = 1.0f / l;
-  const int32_t token = static_cast<int32_t>(at_row / a.group);
-  const int64_t at = (w.e.begin + static_cast<int64_t>(token)) * a.q_heads + static_cast<int64_t>(head) * a.group +
-                     (at_row - static_cast<int64_t>(token) * a.group);
-  *reinterpret_cast<uint2*>(a.out + at * kDim + 4 * lane) = uint2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
 }
 
 }  // namespace hlwq_kv

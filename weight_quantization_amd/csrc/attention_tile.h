@@ -267,23 +267,19 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
 
   const auto tiles = [&](int32_t b) {
     const RowRange r = row_range(a.cu, b, a.rows);
-    return ceil_div(static_cast<int64_t>(r.end - r.begin) * g, kRows);
+    return ceil_div((r.end - r.begin) * g, kRows);
   };
-  int64_t* scratch = reinterpret_cast<int64_t*>(lds);
-  const Prefix pre = prefix_of<64 * NW>(a.requests, tiles, scratch);
-  const Found f = find(pre, blockIdx.x / a.kv_heads, tiles, scratch);
+  const Found f = find(a.requests, blockIdx.x / a.kv_heads, tiles, [](int32_t) { return int64_t{0}; });
   if (f.b < 0) return;
   const RowRange rr = row_range(a.cu, f.b, a.rows);
-  const int32_t n = rr.end - rr.begin;
-  const int64_t rows = static_cast<int64_t>(n) * g;
-  const int64_t r0 = (tiles(f.b) - 1 - f.rest) * kRows;  // the tile's first row
-  const int64_t w0 = r0 + 32 * wave;                      // the wave's
+  const int32_t n = rr.end - rr.begin, rows = n * g;
+  const int32_t r0 = static_cast<int32_t>(tiles(f.b) - 1 - f.rest) * kRows;  // the tile's first row
+  const int32_t w0 = r0 + 32 * wave;                                          // the wave's
   // tokens of the lane's row, of the wave's first and last, of the tile's last
-  const int64_t row = min(w0 + col, rows - 1);
-  const int32_t tok = static_cast<int32_t>(row / g);
-  const auto q_head = [&]() { return head * static_cast<int64_t>(g) + (min(w0 + col, rows - 1) - static_cast<int64_t>(tok) * g); };
-  const int32_t first = static_cast<int32_t>(min(w0, rows - 1) / g), last = w0 < rows ? static_cast<int32_t>(min(w0 + 31, rows - 1) / g) : -1;
-  const int32_t end = static_cast<int32_t>(min(r0 + kRows - 1, rows - 1) / g) + 1;
+  const int32_t tok = token_of(min(w0 + col, rows - 1), g);
+  const auto q_head = [&]() { return head * g + (min(w0 + col, rows - 1) - tok * g); };
+  const int32_t first = token_of(min(w0, rows - 1), g), last = w0 < rows ? token_of(min(w0 + 31, rows - 1), g) : -1;
+  const int32_t end = token_of(min(r0 + kRows - 1, rows - 1), g) + 1;
 
   u32x4 q[16];
   {
