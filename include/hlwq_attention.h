@@ -26,8 +26,8 @@
  *
  * Values in device arrays that name something out of range (a page id, a slot,
  * a request, a length) never make a call read or write outside the buffers it
- * was given: row ranges are cut to [0, rows), and what the others cause is
- * stated at each call.
+ * was given: row ranges are cut to [0, rows), a prefix sum that falls makes the
+ * attention do nothing, and what the others cause is stated at each call.
  *
  * Layouts (row-major, contiguous unless a stride is given):
  *   packed u8   [n_pages][kv_heads][page_size][32 * bits]

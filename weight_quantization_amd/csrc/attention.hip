@@ -19,11 +19,14 @@ int check_heads(int64_t rows, int64_t q_heads, int64_t kv_heads, bool* nothing) 
   return HLWQ_OK;
 }
 
-// Workgroups of a prompt call with `tile` rows to each: at most one tile more
-// per sequence than whole ones.
+// Tiles of m rows of a call: at most one more per request than whole ones,
+// every tile holding a row.
+int64_t tiles_of(int64_t requests, int64_t rows, int64_t group, int64_t kv_heads, int64_t m) {
+  return std::min(rows * group / m + requests, rows * group) * kv_heads;
+}
+
 int64_t prompt_groups(const AttnArgs& a, int64_t tile) {
-  const int64_t rows = static_cast<int64_t>(a.rows) * a.group;
-  return std::min(rows / tile + a.requests, rows) * a.kv_heads;
+  return tiles_of(a.requests, a.rows, a.group, a.kv_heads, tile);
 }
 
 int launch_prompt(const AttnArgs& a, hipStream_t stream) {
@@ -40,69 +43,89 @@ int launch_prompt(const AttnArgs& a, hipStream_t stream) {
 // goes by the mean: where it is few rows the split kernel takes every request,
 // and a single request goes to one of the two.
 constexpr int64_t kFewRows = 32;
-constexpr int64_t kSplitWorkers = 512, kChunkWorkers = 256;
+// Workgroups that the device holds at once: two to a CU of the split kernel with
+// sixteen rows (256 registers a work-item), else one.
+constexpr int64_t kSplitResident = 512, kChunkWorkers = 256;
 struct PagedPlan {
-  int split_rows;      // rows to a tile of the split kernel; 0: it is not called
-  bool chunk;          // whether the chunk kernel is called
-  int64_t split_workers;
+  int split_rows;         // rows to a tile of the split kernel; 0: it is not called
+  bool chunk;             // whether the chunk kernel is called
+  int64_t split_tiles, split_workers;
+  int64_t split_slots;    // of partial sums
   size_t split_bytes, chunk_bytes;  // of workspace, each its own
 };
-PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t group) {
-  PagedPlan p;
+PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
+  PagedPlan p{};
+  const int64_t group = q_heads / kv_heads;
   p.chunk = rows * group > kFewRows * requests;
   p.split_rows = p.chunk && requests == 1 ? 0 : p.chunk || rows * group > 16 * requests ? 32 : 16;
-  p.split_workers = p.split_rows == 32 ? kSplitWorkers / 2 : kSplitWorkers;
-  p.split_bytes = p.split_rows ? partial_floats(p.split_workers, p.split_rows) * sizeof(float) : 0;
-  p.chunk_bytes = p.chunk ? partial_floats(kChunkWorkers, kChunkRows) * sizeof(float) : 0;
+  if (p.split_rows) {
+    const int64_t resident = p.split_rows == 32 ? kSplitResident / 2 : kSplitResident;
+    p.split_tiles = tiles_of(requests, rows, group, kv_heads, p.split_rows);
+    // all at once where the tiles' own workgroups leave most of the room
+    p.split_workers = resident - std::min(p.split_tiles, resident / 4);
+    p.split_slots = 2 * (p.split_workers + p.split_tiles);
+    p.split_bytes = partial_floats(p.split_slots, p.split_rows) * sizeof(float);
+  }
+  p.chunk_bytes = p.chunk ? partial_floats(2 * kChunkWorkers, kChunkRows) * sizeof(float) : 0;
   return p;
 }
 
 size_t workspace_bytes_of(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
   bool nothing;
   if (requests <= 0 || requests > kMaxRequests || check_heads(rows, q_heads, kv_heads, &nothing) != HLWQ_OK || nothing) return 0;
-  const PagedPlan p = paged_plan(requests, rows, q_heads / kv_heads);
+  const PagedPlan p = paged_plan(requests, rows, q_heads, kv_heads);
   return p.split_bytes + p.chunk_bytes;
 }
 
-// Workgroups that join tiles of m rows, `each` rows to a workgroup: at most one
-// tile more per request than whole ones, every tile holding a row.
-constexpr int kJoinWaveRows = 4;  // of wide tiles
-int64_t join_groups(const AttnArgs& a, int64_t m, int64_t each) {
-  const int64_t rows = static_cast<int64_t>(a.rows) * a.group;
-  return std::min(rows / m + a.requests, rows) * a.kv_heads * (m / each);
+template <int BITS, int NR>
+int launch_split(const AttnArgs& a, int64_t tiles, hipStream_t stream) {
+  const int st = launch(hlwq_split_attention_kernel<BITS, NR>, dim3(static_cast<uint32_t>(a.workers + tiles)), dim3(kSplitThreads), stream, a);
+  if (st != HLWQ_OK) return st;
+  return launch(hlwq_split_join_kernel<16 * NR>, dim3(static_cast<uint32_t>(tiles * 16 * NR)), dim3(kSplitThreads), stream, a);
 }
 
-template <int BITS, int NR>
-int launch_split(const AttnArgs& a, hipStream_t stream) {
-  const int st = launch(hlwq_split_attention_kernel<BITS, NR>, dim3(static_cast<uint32_t>(a.workers)), dim3(kSplitThreads), stream, a);
-  if (st != HLWQ_OK) return st;
-  return launch(hlwq_join_attention_kernel<16 * NR, kSplitBlock, kSplitLeast, 0>, dim3(static_cast<uint32_t>(join_groups(a, 16 * NR, 1))),
-                dim3(kSplitThreads), stream, a);
+// The shift that keeps the sum of the costs of tiles of m rows and blocks of kt
+// tokens below 2^31 (Work): 0 unless millions of tiles meet millions of tokens.
+int32_t cost_shift_of(const AttnArgs& a, int64_t m, int64_t kt) {
+  const int64_t rows = static_cast<int64_t>(a.rows) * a.group;
+  const double tiles = static_cast<double>(std::min(rows / m + a.requests, rows)) * a.kv_heads;
+  const double blocks = (static_cast<double>(static_cast<int64_t>(a.width) << a.page_shift) + a.n_res + a.rows) / kt + 4;
+  const double grow = (kBlockCost * m / kt / a.group + 1.0) * (rows / m + 1);
+  if (tiles * (blocks * kBlockCost + grow) < 0x1p30) return 0;
+  int32_t shift = 1;
+  while (tiles * (blocks / (1 << shift) + 2) > 0x1p30 && shift < 30) ++shift;
+  return shift;
 }
 
 int launch_paged(int bits, AttnArgs a, void* ws, hipStream_t stream) {
-  const PagedPlan p = paged_plan(a.requests, a.rows, a.group);
-  if ((p.split_rows && join_groups(a, p.split_rows, 1) > 0xffffff) || (p.chunk && join_groups(a, kChunkRows, 4 * kJoinWaveRows) > 0xffffff))
+  const PagedPlan p = paged_plan(a.requests, a.rows, a.q_heads, a.kv_heads);
+  const int64_t chunk_groups = tiles_of(a.requests, a.rows, a.group, a.kv_heads, kChunkRows) * (kChunkRows / kChunkJoinRows);
+  // the launches' sizes, and the split kernel's count of blocks
+  const int64_t table_blocks = ceil_div(static_cast<int64_t>(a.width) << a.page_shift, kSplitBlock);
+  if (p.split_tiles * p.split_rows > 0xffffff || p.split_tiles * table_blocks > 0x7fffffff || (p.chunk && chunk_groups > 0xffffff))
     return HLWQ_ERR_LIMIT;
+  a.most = 0x7fffffff;
   if (p.split_rows) {
     a.partial = static_cast<float*>(ws);
     a.workers = static_cast<int32_t>(p.split_workers);
+    a.slots = static_cast<int32_t>(p.split_slots);
     a.least = 1;
-    a.most = p.chunk ? kFewRows : 0x7fffffff;
-    const int st = p.split_rows == 16 ? (bits == 3 ? launch_split<3, 1>(a, stream) : launch_split<2, 1>(a, stream))
-                                      : (bits == 3 ? launch_split<3, 2>(a, stream) : launch_split<2, 2>(a, stream));
-    if (st != HLWQ_OK) return st;
+    if (p.chunk) a.most = kFewRows;
+    const int st = p.split_rows == 16
+                       ? (bits == 3 ? launch_split<3, 1>(a, p.split_tiles, stream) : launch_split<2, 1>(a, p.split_tiles, stream))
+                       : (bits == 3 ? launch_split<3, 2>(a, p.split_tiles, stream) : launch_split<2, 2>(a, p.split_tiles, stream));
+    if (st != HLWQ_OK || !p.chunk) return st;
+    a.most = 0x7fffffff;
   }
-  if (!p.chunk) return HLWQ_OK;
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.split_bytes);
   a.workers = kChunkWorkers;
+  a.slots = 2 * kChunkWorkers;
+  a.cost_shift = cost_shift_of(a, kChunkRows, kChunkBlock);
   a.least = p.split_rows ? kFewRows + 1 : 1;
-  a.most = 0x7fffffff;
   const int st = launch(bits == 3 ? hlwq_chunk_attention_kernel<3> : hlwq_chunk_attention_kernel<2>,
                         dim3(static_cast<uint32_t>(a.workers)), dim3(512), stream, a);
   if (st != HLWQ_OK) return st;
-  return launch(hlwq_join_attention_kernel<kChunkRows, kChunkBlock, kChunkLeast, kJoinWaveRows>,
-                dim3(static_cast<uint32_t>(join_groups(a, kChunkRows, 4 * kJoinWaveRows))), dim3(kSplitThreads), stream, a);
+  return launch(hlwq_chunk_join_kernel, dim3(static_cast<uint32_t>(chunk_groups)), dim3(256), stream, a);
 }
 
 int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q_heads, const void* k, int64_t k_stride,

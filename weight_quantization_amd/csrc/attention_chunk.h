@@ -15,7 +15,7 @@ namespace hlwq_kv {
 
 constexpr int kChunkRows = 256;
 constexpr int kChunkBlock = 64;   // tokens to a block
-constexpr int kChunkLeast = 4;    // blocks that are worth a workgroup of their own
+constexpr int kChunkLeast = 4 * kBlockCost;  // cost that is worth a workgroup of its own
 
 // Butterflies over the 256 values of a row whose lanes hold 128 each, v[x] of
 // the lower half and of the upper half differing in one bit of their index,
@@ -83,23 +83,20 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
   const TileLane at = tile_lane(lane);
 
-  const auto cost = [&](int32_t b) {
-    const Work<M, KT> w(a, b);
-    return w.head_cost() * a.kv_heads;
-  };
-  const int64_t total = sum_over(a.requests, cost);
-  const Share share(total, a.workers, kChunkLeast);
-  if (total == 0 || blockIdx.x >= share.workers) return;
+  const auto cost = [&](const Extent& e) { return Work<M, KT>(a, e).head_cost() * a.kv_heads; };
+  Finder<decltype(cost), Nothing> finder(a, cost, Nothing{});
+  const Share share(finder.total, a.workers, kChunkLeast);
+  if (finder.total == 0 || blockIdx.x >= share.workers) return;
   // Workgroups of one XCD (every eighth) take neighbouring stretches, which
   // share a KV head's keys in its L2.
-  const int64_t worker = share.workers % 8 == 0 ? (blockIdx.x % 8) * (share.workers / 8) + blockIdx.x / 8 : blockIdx.x;
-  const Found first = find(a.requests, share.bound(worker), cost, [](int32_t) { return int64_t{0}; });
+  const int32_t worker = share.workers % 8 == 0 ? (blockIdx.x % 8) * (share.workers / 8) + blockIdx.x / 8 : blockIdx.x;
+  const Found first = finder.find(share.bound(worker));
 
   for_segments<M, KT>(a, share, first, worker, [&](const Work<M, KT>& w, const Segment& g) {
     const Extent& e = w.e;
-    const int32_t rows = w.rows(a), w0 = static_cast<int32_t>(g.tile * M) + 32 * wave;
-    const int64_t blocks = w.blocks(a, g.tile);
-    const int64_t u0 = w.block_at(g.from, blocks, g.cost), u1 = w.block_at(g.to, blocks, g.cost);
+    const int32_t rows = w.rows(a), w0 = g.tile * M + 32 * wave;
+    const int32_t blocks = w.blocks(a, g.tile);
+    const int32_t u0 = w.block_at(g.from, blocks, g.cost), u1 = w.block_at(g.to, blocks, g.cost);
     const int64_t near = e.held - e.enc;
     const int32_t tok = token_of(min(w0 + col, rows - 1), a.group);
     const auto q_head = [&]() { return g.head * a.group + (min(w0 + col, rows - 1) - tok * a.group); };
@@ -163,9 +160,7 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
         if (wave == 1) {
           // as in code_step: norms over a power of two that none met so far exceeds
           const float n = there ? f16_value(norm) : 0.0f;
-          float top = n;
-#pragma unroll
-          for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, lane_xor(top, d));
+          const float top = wave_max(n);
           if (top > __builtin_ldexpf(1.0f, exponent)) exponent = __builtin_amdgcn_frexp_expf(top);
           *reinterpret_cast<lds_f32*>(static_cast<uintptr_t>(side + 4 * KT + 4 * lane)) = __builtin_ldexpf(n, -exponent);
           if (lane == 0) *reinterpret_cast<lds_u32*>(static_cast<uintptr_t>(side + 8 * KT + 4)) = exponent;
@@ -253,26 +248,15 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
       const int64_t first_key = near + token_of(min(w0, rows - 1), a.group);               // the last that the wave's first row sees
       const int64_t last_key = idle ? -1 : near + token_of(min(w0 + 31, rows - 1), a.group);  // and its last
       const int64_t end_key = near + w.last_token(a, g.tile);                      // and the tile's last
-      const int64_t ring0 = a.ring > 0 ? e.enc % a.ring : 0;
-      const auto row = [&](int side, int64_t k) {
-        const uint16_t* p;
-        if (k < near) {
-          int64_t slot = ring0 + k;
-          if (slot >= a.ring) slot -= a.ring;
-          p = (side ? a.v_window : a.k_window) + ((static_cast<int64_t>(g.b) * a.kv_heads + g.head) * a.ring + slot) * kDim;
-        } else {
-          p = (side ? a.v_new : a.k_new) + (e.begin + (k - near)) * (side ? a.v_stride : a.k_stride) + g.head * kDim;
-        }
-        return p;
-      };
+      const Tokens tokens(a, e, g.b, g.head);
       const auto stage = [&](int buf, int64_t t0) {
 #pragma unroll
         for (int i = 0; i < KT / 16; ++i) {
           const int pair = 16 * i + 2 * wave;
           const int64_t k = min(t0 + pair + h, end_key);  // past the end the last one again, which nobody sees there
           const uint32_t c = (col ^ swizzle(2 * wave + h)) * 8;
-          stage16(row(0, k) + c, base + buf * kStage + pair * 512);
-          stage16(row(1, k) + c, base + buf * kStage + KT * 512 + pair * 512);
+          stage16(tokens.at(0, k) + c, base + buf * kStage + pair * 512);
+          stage16(tokens.at(1, k) + c, base + buf * kStage + KT * 512 + pair * 512);
         }
       };
       u32x4 q[16];
@@ -300,7 +284,7 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
         }
       }
       add_nonfinite(r, max((first_key + 1) / 32 * 32, from * KT), min(last_key, to * KT - 1), near + tok, h,
-                    [&](int64_t key) { return row(1, key); });
+                    [&](int64_t key) { return tokens.at(1, key); });
       barrier();
     }
 
@@ -319,16 +303,61 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
           }
       } else {
         const int slot = g.from > 0 ? 0 : 1, at_row = 32 * wave + col;
-        float* op = partial_row<M>(a, worker, slot, at_row);
+        float* op = partial_row<M>(a, 2 * worker + slot, at_row);
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<f32x4*>(op + 32 * t + 8 * i + 4 * h) = f32x4{r.o[t][4 * i], r.o[t][4 * i + 1], r.o[t][4 * i + 2], r.o[t][4 * i + 3]};
-        if (h == 0) *partial_stat<M>(a, worker, slot, at_row) = float2{r.m, r.l};
+        if (h == 0) *partial_stat<M>(a, 2 * worker + slot, at_row) = float2{r.m, r.l};
       }
     }
   });
+}
+
+// Joins the tiles that several workgroups shared, four rows to a wave.
+constexpr int kChunkJoinRows = 16;  // of a workgroup
+__global__ void __launch_bounds__(256) hlwq_chunk_join_kernel(const AttnArgs a) {
+  constexpr int M = kChunkRows, KT = kChunkBlock;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const auto cost = [&](const Extent& e) { return Work<M, KT>(a, e).head_cost() * a.kv_heads; };
+  const auto tiles = [&](const Extent& e) { return Work<M, KT>(a, e).tiles * a.kv_heads; };
+  Finder<decltype(tiles), decltype(cost)> finder(a, tiles, cost);
+  const int32_t x = blockIdx.x / (M / kChunkJoinRows);
+  if (x >= finder.total) return;
+  const Found f = finder.find(x);
+  const Work<M, KT> w(a, f.e);
+  const int32_t head = quotient(f.rest, w.tiles), tile = f.rest - head * w.tiles;
+  const int32_t row0 = (blockIdx.x % (M / kChunkJoinRows)) * kChunkJoinRows + 4 * wave, rows = w.rows(a) - tile * M;
+  if (row0 >= rows) return;
+  const int32_t x0 = f.before + head * w.head_cost() + w.cost_before(tile), x1 = x0 + w.cost(tile);
+  const Share share(Finder<decltype(cost), Nothing>(a, cost, Nothing{}).total, a.workers, kChunkLeast);
+  const int32_t w0 = share.worker_at(x0), w1 = share.worker_at(x1 - 1);
+  if (w0 == w1) return;  // one workgroup did it all
+  float m[4], l[4];
+  f32x4 o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -FLT_MAX;
+    l[i] = 0;
+    o[i] = f32x4{0, 0, 0, 0};
+  }
+  for (int32_t k = w0; k <= w1; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (row0 + i >= rows) continue;
+      const int32_t slot = 2 * k + (k == w0 ? 1 : 0);
+      const float2 s = *partial_stat<M>(a, slot, row0 + i);
+      const f32x4 v = *reinterpret_cast<const f32x4*>(partial_row<M>(a, slot, row0 + i) + 4 * lane);
+      const float mn = fmaxf(m[i], s.x);
+      const float f0 = fast_exp2(m[i] - mn), f1 = fast_exp2(s.x - mn);
+      m[i] = mn;
+      l[i] = l[i] * f0 + s.y * f1;
+      o[i] = o[i] * f0 + v * f1;
+    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (row0 + i < rows) write_row(a, w.e.begin, head, tile * M + row0 + i, o[i], l[i], lane);
 }
 
 }  // namespace hlwq_kv

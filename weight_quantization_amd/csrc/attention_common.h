@@ -50,7 +50,9 @@ struct AttnArgs {
   int64_t n_res, ring;
   int32_t requests, rows, q_heads, kv_heads, group, n_pages, page_shift, width;
   int32_t workers;  // workgroups that share the work
+  int32_t slots;    // of partial sums
   int32_t least, most;  // requests with rows * group in [least, most] are this kernel's
+  int32_t cost_shift;
   float scale;
 };
 
@@ -60,15 +62,18 @@ struct Extent {
   int64_t held, enc;  // tokens before the step, those of them encoded
   int64_t paged;      // encoded tokens that have a table entry
 };
-__device__ __forceinline__ Extent extent_of(const AttnArgs& a, int32_t b) {
+__device__ __forceinline__ Extent extent_of(const AttnArgs& a, int32_t begin, int32_t n, int32_t len) {
   Extent e;
-  const RowRange r = row_range(a.cu, b, a.rows);
-  e.begin = r.begin;
-  e.n = r.end - r.begin;
-  e.held = a.lens ? max(static_cast<int64_t>(a.lens[b]) - e.n, int64_t{0}) : 0;
+  e.begin = begin;
+  e.n = n;
+  e.held = max(len - n, 0);
   e.enc = a.lens ? max(e.held - a.n_res, int64_t{0}) : 0;
   e.paged = a.n_pages > 0 ? min(e.enc, static_cast<int64_t>(a.width) << a.page_shift) : 0;
   return e;
+}
+__device__ __forceinline__ Extent extent_of(const AttnArgs& a, int32_t b) {
+  const RowRange r = row_range(a.cu, b, a.rows);
+  return extent_of(a, r.begin, r.end - r.begin, a.lens ? a.lens[b] : 0);
 }
 
 // The token that row r of a request belongs to.
@@ -78,11 +83,7 @@ __device__ __forceinline__ int32_t token_of(int32_t r, int32_t group) {
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Value of lane l ^ 32.
-__device__ __forceinline__ float half_swap(float v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
-}
+__device__ __forceinline__ float half_swap(float v) { return lane_xor(v, 32); }
 
 // Two floats rounded to a pair of fp16, to nearest.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -133,66 +134,76 @@ __device__ __forceinline__ u32x2 look_up(uint32_t c) {
 // ---------------------------------------------------------------------------
 // Finding work.  The requests' lengths are on the device, so every wave sums
 // what the requests ask for and finds its workgroup's share of it, without
-// LDS or a barrier: lane i takes requests i, i + 64, ..
+// LDS or a barrier: lane i takes requests i, i + 64, ..  Sums stay below 2^31
+// (cost_shift), as 64-bit divisions cost hundreds of instructions.
 // ---------------------------------------------------------------------------
 
-// a / b for a, b >= 0, in 32 bits where they fit (64 take ten times as long).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(v) >> 32));
-  return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
-}
-
-// The sum of a quantity over the requests.
-template <class F>
-__device__ __forceinline__ int64_t sum_over(int32_t requests, F of) {
-  int64_t v = 0;
-  for (int32_t b = threadIdx.x & 63; b < requests; b += 64) v += of(b);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  return uniform64(v);
-}
-
-// The request that holds unit x of the quantity (0 <= x < its sum), x's place
-// in it, and the sum of `also` over the requests before it.
+// A quantity of each request, its sum, and the request that holds a place of
+// it.  (Of up to 64 requests everything stays in registers between the two.)
 struct Found {
   int32_t b;
-  int64_t rest, also;
+  int32_t rest, before;  // the place's within the request, the sum of `other` over the requests before it
+  Extent e;              // of the request
 };
 template <class F, class G>
-__device__ __forceinline__ Found find(int32_t requests, int64_t x, F of, G also) {
-  const int lane = threadIdx.x & 63;
-  Found f{0, 0, 0};
-  for (int32_t b0 = 0; b0 < requests; b0 += 64) {
-    const bool in = b0 + lane < requests;
-    const int64_t own = in ? of(b0 + lane) : 0, other = in ? also(b0 + lane) : 0;
-    int64_t v = own, w = other;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t p = __shfl_up(v, d, 64), q = __shfl_up(w, d, 64);
-      if (lane >= d) {
-        v += p;
-        w += q;
-      }
+struct Finder {
+  F of;
+  G other;
+  int32_t requests;
+  int32_t own, prefix, total;
+  Extent mine;
+  const AttnArgs& args;
+  __device__ __forceinline__ Finder(const AttnArgs& a, F f, G g) : of(f), other(g), requests(a.requests), args(a) {
+    const int lane = threadIdx.x & 63;
+    total = 0;
+    bool falls = false;
+    for (int32_t b0 = 0; b0 < requests; b0 += 64) {
+      const int32_t b = min(b0 + lane, requests - 1);
+      mine = extent_of(a, b);
+      own = b0 + lane < requests ? of(mine) : 0;
+      falls |= a.cu[b + 1] < a.cu[b];
+      prefix = wave_scan(own);
+      total += __builtin_amdgcn_readlane(prefix, 63);
     }
-    const uint64_t past = __ballot(x < v);
-    if (past) {
-      const int at = __builtin_ctzll(past);
-      f.b = b0 + at;
-      f.rest = uniform64(x - __shfl(v - own, at, 64));
-      f.also += uniform64(__shfl(w - other, at, 64));
-      return f;
-    }
-    x -= uniform64(__shfl(v, 63, 64));
-    f.also += uniform64(__shfl(w, 63, 64));
+    // where cu falls, rows could belong to several requests and the sums pass
+    // what the host has allowed for: such a call does nothing
+    if (__any(falls)) total = 0;
   }
-  f.b = -1;
-  return f;
+  // place x, 0 <= x < total
+  __device__ __forceinline__ Found find(int32_t x) {
+    const int lane = threadIdx.x & 63;
+    Found f{-1, 0, 0, {}};
+    for (int32_t b0 = 0; b0 < requests; b0 += 64) {
+      const bool in = b0 + lane < requests;
+      if (requests > 64) {
+        mine = extent_of(args, min(b0 + lane, requests - 1));
+        own = in ? of(mine) : 0;
+        prefix = wave_scan(own);
+      }
+      const int32_t aside = wave_scan(in ? other(mine) : 0);
+      const uint64_t past = __ballot(x < prefix);
+      if (past) {
+        const int at = __builtin_ctzll(past);
+        f.b = b0 + at;
+        f.rest = x - __builtin_amdgcn_readlane(prefix - own, at);
+        if (at > 0) f.before += __builtin_amdgcn_readlane(aside, at - 1);
+        f.e = extent_of(args, __builtin_amdgcn_readlane(mine.begin, at), __builtin_amdgcn_readlane(mine.n, at),
+                        static_cast<int32_t>(__builtin_amdgcn_readlane(static_cast<int32_t>(mine.held), at)) +
+                            __builtin_amdgcn_readlane(mine.n, at));
+        return f;
+      }
+      x -= __builtin_amdgcn_readlane(prefix, 63);
+      f.before += __builtin_amdgcn_readlane(aside, 63);
+    }
+    return f;
+  }
+};
+struct Nothing {
+  __device__ __forceinline__ int32_t operator()(const Extent&) const { return 0; }
+};
+
+__device__ __forceinline__ int32_t quotient(int32_t a, int32_t b) {
+  return static_cast<int32_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
 }
 
 // How the paged kernels share their work out.  A tile is M consecutive rows of
@@ -201,107 +212,123 @@ __device__ __forceinline__ Found find(int32_t requests, int64_t x, F of, G also)
 // tile's last row.  The tiles lie one after the other, by request, KV head and
 // row, and every workgroup takes an equal stretch of their cost, so that
 // requests of any lengths load the workgroups alike; a tile that several
-// workgroups share is joined from their partial sums afterwards.
+// workgroups share is joined from their partial sums afterwards.  (The cost
+// need only be near the blocks' number: it is counted in eighths of one, so
+// that it grows by as little as a tile's tokens do, or, where its sum could pass
+// 2^31, in units of 2^cost_shift blocks.)
+constexpr int32_t kBlockCost = 8;
 template <int M, int KT>
 struct Work {
   Extent e;
-  int64_t tiles, base, step, page_blocks;
-  __device__ __forceinline__ Work(const AttnArgs& a, int32_t b) {
-    e = extent_of(a, b);
-    const int32_t rows = e.n * a.group;
-    tiles = rows >= a.least && rows <= a.most ? ceil_div(rows, M) : 0;
-    page_blocks = ceil_div(e.paged, KT);
-    base = page_blocks + ceil_div(e.held - e.enc + 1, KT);
-    // at least the blocks by which a tile's tokens pass those of the one before
-    step = M <= KT ? 1 : (static_cast<uint32_t>(M - 1) / static_cast<uint32_t>(a.group) + KT) / KT;
+  int32_t tiles, page_blocks, base, step;
+  __device__ __forceinline__ Work(const AttnArgs& a, const Extent& x) {
+    e = x;
+    const int32_t r = rows(a);
+    tiles = r >= a.least && r <= a.most ? static_cast<int32_t>(ceil_div(r, M)) : 0;
+    page_blocks = static_cast<int32_t>(ceil_div(e.paged, KT));
+    base = page_blocks + static_cast<int32_t>(ceil_div(e.held - e.enc + 1, KT));
+    if (a.cost_shift) {
+      base = (base >> a.cost_shift) + 1;
+      step = 0;
+    } else {
+      base *= kBlockCost;
+      step = quotient(kBlockCost * M / KT, a.group) + 1;  // what a tile's tokens come to, rounded up
+    }
   }
   // of one KV head
-  __device__ __forceinline__ int64_t cost_before(int64_t j) const { return j * base + step * (j * (j - 1) / 2); }
-  __device__ __forceinline__ int64_t cost(int64_t j) const { return base + step * j; }
-  __device__ __forceinline__ int64_t head_cost() const { return cost_before(tiles); }
-  // the tile that holds place x of a KV head's cost
-  __device__ __forceinline__ int64_t tile_at(int64_t x) const {
+  __device__ __forceinline__ int32_t cost_before(int32_t j) const { return j * base + step * (j * (j - 1) / 2); }
+  __device__ __forceinline__ int32_t cost(int32_t j) const { return base + step * j; }
+  __device__ __forceinline__ int32_t head_cost() const { return cost_before(tiles); }
+  // the tile that holds place x of a KV head's cost: from an estimate of the
+  // root of cost_before(j) = x
+  __device__ __forceinline__ int32_t tile_at(int32_t x) const {
     if (tiles == 1) return 0;
-    const double b = 2.0 * base - step, s = step;
-    int64_t j = static_cast<int64_t>((sqrt(b * b + 8.0 * s * x) - b) / (2.0 * s));
-    j = max(min(j, tiles - 1), int64_t{0});
+    const float b = 2.0f * base - step, s = step;
+    int32_t j = step ? static_cast<int32_t>((__builtin_amdgcn_sqrtf(b * b + 8.0f * s * x) - b) * 0.5f * __builtin_amdgcn_rcpf(s))
+                     : quotient(x, base);
+    j = max(min(j, tiles - 1), 0);
     while (j > 0 && cost_before(j) > x) --j;
     while (j + 1 < tiles && cost_before(j + 1) <= x) ++j;
     return j;
   }
   __device__ __forceinline__ int32_t rows(const AttnArgs& a) const { return e.n * a.group; }
   // tokens (of the step) of the tile's first row and last row
-  __device__ __forceinline__ int32_t first_token(const AttnArgs& a, int64_t j) const {
-    return static_cast<uint32_t>(j * M) / static_cast<uint32_t>(a.group);
-  }
-  __device__ __forceinline__ int32_t last_token(const AttnArgs& a, int64_t j) const {
-    return static_cast<uint32_t>(min((j + 1) * M, static_cast<int64_t>(rows(a))) - 1) / static_cast<uint32_t>(a.group);
+  __device__ __forceinline__ int32_t first_token(const AttnArgs& a, int32_t j) const { return token_of(j * M, a.group); }
+  __device__ __forceinline__ int32_t last_token(const AttnArgs& a, int32_t j) const {
+    return token_of(min(M, rows(a) - j * M) + j * M - 1, a.group);
   }
   // key blocks of tile j: the pages', then the others
-  __device__ __forceinline__ int64_t blocks(const AttnArgs& a, int64_t j) const {
-    return page_blocks + ceil_div(e.held - e.enc + last_token(a, j) + 1, KT);
+  __device__ __forceinline__ int32_t blocks(const AttnArgs& a, int32_t j) const {
+    return page_blocks + static_cast<int32_t>(ceil_div(e.held - e.enc + last_token(a, j) + 1, KT));
   }
   // the block at place x of a tile's cost: its blocks spread evenly over it
-  __device__ __forceinline__ static int64_t block_at(int64_t x, int64_t blocks, int64_t cost) {
-    return blocks == cost ? x : quotient(x * blocks, cost);
+  __device__ __forceinline__ static int32_t block_at(int32_t x, int32_t blocks, int32_t cost) {
+    if (cost == blocks * kBlockCost) return x / kBlockCost;
+    if (x == cost) return blocks;
+    return static_cast<int32_t>(static_cast<double>(x) * blocks / cost);
   }
 };
 
 // The stretches: worker w of `workers` takes cost [bound(w), bound(w + 1)),
 // the first `more` one unit more than the others.  Fewer workgroups than there
-// are share a small total, at least least_blocks to each.
+// are share a small total, at least the cost `least` to each.
 struct Share {
-  int64_t workers, each, more;
-  __device__ __forceinline__ Share(int64_t total, int64_t most, int64_t least_blocks) {
-    workers = max(min(most, total / least_blocks), int64_t{1});
+  int32_t workers, each, more;
+  __device__ __forceinline__ Share(int32_t total, int32_t most, int32_t least) {
+    workers = max(min(most, total / least), 1);
     each = quotient(total, workers);
     more = total - each * workers;
   }
-  __device__ __forceinline__ int64_t bound(int64_t w) const { return w * each + min(w, more); }
+  __device__ __forceinline__ int32_t bound(int32_t w) const { return w * each + min(w, more); }
   // the worker whose stretch holds x
-  __device__ __forceinline__ int64_t worker_at(int64_t x) const {
-    const int64_t cut = more * (each + 1);
+  __device__ __forceinline__ int32_t worker_at(int32_t x) const {
+    const int32_t cut = more * (each + 1);
     return x < cut ? quotient(x, each + 1) : more + quotient(x - cut, each);
   }
 };
 
-// A worker's partial sums of a tile: slot 0 if its stretch begins inside the
-// tile, 1 if it begins with or before it.  M rows of 256 floats to a slot, then for
-// all slots the rows' maxima and sums.
+// Partial sums lie in slots of M rows of 256 floats, followed for all slots by
+// the rows' maxima and sums.  Worker w has slot 2 w for a stretch that begins
+// inside a tile and 2 w + 1 for one that begins with the tile and ends inside it.
 template <int M>
-__device__ __forceinline__ float* partial_row(const AttnArgs& a, int64_t worker, int slot, int row) {
-  return a.partial + ((worker * 2 + slot) * M + row) * kDim;
+__device__ __forceinline__ float* partial_row(const AttnArgs& a, int32_t slot, int row) {
+  return a.partial + (slot * static_cast<int64_t>(M) + row) * kDim;
 }
 template <int M>
-__device__ __forceinline__ float2* partial_stat(const AttnArgs& a, int64_t worker, int slot, int row) {
-  return reinterpret_cast<float2*>(a.partial + static_cast<int64_t>(a.workers) * 2 * M * kDim) + (worker * 2 + slot) * M + row;
+__device__ __forceinline__ float2* partial_stat(const AttnArgs& a, int32_t slot, int row) {
+  return reinterpret_cast<float2*>(a.partial + static_cast<int64_t>(a.slots) * M * kDim) + slot * static_cast<int64_t>(M) + row;
 }
-constexpr int64_t partial_floats(int64_t workers, int64_t m) { return workers * 2 * m * (kDim + 2); }
+constexpr int64_t partial_floats(int64_t slots, int64_t m) { return slots * m * (kDim + 2); }
 
 // One worker's segments, one after the other.
 struct Segment {
   int32_t b, head;
-  int64_t tile, from, to, cost;  // places [from, to) of the tile's cost
+  int32_t tile, from, to, cost;  // places [from, to) of the tile's cost
 };
 template <int M, int KT, class F>
-__device__ __forceinline__ void for_segments(const AttnArgs& a, const Share& s, const Found& first, int64_t worker, F run) {
-  int64_t left = s.bound(worker + 1) - s.bound(worker);
-  int64_t rest = first.rest;
-  for (int32_t b = first.b; left > 0 && b < a.requests; ++b, rest = 0) {
-    const Work<M, KT> w(a, b);
-    if (w.tiles == 0) continue;
-    const int64_t head_cost = w.head_cost();
-    int32_t head = static_cast<int32_t>(quotient(rest, head_cost));
-    rest -= head * head_cost;
-    for (; head < a.kv_heads && left > 0; ++head, rest = 0) {
-      int64_t j = w.tile_at(rest);
-      rest -= w.cost_before(j);
-      for (; j < w.tiles && left > 0; ++j, rest = 0) {
-        Segment g{b, head, j, rest, min(rest + left, w.cost(j)), w.cost(j)};
-        left -= g.to - g.from;
-        run(w, g);
-      }
+__device__ __forceinline__ void for_segments(const AttnArgs& a, const Share& s, const Found& first, int32_t worker, F run) {
+  int32_t left = s.bound(worker + 1) - s.bound(worker);
+  int32_t b = first.b, rest = first.rest;
+#pragma clang loop unroll(disable)
+  while (left > 0 && b < a.requests) {
+    const Work<M, KT> w(a, b == first.b ? first.e : extent_of(a, b));
+    const int32_t head_cost = w.head_cost();
+    Segment g;
+    g.b = b;
+    g.head = head_cost ? quotient(rest, head_cost) : a.kv_heads;
+    if (g.head >= a.kv_heads) {  // past the request's last
+      ++b;
+      rest = 0;
+      continue;
     }
+    const int32_t x = rest - g.head * head_cost;
+    g.tile = w.tile_at(x);
+    g.cost = w.cost(g.tile);
+    g.from = x - w.cost_before(g.tile);
+    g.to = min(g.from + left, g.cost);
+    left -= g.to - g.from;
+    rest += g.to - g.from;
+    run(w, g);
   }
 }
 

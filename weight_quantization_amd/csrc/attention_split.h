@@ -14,8 +14,13 @@
 //     operands take the order the bytes come in, and q is laid out to match.
 //   - q is rotated once: q . H c = (H q) . c; the sum over tokens of p n c is
 //     rotated once at the end.
-// A workgroup is four waves with 32 tokens each to a block of 128; sums are
-// joined over the waves in LDS, and over workgroups in the workspace.
+// A workgroup is four waves with 32 tokens each to a block of 128.  Some
+// workgroups share the pages' blocks of all requests in equal stretches, one
+// more per tile (sixteen or 32 rows of a KV head) takes the window's and the
+// step's own tokens; each joins its waves' sums in LDS and leaves them in the
+// workspace, and a second kernel joins a tile's.  A workgroup runs through its
+// code once or twice, so what bounds a short call is the fetching of
+// instructions: what is not in the loop over blocks is kept small, not unrolled.
 #pragma once
 
 #include "attention_common.h"
@@ -28,7 +33,6 @@ typedef uint32_t u32x3_4 __attribute__((ext_vector_type(3), aligned(4)));
 constexpr int kSplitThreads = 256;
 constexpr int kSplitBlock = 128;  // tokens to a block
 constexpr int kSplitPitch = kDim + 4;  // floats to a row of sums in LDS: rows 4 banks apart
-constexpr int kSplitLeast = 1;    // blocks that are worth a workgroup of their own
 
 // Eight code registers, code i of four 3-byte groups each, from the groups'
 // first, second and third bytes.
@@ -302,27 +306,68 @@ __device__ __forceinline__ void code_step(SplitRows<NR>& r, const u32x4 (&q)[NR]
   }
 }
 
-// 32 bf16 tokens from k0 on; row(side, k): token k's vector; lim[n]: last
-// token that the lane's row of set n sees; last: the last one there is.
-template <int NR, class F>
+// Where the window's and the step's tokens of a KV head lie, K and V: token k
+// below `near` in ring slot ring0 + k (mod ring), the others in the step's rows.
+struct Tokens {
+  const uint16_t *window[2], *rows[2];
+  uint32_t stride[2];  // of the rows; the window's is kDim
+  int64_t near, ring0, ring;
+  __device__ __forceinline__ Tokens(const AttnArgs& a, const Extent& e, int32_t b, int32_t head) {
+    const int64_t w = (static_cast<int64_t>(b) * a.kv_heads + head) * a.ring * kDim;
+    window[0] = a.k_window + w;
+    window[1] = a.v_window + w;
+    stride[0] = static_cast<uint32_t>(a.k_stride);
+    stride[1] = static_cast<uint32_t>(a.v_stride);
+    rows[0] = a.k_new + e.begin * a.k_stride + head * kDim;
+    rows[1] = a.v_new + e.begin * a.v_stride + head * kDim;
+    near = e.held - e.enc;
+    ring = a.ring;
+    ring0 = near > 0 ? static_cast<uint32_t>(e.enc) % static_cast<uint32_t>(a.ring) : 0;  // both below 2^31
+  }
+  // Token k's vector: selects and one multiply, no branch, so that loads of
+  // several tokens are in flight together.
+  __device__ __forceinline__ const uint16_t* at(int side, int64_t k) const {
+    const bool in = k < near;
+    const int64_t slot = ring0 + k >= ring ? ring0 + k - ring : ring0 + k;
+    const uint32_t index = static_cast<uint32_t>(in ? slot : k - near);
+    return (in ? window[side] : rows[side]) + static_cast<uint64_t>(index) * (in ? static_cast<uint32_t>(kDim) : stride[side]);
+  }
+};
+
+// 32 bf16 tokens from k0 on; lim[n]: last token that the lane's row of set n
+// sees; last: the last one there is.
+template <int NR>
 __device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR][8], float factor, int64_t k0, int64_t last,
-                                           const int64_t (&lim)[NR], bool masked, F row, int lane) {
+                                           const int64_t (&lim)[NR], bool masked, const Tokens& tokens, int lane) {
   const int c = lane & 15, h4 = lane >> 4;
-  f32x4 s[NR][2];
+  const auto token = [&](int i) { return k0 + 16 * (i >> 2) + 4 * h4 + (i & 3); };
+  // every load before the first use
+  u32x4 f[2][8], v[2][8];
 #pragma unroll
   for (int sub = 0; sub < 2; ++sub) {
-    const uint16_t* p = row(0, min(k0 + 16 * sub + c, last)) + 8 * h4;
-    u32x4 f[8];
+    const uint16_t* p = tokens.at(0, min(k0 + 16 * sub + c, last)) + 8 * h4;
 #pragma unroll
-    for (int x = 0; x < 8; ++x) f[x] = *reinterpret_cast<const u32x4*>(p + 32 * x);
+    for (int x = 0; x < 8; ++x) f[sub][x] = *reinterpret_cast<const u32x4*>(p + 32 * x);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint16_t* p = tokens.at(1, min(token(i), last)) + 16 * c;
+    v[0][i] = *reinterpret_cast<const u32x4*>(p);
+    v[1][i] = *reinterpret_cast<const u32x4*>(p + 8);
+  }
+#pragma unroll
+  for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+    for (int x = 0; x < 8; ++x) asm volatile("" : "+v"(f[sub][x]));
+  f32x4 s[NR][2];
+#pragma unroll
+  for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       s[n][sub] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int x = 0; x < 8; ++x) s[n][sub] = mfma16<false>(f[x], q[n][x], s[n][sub]);
+      for (int x = 0; x < 8; ++x) s[n][sub] = mfma16<false>(f[sub][x], q[n][x], s[n][sub]);
     }
-  }
-  const auto token = [&](int i) { return k0 + 16 * (i >> 2) + 4 * h4 + (i & 3); };
   u32x4 pf[NR];
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
@@ -336,26 +381,24 @@ __device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR
   uint32_t left = 0;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    u32x4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4*>(row(1, min(token(i), last)) + 16 * c + 8 * half);
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       const uint32_t sel = x & 1 ? 0x07060302u : 0x05040100u;
       u32x4 f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f[i] = __builtin_amdgcn_perm(v[2 * i + 1][x >> 1], v[2 * i][x >> 1], sel);
+        f[i] = __builtin_amdgcn_perm(v[half][2 * i + 1][x >> 1], v[half][2 * i][x >> 1], sel);
         // as in key_step: 0 times what a row does not see must stay 0
-        if (masked) f[i] = finite_pair(f[i], left);
+        const uint32_t clean = finite_pair(f[i], left);
+        f[i] = masked ? clean : f[i];
       }
 #pragma unroll
       for (int n = 0; n < NR; ++n) r.o[n][8 * half + x] = mfma16<false>(f, pf[n], r.o[n][8 * half + x]);
     }
   }
-  if (__any(left != 0)) {
+  if (masked && __any(left != 0)) {
     for (int k = 0; k < 32 && k0 + k <= last; ++k) {
-      const uint16_t* p = row(1, k0 + k) + 64 * h4;
+      const uint16_t* p = tokens.at(1, k0 + k) + 64 * h4;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -368,22 +411,27 @@ __device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR
   }
 }
 
-// Rows of a segment joined over the waves: wave w owns rows 4 w .. 4 w + 3 of
-// each set, four values to a lane.
-template <int NR>
-struct Joined {
-  float o[NR][4][4], m[NR][4], l[NR][4];
-};
+// An output row from its sums.
+__device__ __forceinline__ void write_row(const AttnArgs& a, int32_t begin, int32_t head, int32_t row, f32x4 o, float l, int lane) {
+  const float inv = 1.0f / l;
+  const int32_t token = token_of(row, a.group);
+  const int64_t at = (begin + static_cast<int64_t>(token)) * a.q_heads + head * a.group + (row - token * a.group);
+  *reinterpret_cast<uint2*>(a.out + at * kDim + 4 * lane) = uint2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+}
+
 constexpr int kSplitStats = 4 * 16 * 2;  // floats
 
-// Adds the waves' sums to the joined ones, rotated if they are over centroids.
-template <int NR>
-__device__ __forceinline__ void join(Joined<NR>& j, SplitRows<NR>& r, bool enc, float* lds, int lane, int wave) {
+// The four waves' sums of a tile's `there` rows joined, rotated if they are
+// over centroids, and given to write(row, sums of lane's four values, maximum,
+// sum of weights).
+template <int NR, class F>
+__device__ __forceinline__ void join_waves(SplitRows<NR>& r, bool enc, int there, float* lds, int lane, int wave, F write) {
   const int c = lane & 15, h4 = lane >> 4;
   const float f = enc ? __builtin_ldexpf(1.0f, r.exponent - 8) : 1.0f;  // H c n / 256
   float* stat = lds + 4 * 16 * kSplitPitch;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
+    if (16 * n >= there) continue;
     const float l = group_sum(r.l[n]);
     __syncthreads();
 #pragma unroll
@@ -400,302 +448,295 @@ __device__ __forceinline__ void join(Joined<NR>& j, SplitRows<NR>& r, bool enc, 
       stat[(wave * 16 + c) * 2 + 1] = l;
     }
     __syncthreads();
+#pragma clang loop unroll(disable)
+    for (int row = wave; row < min(there - 16 * n, 16); row += 4) {
+      float2 s[4];
+      float m = -FLT_MAX;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int row = 4 * wave + k;
-      float m = j.m[n][k];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) m = fmaxf(m, stat[(w * 16 + row) * 2]);
-      const float old = fast_exp2(j.m[n][k] - m);
+      for (int w = 0; w < 4; ++w) {
+        s[w] = *reinterpret_cast<const float2*>(stat + (w * 16 + row) * 2);
+        m = fmaxf(m, s[w].x);
+      }
       float o[4] = {0, 0, 0, 0}, sum = 0;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float g = fast_exp2(stat[(w * 16 + row) * 2] - m);
-        sum += stat[(w * 16 + row) * 2 + 1] * g;
+        const float g = fast_exp2(s[w].x - m);
+        sum += s[w].y * g;
         const f32x4 v = *reinterpret_cast<const f32x4*>(lds + (w * 16 + row) * kSplitPitch + 4 * lane);
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] += v[e] * g;
       }
       if (enc) wave_fwht(o, lane);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) j.o[n][k][e] = j.o[n][k][e] * old + o[e];
-      j.l[n][k] = j.l[n][k] * old + sum;
-      j.m[n][k] = m;
+      write(16 * n + row, f32x4{o[0], o[1], o[2], o[3]}, m, sum);
     }
   }
+}
+
+// What a request asks of the split kernel.
+template <int M>
+struct SplitWork {
+  Extent e;
+  int32_t tiles, blocks;  // tiles of a KV head, page blocks of each
+  __device__ __forceinline__ SplitWork(const AttnArgs& a, const Extent& x) {
+    e = x;
+    const int32_t r = e.n * a.group;
+    tiles = r >= a.least && r <= a.most ? static_cast<int32_t>(ceil_div(r, M)) : 0;
+    blocks = static_cast<int32_t>(ceil_div(e.paged, kSplitBlock));
+  }
+};
+// Slots of partial sums (attention_common.h): after the workers' come two to a
+// tile, for pages that one workgroup took whole and for the other tokens.
+__device__ __forceinline__ int32_t tile_slot(const AttnArgs& a, int32_t tile, int which) { return 2 * (a.workers + tile) + which; }
+
+// Pages [u0, u1) of a tile.
+template <int BITS, int NR, class F>
+__device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e, int32_t b, int32_t head, int32_t r0, int32_t u0,
+                                             int32_t u1, float* lds, int lane, int wave, F write) {
+  constexpr int M = 16 * NR;
+  constexpr int kQPitch = kDim + 8;  // fp16 to a row of rotated q in LDS
+  const int c = lane & 15, h4 = lane >> 4;
+  const int32_t rows = e.n * a.group;
+  // Pages: lane 2 i + s holds that of sixteen s of the wave's 32 tokens of
+  // block u0 + i, for 32 blocks at a time and the next 32 ahead.
+  const auto pages = [&](int32_t u) {
+    const int64_t t = static_cast<int64_t>(u + (lane >> 1)) * kSplitBlock + 32 * wave + 16 * (lane & 1);
+    const int32_t id = t < e.paged ? a.table[static_cast<int64_t>(b) * a.width + (t >> a.page_shift)] : -1;
+    return id < a.n_pages ? id : -1;
+  };
+  int32_t ids = pages(u0), ids_ahead = u0 + 32 < u1 ? pages(u0 + 32) : -1;
+
+  const auto q_load = [&](int row) {
+    const int32_t token = token_of(min(r0 + row, rows - 1), a.group);
+    return *reinterpret_cast<const uint2*>(a.q + (e.begin + static_cast<int64_t>(token)) * a.q_stride +
+                                           (head * a.group + (min(r0 + row, rows - 1) - token * a.group)) * kDim + 4 * lane);
+  };
+  uint2 v = q_load(wave);
+
+  const auto fetch = [&](int32_t u, Codes<BITS>& to, int (&there)[2]) {
+    const int at = (u - u0) & 31;
+    if (at == 0 && u > u0) {
+      ids = ids_ahead;
+      if (u + 32 < u1) ids_ahead = pages(u + 32);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int64_t t = static_cast<int64_t>(u) * kSplitBlock + 32 * wave + 16 * s;
+      const int32_t id = __builtin_amdgcn_readlane(ids, 2 * at + s);
+      there[s] = id < 0 ? 0 : static_cast<int>(min(e.paged - t, int64_t{16}));
+      const int64_t vec = ((static_cast<int64_t>(max(id, 0)) * a.kv_heads + head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+      load_codes<BITS>(to, a, s, vec, lane);
+    }
+  };
+  Codes<BITS> cur, next;
+  int there[2], there_next[2] = {0, 0};
+  fetch(u0, cur, there);
+
+  // q rotated, each row over a power of two that brings its largest value to
+  // [1, 2), as fp16, while the codes are on their way
+  uint16_t* ql = reinterpret_cast<uint16_t*>(lds);
+  float* qf = lds + M * kQPitch / 2;
+#pragma clang loop unroll(disable)
+  for (int row = wave; row < M; row += 4) {
+    float x[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+    if (r0 + row + 4 < rows && row + 4 < M) v = q_load(row + 4);
+    if (r0 + row >= rows) {  // rows that are not there: zeros, and no more to load
+      *reinterpret_cast<uint2*>(ql + row * kQPitch + 4 * lane) = uint2{0, 0};
+      if (lane == 0) qf[row] = 0;
+      continue;
+    }
+    wave_fwht(x, lane);
+    const float mx = wave_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+    const int ex = mx > 0 ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
+    const float f = __builtin_ldexpf(a.scale < 0 ? -1.0f : 1.0f, -ex);
+    *reinterpret_cast<uint2*>(ql + row * kQPitch + 4 * lane) = uint2{pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f)};
+    if (lane == 0) qf[row] = __builtin_ldexpf(fabsf(a.scale) * kLog2e, ex - 8);
+  }
+  __syncthreads();
+  u32x4 q[NR][8];
+  float factor[NR];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    factor[n] = qf[16 * n + c];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      uint32_t d[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        d[k] = *reinterpret_cast<const uint32_t*>(ql + (16 * n + c) * kQPitch + 64 * h4 + dim_of<BITS>(x, k));
+      q[n][x] = u32x4{__builtin_amdgcn_perm(d[1], d[0], 0x05040100u), __builtin_amdgcn_perm(d[3], d[2], 0x05040100u),
+                      __builtin_amdgcn_perm(d[1], d[0], 0x07060302u), __builtin_amdgcn_perm(d[3], d[2], 0x07060302u)};
+    }
+  }
+  SplitRows<NR> r;
+  clear(r);
+  for (int32_t u = u0; u < u1; ++u) {
+    if (u + 1 < u1) fetch(u + 1, next, there_next);
+    if (there[0] + there[1] > 0) code_step<BITS, NR>(r, q, factor, cur, there[0], there[1], lane);
+    cur = next;
+    there[0] = there_next[0];
+    there[1] = there_next[1];
+  }
+  join_waves<NR>(r, true, rows - r0, lds, lane, wave, write);
+}
+
+// The window's and the step's own tokens of a tile.
+template <int NR, class F>
+__device__ __forceinline__ void attend_tokens(const AttnArgs& a, const Extent& e, int32_t b, int32_t head, int32_t r0, float* lds,
+                                              int lane, int wave, F write) {
+  constexpr int M = 16 * NR;
+  const int c = lane & 15, h4 = lane >> 4;
+  const int32_t rows = e.n * a.group;
+  const Tokens tokens(a, e, b, head);
+  const int64_t first = tokens.near + token_of(r0, a.group), last = tokens.near + token_of(min(r0 + M, rows) - 1, a.group);
+  u32x4 q[NR][8];
+  int64_t lim[NR];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const int32_t row = min(r0 + 16 * n + c, rows - 1), token = token_of(row, a.group);
+    const uint16_t* p = a.q + (e.begin + static_cast<int64_t>(token)) * a.q_stride + (head * a.group + (row - token * a.group)) * kDim + 8 * h4;
+    lim[n] = tokens.near + token;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      q[n][x] = *reinterpret_cast<const u32x4*>(p + 32 * x);
+      if (a.scale < 0) q[n][x] ^= 0x80008000u;
+    }
+  }
+  SplitRows<NR> r;
+  clear(r);
+  for (int64_t k0 = 32 * wave; k0 <= last; k0 += kSplitBlock)
+    token_step<NR>(r, q, fabsf(a.scale) * kLog2e, k0, last, lim, k0 + 31 > first, tokens, lane);
+  join_waves<NR>(r, false, rows - r0, lds, lane, wave, write);
 }
 
 template <int BITS, int NR>
 __global__ void __launch_bounds__(kSplitThreads) __attribute__((amdgpu_waves_per_eu(NR == 1 ? 2 : 1, NR == 1 ? 2 : 1)))
 hlwq_split_attention_kernel(const AttnArgs a) {
   constexpr int M = 16 * NR;
-  constexpr int kQPitch = kDim + 8;  // fp16 to a row of rotated q in LDS
   __shared__ __attribute__((aligned(16))) float lds[4 * 16 * kSplitPitch + kSplitStats];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, h4 = lane >> 4;
-  const auto cost = [&](int32_t b) {
-    const Work<M, kSplitBlock> w(a, b);
-    return w.head_cost() * a.kv_heads;
+  const auto tiles = [&](const Extent& e) { return SplitWork<M>(a, e).tiles * a.kv_heads; };
+  const auto cost = [&](const Extent& e) {
+    const SplitWork<M> w(a, e);
+    return w.tiles * w.blocks * a.kv_heads;
   };
-  const int64_t total = sum_over(a.requests, cost);
-  const Share share(total, a.workers, kSplitLeast);
-  const int64_t worker = blockIdx.x;
-  if (total == 0 || worker >= share.workers) return;
-  const Found first = find(a.requests, share.bound(worker), cost, [](int32_t) { return int64_t{0}; });
-
-  for_segments<M, kSplitBlock>(a, share, first, worker, [&](const Work<M, kSplitBlock>& w, const Segment& g) {
-    const Extent& e = w.e;
-    const int32_t r0 = static_cast<int32_t>(g.tile * M), rows = w.rows(a);
-    const int64_t blocks = w.blocks(a, g.tile);
-    const int64_t u0 = w.block_at(g.from, blocks, g.cost), u1 = w.block_at(g.to, blocks, g.cost);
-    const int64_t near = e.held - e.enc;  // tokens in the window
-    Joined<NR> all;
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        all.m[n][k] = -FLT_MAX;
-        all.l[n][k] = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) all.o[n][k][x] = 0;
-      }
-    // token (of the step) and q vector of a row of the tile
-    const auto q_row = [&](int32_t row, int32_t& token) {
-      token = token_of(row, a.group);
-      return a.q + (e.begin + static_cast<int64_t>(token)) * a.q_stride + (g.head * a.group + (row - token * a.group)) * kDim;
+  const auto to_slot = [&](int32_t slot) {
+    return [&a, slot, lane](int row, f32x4 o, float m, float l) {
+      *reinterpret_cast<f32x4*>(partial_row<M>(a, slot, row) + 4 * lane) = o;
+      if (lane == 0) *partial_stat<M>(a, slot, row) = float2{m, l};
     };
+  };
 
-    if (u0 < w.page_blocks && u0 < u1) {
-      const int64_t end = min(u1, w.page_blocks);
-      // Pages: lane 2 i + s holds that of sixteen s of the wave's 32 tokens of
-      // block u0 + i, for 32 blocks at a time and the next 32 ahead.
-      const auto pages = [&](int64_t u) {
-        const int64_t t = (u + (lane >> 1)) * kSplitBlock + 32 * wave + 16 * (lane & 1);
-        const int32_t id = t < e.paged ? a.table[static_cast<int64_t>(g.b) * a.width + (t >> a.page_shift)] : -1;
-        return id < a.n_pages ? id : -1;
-      };
-      int32_t ids = pages(u0), ids_ahead = u0 + 32 < end ? pages(u0 + 32) : -1;
-      const auto fetch = [&](int64_t u, Codes<BITS>& to, int (&there)[2]) {
-        const int at = static_cast<int>(u - u0) & 31;
-        if (at == 0 && u > u0) {
-          ids = ids_ahead;
-          if (u + 32 < end) ids_ahead = pages(u + 32);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int64_t t = u * kSplitBlock + 32 * wave + 16 * s;
-          const int32_t id = __builtin_amdgcn_readlane(ids, 2 * at + s);
-          there[s] = id < 0 ? 0 : static_cast<int>(min(e.paged - t, int64_t{16}));
-          const int64_t vec = ((static_cast<int64_t>(max(id, 0)) * a.kv_heads + g.head) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-          load_codes<BITS>(to, a, s, vec, lane);
-        }
-      };
-      Codes<BITS> cur, next;
-      int there[2], there_next[2] = {0, 0};
-      fetch(u0, cur, there);
+  if (static_cast<int32_t>(blockIdx.x) >= a.workers) {
+    // a tile's window and own tokens
+    const int32_t x = blockIdx.x - a.workers;
+    Finder<decltype(tiles), Nothing> finder(a, tiles, Nothing{});
+    if (x >= finder.total) return;
+    const Found f = finder.find(x);
+    const SplitWork<M> w(a, f.e);
+    const int32_t head = quotient(f.rest, w.tiles), r0 = (f.rest - head * w.tiles) * M;
+    const int32_t slot = tile_slot(a, x, 1);
+    attend_tokens<NR>(a, w.e, f.b, head, r0, lds, lane, wave, [&](int row, f32x4 o, float m, float l) {
+      if (w.blocks == 0)
+        write_row(a, w.e.begin, head, r0 + row, o, l, lane);
+      else
+        to_slot(slot)(row, o, m, l);
+    });
+    return;
+  }
 
-      // q rotated, each row over a power of two that brings its largest value
-      // to [1, 2), as fp16
-      uint16_t* ql = reinterpret_cast<uint16_t*>(lds);
-      float* qf = lds + M * kQPitch / 2;
-      for (int row = wave; row < M; row += 4) {
-        float x[4] = {0, 0, 0, 0};
-        if (r0 + row < rows) {
-          int32_t token;
-          const uint2 v = *reinterpret_cast<const uint2*>(q_row(r0 + row, token) + 4 * lane);
-          x[0] = bf16_lo(v.x);
-          x[1] = bf16_hi(v.x);
-          x[2] = bf16_lo(v.y);
-          x[3] = bf16_hi(v.y);
-        }
-        wave_fwht(x, lane);
-        float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, lane_xor(mx, d));
-        const int ex = mx > 0 ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
-        const float f = __builtin_ldexpf(a.scale < 0 ? -1.0f : 1.0f, -ex);
-        *reinterpret_cast<uint2*>(ql + row * kQPitch + 4 * lane) = uint2{pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f)};
-        if (lane == 0) qf[row] = __builtin_ldexpf(fabsf(a.scale) * kLog2e, ex - 8);
-      }
-      __syncthreads();
-      u32x4 q[NR][8];
-      float factor[NR];
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        factor[n] = qf[16 * n + c];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          uint32_t d[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            d[k] = *reinterpret_cast<const uint32_t*>(ql + (16 * n + c) * kQPitch + 64 * h4 + dim_of<BITS>(x, k));
-          q[n][x] = u32x4{__builtin_amdgcn_perm(d[1], d[0], 0x05040100u), __builtin_amdgcn_perm(d[3], d[2], 0x05040100u),
-                          __builtin_amdgcn_perm(d[1], d[0], 0x07060302u), __builtin_amdgcn_perm(d[3], d[2], 0x07060302u)};
-        }
-      }
-      SplitRows<NR> r;
-      clear(r);
-      for (int64_t u = u0; u < end; ++u) {
-        if (u + 1 < end) fetch(u + 1, next, there_next);
-        if (there[0] + there[1] > 0) code_step<BITS, NR>(r, q, factor, cur, there[0], there[1], lane);
-        cur = next;
-        there[0] = there_next[0];
-        there[1] = there_next[1];
-      }
-      join<NR>(all, r, true, lds, lane, wave);
-      __syncthreads();
+  Finder<decltype(cost), decltype(tiles)> finder(a, cost, tiles);
+  const Share share(finder.total, a.workers, 1);
+  const int32_t worker = blockIdx.x;
+  if (finder.total == 0 || worker >= share.workers) return;
+  const Found first = finder.find(share.bound(worker));
+  int32_t left = share.bound(worker + 1) - share.bound(worker), b = first.b, rest = first.rest, before = first.before;
+#pragma clang loop unroll(disable)
+  while (left > 0 && b < a.requests) {
+    const SplitWork<M> w(a, b == first.b ? first.e : extent_of(a, b));
+    const int32_t tile = w.blocks ? quotient(rest, w.blocks) : 0;  // of all KV heads'
+    if (w.blocks == 0 || tile >= w.tiles * a.kv_heads) {            // past the request's last
+      before += w.tiles * a.kv_heads;
+      rest = 0;
+      ++b;
+      continue;
     }
-
-    if (u1 > w.page_blocks) {
-      const int64_t from = max(u0, w.page_blocks) - w.page_blocks, to = u1 - w.page_blocks;
-      const int32_t first_token = w.first_token(a, g.tile);
-      const int64_t last = near + w.last_token(a, g.tile);
-      u32x4 q[NR][8];
-      int64_t lim[NR];
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        int32_t token;
-        const uint16_t* p = q_row(min(r0 + 16 * n + c, rows - 1), token) + 8 * h4;
-        lim[n] = near + token;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          q[n][x] = *reinterpret_cast<const u32x4*>(p + 32 * x);
-          if (a.scale < 0) q[n][x] ^= 0x80008000u;
-        }
-      }
-      const int64_t ring0 = a.ring > 0 ? e.enc % a.ring : 0;
-      const auto row = [&](int side, int64_t k) {
-        if (k < near) {
-          int64_t slot = ring0 + k;
-          if (slot >= a.ring) slot -= a.ring;
-          return (side ? a.v_window : a.k_window) + ((static_cast<int64_t>(g.b) * a.kv_heads + g.head) * a.ring + slot) * kDim;
-        }
-        return (side ? a.v_new : a.k_new) + (e.begin + (k - near)) * (side ? a.v_stride : a.k_stride) + g.head * kDim;
-      };
-      SplitRows<NR> r;
-      clear(r);
-      for (int64_t u = from; u < to; ++u) {
-        const int64_t k0 = u * kSplitBlock + 32 * wave;
-        if (k0 <= last) token_step<NR>(r, q, fabsf(a.scale) * kLog2e, k0, last, lim, k0 + 31 > near + first_token, row, lane);
-      }
-      join<NR>(all, r, false, lds, lane, wave);
-      __syncthreads();
-    }
-
-    const bool whole = g.from == 0 && g.to == g.cost;
-    const int slot = g.from > 0 ? 0 : 1;
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int row = 16 * n + 4 * wave + k;
-        if (r0 + row >= rows) continue;
-        if (whole) {
-          const float inv = 1.0f / all.l[n][k];
-          const int32_t token = token_of(r0 + row, a.group);
-          const int64_t at = (e.begin + static_cast<int64_t>(token)) * a.q_heads + g.head * a.group + (r0 + row - token * a.group);
-          *reinterpret_cast<uint2*>(a.out + at * kDim + 4 * lane) =
-              uint2{pack_bf16x2(all.o[n][k][0] * inv, all.o[n][k][1] * inv), pack_bf16x2(all.o[n][k][2] * inv, all.o[n][k][3] * inv)};
-        } else {
-          *reinterpret_cast<f32x4*>(partial_row<M>(a, worker, slot, row) + 4 * lane) =
-              f32x4{all.o[n][k][0], all.o[n][k][1], all.o[n][k][2], all.o[n][k][3]};
-          if (lane == 0) *partial_stat<M>(a, worker, slot, row) = float2{all.m[n][k], all.l[n][k]};
-        }
-      }
-  });
+    const int32_t u0 = rest - tile * w.blocks, u1 = min(u0 + left, w.blocks);
+    const int32_t head = quotient(tile, w.tiles);
+    const int32_t slot = u0 == 0 && u1 == w.blocks ? tile_slot(a, before + tile, 0) : 2 * worker + (u0 > 0 ? 0 : 1);
+    attend_pages<BITS, NR>(a, w.e, b, head, (tile - head * w.tiles) * M, u0, u1, lds, lane, wave, to_slot(slot));
+    __syncthreads();
+    left -= u1 - u0;
+    rest += u1 - u0;
+  }
 }
 
-// ---------------------------------------------------------------------------
-// Tiles that several workgroups shared.  Where tiles are narrow and many
-// workgroups share one (few rows over a long cache), a workgroup joins one row
-// and each wave every fourth partial sum; where they are wide (WAVE_ROWS > 0)
-// a wave joins that many rows by itself.
-// ---------------------------------------------------------------------------
-
-template <int M, int KT, int LEAST, int WAVE_ROWS>
-__global__ void __launch_bounds__(kSplitThreads) hlwq_join_attention_kernel(const AttnArgs a) {
-  constexpr int kRows = WAVE_ROWS ? 4 * WAVE_ROWS : 1;  // of a workgroup
-  __shared__ __attribute__((aligned(16))) float lds[4 * (kDim + 4)];
+// Joins a row of a tile from the partial sums of its pages and its other
+// tokens, each wave every fourth.
+template <int M>
+__global__ void __launch_bounds__(kSplitThreads) hlwq_split_join_kernel(const AttnArgs a) {
+  __shared__ __attribute__((aligned(16))) float lds[4 * kSplitPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const auto cost = [&](int32_t b) {
-    const Work<M, KT> w(a, b);
-    return w.head_cost() * a.kv_heads;
+  const auto tiles = [&](const Extent& e) { return SplitWork<M>(a, e).tiles * a.kv_heads; };
+  const auto cost = [&](const Extent& e) {
+    const SplitWork<M> w(a, e);
+    return w.tiles * w.blocks * a.kv_heads;
   };
-  const auto tiles = [&](int32_t b) {
-    const Work<M, KT> w(a, b);
-    return w.tiles * a.kv_heads;
+  Finder<decltype(tiles), decltype(cost)> finder(a, tiles, cost);
+  const int32_t x = blockIdx.x / M, row = blockIdx.x % M;
+  if (x >= finder.total) return;
+  const Found f = finder.find(x);
+  const SplitWork<M> w(a, f.e);
+  const int32_t head = quotient(f.rest, w.tiles), r0 = (f.rest - head * w.tiles) * M;
+  if (w.blocks == 0 || r0 + row >= w.e.n * a.group) return;
+  const Share share(Finder<decltype(cost), Nothing>(a, cost, Nothing{}).total, a.workers, 1);
+  const int32_t x0 = f.before + f.rest * w.blocks;
+  const int32_t w0 = share.worker_at(x0), w1 = share.worker_at(x0 + w.blocks - 1);
+  const int32_t parts = w1 - w0 + 2;  // the pages', then the other tokens'
+  const auto slot_of = [&](int32_t k) {
+    return k == parts - 1 ? tile_slot(a, x, 1) : w0 == w1 ? tile_slot(a, x, 0) : 2 * (w0 + k) + (k == 0 ? 1 : 0);
   };
-  const int64_t total = sum_over(a.requests, cost);
-  if (total == 0) return;
-  const Found f = find(a.requests, blockIdx.x / (M / kRows), tiles, cost);
-  if (f.b < 0) return;
-  const Work<M, KT> w(a, f.b);
-  const int32_t head = static_cast<int32_t>(quotient(f.rest, w.tiles));
-  const int64_t tile = f.rest - head * w.tiles;
-  const int32_t row0 = (blockIdx.x % (M / kRows)) * kRows, r0 = static_cast<int32_t>(tile * M), rows = w.rows(a);
-  if (r0 + row0 >= rows) return;
-  const int64_t x0 = f.also + head * w.head_cost() + w.cost_before(tile), x1 = x0 + w.cost(tile);
-  const Share share(total, a.workers, LEAST);
-  const int64_t w0 = share.worker_at(x0), w1 = share.worker_at(x1 - 1);
-  if (w0 == w1) return;  // one workgroup did it all
 
-  const auto write = [&](int32_t at_row, f32x4 o, float l) {
-    const float inv = 1.0f / l;
-    const int32_t token = token_of(at_row, a.group);
-    const int64_t at = (w.e.begin + static_cast<int64_t>(token)) * a.q_heads + head * a.group + (at_row - token * a.group);
-    *reinterpret_cast<uint2*>(a.out + at * kDim + 4 * lane) = uint2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
-  };
-  const auto add = [&](int64_t k, int row, f32x4& o, float& m, float& l) {
-    const int slot = k == w0 ? 1 : 0;
-    const float2 s = *partial_stat<M>(a, k, slot, row);
-    const f32x4 v = *reinterpret_cast<const f32x4*>(partial_row<M>(a, k, slot, row) + 4 * lane);
-    const float mn = fmaxf(m, s.x);
-    const float f0 = fast_exp2(m - mn), f1 = fast_exp2(s.x - mn);
+  // 64 partial sums at a time: a lane reads each one's maximum and sum, then
+  // the weighted rows, several in flight
+  float m = -FLT_MAX, l = 0;
+  f32x4 o = {0, 0, 0, 0};
+  for (int32_t k0 = wave; k0 < parts; k0 += 256) {
+    float2 s{-FLT_MAX, 0};
+    if (k0 + 4 * lane < parts) s = *partial_stat<M>(a, slot_of(k0 + 4 * lane), row);
+    const float mn = fmaxf(m, wave_max(s.x)), old = fast_exp2(m - mn), g = fast_exp2(s.x - mn);
     m = mn;
-    l = l * f0 + s.y * f1;
-    o = o * f0 + v * f1;
-  };
-  if constexpr (WAVE_ROWS > 0) {
-    float m[WAVE_ROWS], l[WAVE_ROWS];
-    f32x4 o[WAVE_ROWS];
+    l = l * old + wave_sum(s.y * g);
+    o *= old;
+    const int count = min((parts - k0 + 3) / 4, 64);
+    for (int i = 0; i < count; i += 8) {
+      f32x4 v[8];
 #pragma unroll
-    for (int i = 0; i < WAVE_ROWS; ++i) {
-      m[i] = -FLT_MAX;
-      l[i] = 0;
-      o[i] = f32x4{0, 0, 0, 0};
+      for (int j = 0; j < 8; ++j)
+        v[j] = *reinterpret_cast<const f32x4*>(partial_row<M>(a, slot_of(k0 + 4 * min(i + j, count - 1)), row) + 4 * lane);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < count) o += v[j] * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), i + j));
     }
-    const int row = row0 + wave * WAVE_ROWS;
-    for (int64_t k = w0; k <= w1; ++k)
-#pragma unroll
-      for (int i = 0; i < WAVE_ROWS; ++i)
-        if (r0 + row + i < rows) add(k, row + i, o[i], m[i], l[i]);
-#pragma unroll
-    for (int i = 0; i < WAVE_ROWS; ++i)
-      if (r0 + row + i < rows) write(r0 + row + i, o[i], l[i]);
-  } else {
-    float m = -FLT_MAX, l = 0;
-    f32x4 o = {0, 0, 0, 0};
-    for (int64_t k = w0 + wave; k <= w1; k += 4) add(k, row0, o, m, l);
-    *reinterpret_cast<f32x4*>(lds + wave * (kDim + 4) + 4 * lane) = o;
-    if (lane == 0) {
-      lds[wave * (kDim + 4) + kDim] = m;
-      lds[wave * (kDim + 4) + kDim + 1] = l;
-    }
-    __syncthreads();
-    if (wave != 0) return;
-    float mx = -FLT_MAX;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, lds[k * (kDim + 4) + kDim]);
-    l = 0;
-    o = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float g = fast_exp2(lds[k * (kDim + 4) + kDim] - mx);
-      l += lds[k * (kDim + 4) + kDim + 1] * g;
-      o += *reinterpret_cast<const f32x4*>(lds + k * (kDim + 4) + 4 * lane) * g;
-    }
-    write(r0 + row0, o, l);
   }
+  *reinterpret_cast<f32x4*>(lds + wave * kSplitPitch + 4 * lane) = o;
+  if (lane == 0) {
+    lds[wave * kSplitPitch + kDim] = m;
+    lds[wave * kSplitPitch + kDim + 1] = l;
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  float mx = -FLT_MAX;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mx = fmaxf(mx, lds[k * kSplitPitch + kDim]);
+  l = 0;
+  o = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float g = fast_exp2(lds[k * kSplitPitch + kDim] - mx);
+    l += lds[k * kSplitPitch + kDim + 1] * g;
+    o += *reinterpret_cast<const f32x4*>(lds + k * kSplitPitch + 4 * lane) * g;
+  }
+  write_row(a, w.e.begin, head, r0 + row, o, l, lane);
 }
 
 }  // namespace hlwq_kv

@@ -265,15 +265,12 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
   const int head = blockIdx.x % a.kv_heads;
   const int g = a.group;
 
-  const auto tiles = [&](int32_t b) {
-    const RowRange r = row_range(a.cu, b, a.rows);
-    return ceil_div((r.end - r.begin) * g, kRows);
-  };
-  const Found f = find(a.requests, blockIdx.x / a.kv_heads, tiles, [](int32_t) { return int64_t{0}; });
-  if (f.b < 0) return;
-  const RowRange rr = row_range(a.cu, f.b, a.rows);
-  const int32_t n = rr.end - rr.begin, rows = n * g;
-  const int32_t r0 = static_cast<int32_t>(tiles(f.b) - 1 - f.rest) * kRows;  // the tile's first row
+  const auto tiles = [&](const Extent& e) { return static_cast<int32_t>(ceil_div(e.n * g, kRows)); };
+  Finder<decltype(tiles), Nothing> finder(a, tiles, Nothing{});
+  if (static_cast<int32_t>(blockIdx.x / a.kv_heads) >= finder.total) return;
+  const Found f = finder.find(blockIdx.x / a.kv_heads);
+  const int32_t begin = f.e.begin, n = f.e.n, rows = n * g;
+  const int32_t r0 = (tiles(f.e) - 1 - f.rest) * kRows;  // the tile's first row
   const int32_t w0 = r0 + 32 * wave;                                          // the wave's
   // tokens of the lane's row, of the wave's first and last, of the tile's last
   const int32_t tok = token_of(min(w0 + col, rows - 1), g);
@@ -283,7 +280,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
 
   u32x4 q[16];
   {
-    const uint16_t* qp = a.q + (rr.begin + static_cast<int64_t>(tok)) * a.q_stride + q_head() * kDim + 8 * h;
+    const uint16_t* qp = a.q + (begin + static_cast<int64_t>(tok)) * a.q_stride + q_head() * kDim + 8 * h;
 #pragma unroll
     for (int s = 0; s < 16; ++s) q[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
   }
@@ -301,7 +298,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
   const uint32_t place = (col ^ swizzle(2 * wave + h)) * 16;
   uint32_t ko = (2 * wave + h) * static_cast<uint32_t>(a.k_stride) * 2, vo = (2 * wave + h) * static_cast<uint32_t>(a.v_stride) * 2;
   const auto stage = [&](int buf, int32_t t0) {
-    const int64_t at = rr.begin + static_cast<int64_t>(t0);
+    const int64_t at = begin + static_cast<int64_t>(t0);
     const u32x4 kb = buffer_of(a.k_new + at * a.k_stride + head * kDim, ((n - t0 - 1) * a.k_stride + kDim) * 2);
     const u32x4 vb = buffer_of(a.v_new + at * a.v_stride + head * kDim, ((n - t0 - 1) * a.v_stride + kDim) * 2);
     asm volatile("" : "+v"(ko), "+v"(vo));  // the sums below are made each time, not kept in registers
@@ -336,12 +333,12 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
     }
   }
   add_nonfinite(r, (first + 1) / 32 * 32, last, tok, h, [&](int64_t key) {
-    return a.v_new + (rr.begin + key) * a.v_stride + head * kDim;
+    return a.v_new + (begin + key) * a.v_stride + head * kDim;
   });
   r.l += half_swap(r.l);
   const float inv = 1.0f / r.l;
   if (w0 + col < rows) {
-    uint16_t* op = a.out + ((rr.begin + static_cast<int64_t>(tok)) * a.q_heads + q_head()) * kDim;
+    uint16_t* op = a.out + ((begin + static_cast<int64_t>(tok)) * a.q_heads + q_head()) * kDim;
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll

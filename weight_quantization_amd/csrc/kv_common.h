@@ -40,19 +40,66 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ uint16_t f16_bits(float f) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f)); }
 __device__ __forceinline__ float f16_value(uint16_t b) { return static_cast<float>(__builtin_bit_cast(_Float16, b)); }
 
-// Value of lane l ^ d (d a compile-time power of two after unrolling): a DPP
-// quad permutation for d = 1 and 2, a swizzle (xor mode) for d = 4, 8 and 16,
-// a bpermute for d = 32.
+// Value of lane l ^ d (d a compile-time power of two after unrolling), all in
+// the VALU: quad permutations for d = 1 and 2; two mirrors for 4 and 8 (l ^ 3
+// then l ^ 7, l ^ 7 then l ^ 15); for 16 and 32 the swaps of half rows and half
+// waves between two copies.  A swizzle through LDS takes ten times as long.
 __device__ __forceinline__ uint32_t lane_xor(uint32_t v, int d) {
   const int i = static_cast<int>(v);
   if (d == 1) return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(i, 0xB1, 0xF, 0xF, true));
   if (d == 2) return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(i, 0x4E, 0xF, 0xF, true));
-  if (d == 4) return static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(i, 0x1F | (4 << 10)));
-  if (d == 8) return static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(i, 0x1F | (8 << 10)));
-  if (d == 16) return static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(i, 0x1F | (16 << 10)));
-  return static_cast<uint32_t>(__shfl_xor(i, d, 64));
+  if (d == 4) {
+    const int j = __builtin_amdgcn_mov_dpp(i, 0x1B, 0xF, 0xF, true);
+    return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(j, 0x141, 0xF, 0xF, true));
+  }
+  if (d == 8) {
+    const int j = __builtin_amdgcn_mov_dpp(i, 0x141, 0xF, 0xF, true);
+    return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(j, 0x140, 0xF, 0xF, true));
+  }
+  if (d == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (threadIdx.x & 16) ? r[0] : r[1];
+  }
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return (threadIdx.x & 32) ? r[0] : r[1];
 }
 __device__ __forceinline__ float lane_xor(float v, int d) { return __uint_as_float(lane_xor(__float_as_uint(v), d)); }
+
+// Inclusive prefix sum over the wave: within rows of sixteen, then the rows'
+// last values on.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t scan_step(int64_t v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, ROWS, 0xF, false);
+  return v + static_cast<int64_t>((static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32) | static_cast<uint32_t>(lo));
+}
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+  v = scan_step<0x111, 0xF>(v);
+  v = scan_step<0x112, 0xF>(v);
+  v = scan_step<0x114, 0xF>(v);
+  v = scan_step<0x118, 0xF>(v);
+  v = scan_step<0x142, 0xA>(v);
+  return scan_step<0x143, 0xC>(v);
+}
+__device__ __forceinline__ int32_t wave_scan(int32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+}
+// Largest value and sum over the wave, in every lane.
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, lane_xor(v, d));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += lane_xor(v, d);
+  return v;
+}
 
 // Unnormalised butterflies of a 256-vector held four values to a lane (lane l
 // holds 4l .. 4l + 3), strides 1, 2, 4, .. 128, each sum one fp32 rounding.

@@ -62,15 +62,6 @@ __device__ __forceinline__ Need need_of(const PlanArgs& a, int32_t b) {
   return d;
 }
 
-__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
-  return v;
-}
-
 __global__ void __launch_bounds__(kPlanThreads) hlwq_kv_plan_tables_kernel(const PlanArgs a) {
   __shared__ int64_t sums[3][kPlanWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -92,7 +83,7 @@ __global__ void __launch_bounds__(kPlanThreads) hlwq_kv_plan_tables_kernel(const
   int64_t pre[3], total[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    const int64_t s = wave_scan(own[k], lane);
+    const int64_t s = wave_scan(own[k]);
     pre[k] = s - own[k];
     if (lane == 63) sums[k][wave] = s;
   }
