@@ -11,6 +11,24 @@ from weight_quantization_amd import paged
 
 OK, ENULL, ESHAPE, EBITS, EBLOCK, EDEV, EALIGN, ELIMIT, EOVERLAP = 0, -1, -2, -3, -4, -5, -6, -7, -8
 HEADER = os.path.join(os.path.dirname(wq.binding.HEADER_PATH), "hlwq_attention.h")
+
+
+class KvStore(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("packed", "norms", "window")]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", KvStore), ("v", KvStore)]
+    _fields_ += [(n, ctypes.c_int64) for n in ("n_pages", "requests", "kv_heads", "page_size", "n_residual", "ring")]
+    _fields_ += [("head_dim", ctypes.c_int), ("bits", ctypes.c_int)]
+
+
+class KvPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("tokens", "n_new", "reset", "n_free", "free_pages", "block_table", "cu_new",
+                                               "lens", "row_request", "positions", "slots", "n_free_after", "status")]
+    _fields_ += [(n, ctypes.c_int64) for n in ("requests", "rows", "max_pages", "n_pages", "page_size", "n_residual")]
+
+
 A = 1 << 32  # aligned addresses far apart, never dereferenced
 STEP = 1 << 36
 
@@ -38,9 +56,9 @@ def test_exports_every_declared_symbol(lib):
 def cache(**kw):
     d = dict(n_pages=8, requests=2, kv_heads=4, page_size=64, n_residual=128, ring=128, head_dim=256, bits=3)
     d.update({k: v for k, v in kw.items() if k not in ("k", "v")})
-    k = paged.KvStore(*kw.get("k", (at(0), at(1), at(2))))
-    v = paged.KvStore(*kw.get("v", (at(3), at(4), at(5))))
-    return paged.KvCache(k, v, d["n_pages"], d["requests"], d["kv_heads"], d["page_size"], d["n_residual"], d["ring"],
+    k = KvStore(*kw.get("k", (at(0), at(1), at(2))))
+    v = KvStore(*kw.get("v", (at(3), at(4), at(5))))
+    return KvCache(k, v, d["n_pages"], d["requests"], d["kv_heads"], d["page_size"], d["n_residual"], d["ring"],
                          d["head_dim"], d["bits"])
 
 
@@ -165,7 +183,7 @@ def plan_args(**kw):
                                          "row_request", "positions", "slots", "n_free_after", "status"))}
     d.update(requests=3, rows=7, max_pages=5, n_pages=11, page_size=64, n_residual=128)
     d.update(kw)
-    return paged.KvPlanArgs(**d)
+    return KvPlan(**d)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -183,6 +201,15 @@ def test_plan_argument_errors(lib, kw, status):
 
 def test_plan_needs_arguments(lib):
     assert lib.hlwq_kv_page_plan(None, None) == ENULL
+
+
+def test_packed_arguments_are_the_c_structures():
+    assert paged._CACHE.size == ctypes.sizeof(KvCache) and paged._PLAN.size == ctypes.sizeof(KvPlan)
+    c = KvCache.from_buffer_copy(paged._CACHE.pack(*range(1, 15)))
+    assert [c.k.packed, c.k.norms, c.k.window, c.v.packed, c.v.norms, c.v.window] == [1, 2, 3, 4, 5, 6]
+    assert [getattr(c, n) for n, _ in KvCache._fields_[2:]] == list(range(7, 15))
+    p = KvPlan.from_buffer_copy(paged._PLAN.pack(*range(1, 20)))
+    assert [getattr(p, n) for n, _ in KvPlan._fields_] == list(range(1, 20))
 
 
 def test_python_refuses_host_tensors_and_wrong_types():

@@ -253,10 +253,10 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
         for (int i = 0; i < KT / 16; ++i) {
           const int pair = 16 * i + 2 * wave;
-          const int64_t k = min(t0 + pair + h, end_key);  // past the end the last one again, which nobody sees there
+          const int64_t k = t0 + pair + h;
           const uint32_t c = (col ^ swizzle(2 * wave + h)) * 8;
-          stage16(tokens.at(0, k) + c, base + buf * kStage + pair * 512);
-          stage16(tokens.at(1, k) + c, base + buf * kStage + KT * 512 + pair * 512);
+          stage16(tokens.at(0, k, end_key) + c, base + buf * kStage + pair * 512);
+          stage16(tokens.at(1, k, end_key) + c, base + buf * kStage + KT * 512 + pair * 512);
         }
       };
       u32x4 q[16];
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
         }
       }
       add_nonfinite(r, max((first_key + 1) / 32 * 32, from * KT), min(last_key, to * KT - 1), near + tok, h,
-                    [&](int64_t key) { return tokens.at(1, key); });
+                    [&](int64_t key) { return tokens.at(1, key, end_key); });
       barrier();
     }
 

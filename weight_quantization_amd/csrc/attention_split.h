@@ -306,6 +306,8 @@ __device__ __forceinline__ void code_step(SplitRows<NR>& r, const u32x4 (&q)[NR]
   }
 }
 
+__constant__ uint16_t c_zero_vector[kDim] = {};
+
 // Where the window's and the step's tokens of a KV head lie, K and V: token k
 // below `near` in ring slot ring0 + k (mod ring), the others in the step's rows.
 struct Tokens {
@@ -325,8 +327,9 @@ struct Tokens {
     ring0 = near > 0 ? static_cast<uint32_t>(e.enc) % static_cast<uint32_t>(a.ring) : 0;  // both below 2^31
   }
   // Token k's vector: selects and one multiply, no branch, so that loads of
-  // several tokens are in flight together.
-  __device__ __forceinline__ const uint16_t* at(int side, int64_t k) const {
+  // several tokens are in flight together.  Past `last`, a vector of zeros.
+  __device__ __forceinline__ const uint16_t* at(int side, int64_t k, int64_t last) const {
+    if (k > last) return c_zero_vector;
     const bool in = k < near;
     const int64_t slot = ring0 + k >= ring ? ring0 + k - ring : ring0 + k;
     const uint32_t index = static_cast<uint32_t>(in ? slot : k - near);
@@ -335,23 +338,25 @@ struct Tokens {
 };
 
 // 32 bf16 tokens from k0 on; lim[n]: last token that the lane's row of set n
-// sees; last: the last one there is.
+// sees; last: the last one there is.  masked: some row does not see some token;
+// mixed: nor do all that are there see the same.
 template <int NR>
 __device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR][8], float factor, int64_t k0, int64_t last,
-                                           const int64_t (&lim)[NR], bool masked, const Tokens& tokens, int lane) {
+                                           const int64_t (&lim)[NR], bool masked, bool mixed, const Tokens& tokens,
+                                           int lane) {
   const int c = lane & 15, h4 = lane >> 4;
   const auto token = [&](int i) { return k0 + 16 * (i >> 2) + 4 * h4 + (i & 3); };
   // every load before the first use
   u32x4 f[2][8], v[2][8];
 #pragma unroll
   for (int sub = 0; sub < 2; ++sub) {
-    const uint16_t* p = tokens.at(0, min(k0 + 16 * sub + c, last)) + 8 * h4;
+    const uint16_t* p = tokens.at(0, k0 + 16 * sub + c, last) + 8 * h4;
 #pragma unroll
     for (int x = 0; x < 8; ++x) f[sub][x] = *reinterpret_cast<const u32x4*>(p + 32 * x);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint16_t* p = tokens.at(1, min(token(i), last)) + 16 * c;
+    const uint16_t* p = tokens.at(1, token(i), last) + 16 * c;
     v[0][i] = *reinterpret_cast<const u32x4*>(p);
     v[1][i] = *reinterpret_cast<const u32x4*>(p + 8);
   }
@@ -378,7 +383,17 @@ __device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR
 #pragma unroll
     for (int i = 0; i < 4; ++i) pf[n][i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
   }
+  // as in key_step: where some rows see a token and others do not, 0 times its
+  // value must stay 0
   uint32_t left = 0;
+  if (mixed) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[half][i][x] = finite_pair(v[half][i][x], left);
+  }
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -388,17 +403,14 @@ __device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f[i] = __builtin_amdgcn_perm(v[half][2 * i + 1][x >> 1], v[half][2 * i][x >> 1], sel);
-        // as in key_step: 0 times what a row does not see must stay 0
-        const uint32_t clean = finite_pair(f[i], left);
-        f[i] = masked ? clean : f[i];
       }
 #pragma unroll
       for (int n = 0; n < NR; ++n) r.o[n][8 * half + x] = mfma16<false>(f, pf[n], r.o[n][8 * half + x]);
     }
   }
-  if (masked && __any(left != 0)) {
+  if (mixed && __any(left != 0)) {
     for (int k = 0; k < 32 && k0 + k <= last; ++k) {
-      const uint16_t* p = tokens.at(1, k0 + k) + 64 * h4;
+      const uint16_t* p = tokens.at(1, k0 + k, last) + 64 * h4;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -604,7 +616,7 @@ __device__ __forceinline__ void attend_tokens(const AttnArgs& a, const Extent& e
   SplitRows<NR> r;
   clear(r);
   for (int64_t k0 = 32 * wave; k0 <= last; k0 += kSplitBlock)
-    token_step<NR>(r, q, fabsf(a.scale) * kLog2e, k0, last, lim, k0 + 31 > first, tokens, lane);
+    token_step<NR>(r, q, fabsf(a.scale) * kLog2e, k0, last, lim, k0 + 31 > first, k0 + 31 > first && first < last, tokens, lane);
   join_waves<NR>(r, false, rows - r0, lds, lane, wave, write);
 }
 

@@ -98,24 +98,35 @@ __global__ void __launch_bounds__(kPlanThreads) hlwq_kv_plan_tables_kernel(const
   }
   bad |= total[0] > a.rows || nf + total[1] > a.n_pages;
 
-  // pages given back: where each request's begin on the stack, kept in lens
-  // until the lengths are written
-  if (!bad && total[1] > 0) {
+  // Pages given back: a wave goes through its lanes' requests one by one, 256
+  // pages at a time.  All are looked at before any is moved.
+  const auto for_back = [&](auto run) {
     int64_t at = pre[1];
-    for (int32_t b = b0; b < b1; ++b) {
-      a.lens[b] = static_cast<int32_t>(at);
-      at += need_of(a, b).back;
-    }
-    __syncthreads();
-    bool off = false;
-    for (int32_t b = wave; b < a.requests; b += kPlanWaves) {
-      if (!a.reset[b]) continue;
-      const int64_t n = pages_of(a, a.tokens[b]);
-      for (int64_t p = lane; p < n; p += 64) {
-        const int32_t id = a.table[static_cast<int64_t>(b) * a.width + p];
-        off |= id < 0 || id >= a.n_pages;
+    for (int32_t k = 0; k < per; ++k) {
+      const int32_t b = b0 + k;
+      const int32_t own = b < b1 ? static_cast<int32_t>(need_of(a, b).back) : 0;
+      uint64_t todo = __ballot(own > 0);
+      while (todo) {
+        const int l = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        const int32_t n = __builtin_amdgcn_readlane(own, l);
+        const int32_t to = __builtin_amdgcn_readlane(static_cast<int32_t>(at), l);
+        const int32_t* from = a.table + static_cast<int64_t>(__builtin_amdgcn_readlane(b, l)) * a.width;
+        for (int32_t p0 = 0; p0 < n; p0 += 256) {
+          int32_t id[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) id[i] = p0 + 64 * i + lane < n ? from[p0 + 64 * i + lane] : 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (p0 + 64 * i + lane < n) run(id[i], to + p0 + 64 * i + lane);
+        }
       }
+      at += own;
     }
+  };
+  if (!bad && total[1] > 0) {
+    bool off = false;
+    for_back([&](int32_t id, int32_t) { off |= id < 0 || id >= a.n_pages; });
     bad = __syncthreads_or(off);
   }
   const int64_t top = nf + total[1];
@@ -133,12 +144,7 @@ __global__ void __launch_bounds__(kPlanThreads) hlwq_kv_plan_tables_kernel(const
     return;
   }
   if (total[1] > 0) {
-    for (int32_t b = wave; b < a.requests; b += kPlanWaves) {
-      if (!a.reset[b]) continue;
-      const int64_t n = pages_of(a, a.tokens[b]);
-      int32_t* to = a.free_pages + nf + a.lens[b];
-      for (int64_t p = lane; p < n; p += 64) to[p] = a.table[static_cast<int64_t>(b) * a.width + p];
-    }
+    for_back([&](int32_t id, int32_t to) { a.free_pages[nf + to] = id; });
     __syncthreads();
   }
   int64_t row = pre[0], taken = pre[2];
@@ -188,11 +194,16 @@ __global__ void __launch_bounds__(kRowThreads) hlwq_kv_plan_rows_kernel(const Pl
 }
 
 // ---------------------------------------------------------------------------
-// Append.  One wave takes one head vector of one row, K or V: it encodes the
-// token that the row pushes out of the window (from the ring, or from the
-// step's own row n_residual before it) into its slot, and puts a new token
-// that stays into the ring.  A ring slot that is read and rewritten in the
-// same call has one wave do both, in that order, so no wave waits for another.
+// Append.  Eight lanes take one head vector of one row, K or V, 32 values a
+// lane: they encode the token that the row pushes out of the window (from the
+// ring, or from the step's own row n_residual before it) into its slot, and put
+// a new token that stays into the ring.  A ring slot that is read and rewritten
+// in the same call has the same lanes do both, in that order, so nobody waits
+// for anybody.
+//
+// What bounds a long append is the VALU (about 125 instructions a vector; a
+// whole wave to a vector, four values a lane, takes 320), what bounds a decode
+// step the chain of three loads behind one another.
 // ---------------------------------------------------------------------------
 
 struct AppendArgs {
@@ -207,72 +218,113 @@ struct AppendArgs {
   const int32_t* slots;
   int64_t n_slots;  // n_pages * page_size
   int32_t requests, rows, heads, page_shift;
-  int64_t n_res, ring;
+  int64_t n_res;
+  int32_t ring;
 };
 
-__device__ __forceinline__ int64_t floor_mod(int64_t a, int64_t m) {
-  const int64_t r = a % m;
-  return r < 0 ? r + m : r;
+constexpr int kAppendThreads = 256;
+constexpr int kAppendLanes = 8;  // to a vector
+
+__device__ __forceinline__ int32_t floor_mod(int64_t a, int32_t m) {
+  const int32_t r = static_cast<int32_t>(a < 0 ? ~a : a) % m;  // positions and their differences fit 31 bits
+  return a < 0 ? m - 1 - r : r;
 }
 
-// Codes and norm of the vector whose values 4 lane .. 4 lane + 3 are in w, to
-// packed[vec] and norms[vec].
+// 8 codes of y[0 .. 7], first in the lowest bits: the number of thresholds
+// strictly below y, found by halves, each comparison's bit shifted in.
 template <int BITS>
-__device__ __forceinline__ void encode_wave(uint2 w, uint8_t* packed, uint16_t* norms, int64_t vec, int lane) {
-  constexpr int K = 1 << BITS;
-  constexpr float thr3[7] = HLWQ_THRESHOLDS_3;
-  constexpr float thr2[3] = HLWQ_THRESHOLDS_2;
-  float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-  float s = __builtin_fmaf(x[0], x[0], x[1] * x[1]) + __builtin_fmaf(x[2], x[2], x[3] * x[3]);
+__device__ __forceinline__ uint32_t eight_codes(const float* y) {
+  constexpr float t3[7] = HLWQ_THRESHOLDS_3;
+  constexpr float t2[3] = HLWQ_THRESHOLDS_2;
+  uint32_t v = 0;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) s = s + lane_xor(s, d);
-  const float n = sqrtf(s);
-  const float r = n >= FLT_MIN ? 1.0f / n : 0.0f;
-  wave_fwht(x, lane);
-  uint32_t f = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float y = x[j] * r;
-    uint32_t c = 0;
-#pragma unroll
-    for (int k = 0; k < K - 1; ++k) c += (y > (BITS == 3 ? thr3[k] : thr2[k])) ? 1u : 0u;
-    f |= c << (BITS * j);
-  }
-  uint8_t* dst = packed + vec * (32 * BITS);
-  if constexpr (BITS == 2) {
-    dst[lane] = static_cast<uint8_t>(f);
-  } else {
-    // 8 lanes hold 32 codes = 96 bits = 3 words
-    const int i = lane & 7, bit = 12 * i;
-    const uint64_t v = static_cast<uint64_t>(f) << (bit & 31);
-    uint32_t wd[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      wd[k] = ((bit >> 5) == k ? static_cast<uint32_t>(v) : 0u) | ((bit >> 5) + 1 == k ? static_cast<uint32_t>(v >> 32) : 0u);
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) wd[k] |= lane_xor(wd[k], d);
-    if (i == 0) {
-      uint32_t* out = reinterpret_cast<uint32_t*>(dst + 12 * (lane >> 3));
-      out[0] = wd[0];
-      out[1] = wd[1];
-      out[2] = wd[2];
+  for (int i = 7; i >= 0; --i) {
+    if constexpr (BITS == 3) {
+      const bool c2 = y[i] > t3[3];
+      const bool c1 = y[i] > (c2 ? t3[5] : t3[1]);
+      const float lo = c1 ? t3[2] : t3[0], hi = c1 ? t3[6] : t3[4];
+      const bool c0 = y[i] > (c2 ? hi : lo);
+      v = v + v + c2;
+      v = v + v + c1;
+      v = v + v + c0;
+    } else {
+      const bool c1 = y[i] > t2[1];
+      const bool c0 = y[i] > (c1 ? t2[2] : t2[0]);
+      v = v + v + c1;
+      v = v + v + c0;
     }
   }
-  if (lane == 0) norms[vec] = f16_bits(n);
+  return v;
 }
 
-constexpr int kAppendThreads = 256;
+// Codes and norm of the vector whose values 32 i .. 32 i + 31 are lane i's (of
+// eight), to `packed` (the vector's bytes) and *norm.
+template <int BITS>
+__device__ __forceinline__ void encode(const u32x4 (&w)[4], uint8_t* packed, uint16_t* norm, int i) {
+  float x[32];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    x[2 * k] = bf16_lo(w[k >> 2][k & 3]);
+    x[2 * k + 1] = bf16_hi(w[k >> 2][k & 3]);
+  }
+  // the norm's adjacent-pair tree, five levels in the lane, three across
+  float s[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) s[k] = __builtin_fmaf(x[2 * k], x[2 * k], x[2 * k + 1] * x[2 * k + 1]);
+#pragma unroll
+  for (int n = 8; n >= 1; n >>= 1)
+#pragma unroll
+    for (int k = 0; k < n; ++k) s[k] = s[2 * k] + s[2 * k + 1];
+  float sum = s[0];
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) sum = sum + lane_xor(sum, d);
+  const float n = sqrtf(sum);
+  const float r = n >= FLT_MIN ? 1.0f / n : 0.0f;
+  // butterflies at strides 1 .. 16 in the lane, 32 .. 128 across: a + b below,
+  // a - b above, each one rounding (the product by +-1 is exact)
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if ((k & h) == 0) {
+        const float a = x[k], b = x[k + h];
+        x[k] = a + b;
+        x[k + h] = a - b;
+      }
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) {
+    const float sign = (i & d) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = __builtin_fmaf(x[k], sign, lane_xor(x[k], d));
+  }
+#pragma unroll
+  for (int k = 0; k < 32; ++k) x[k] *= r;
+  uint32_t g[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) g[k] = eight_codes<BITS>(x + 8 * k);
+  if constexpr (BITS == 3) {
+    u32x3 out;
+    out[0] = g[0] | (g[1] << 24);
+    out[1] = (g[1] >> 8) | (g[2] << 16);
+    out[2] = (g[2] >> 16) | (g[3] << 8);
+    uint32_t* to = reinterpret_cast<uint32_t*>(packed + 12 * i);
+    to[0] = out[0];
+    to[1] = out[1];
+    to[2] = out[2];
+  } else {
+    *reinterpret_cast<u32x2*>(packed + 8 * i) = u32x2{g[0] | (g[1] << 16), g[2] | (g[3] << 16)};
+  }
+  if (i == 0) *norm = f16_bits(n);
+}
 
 template <int BITS>
 __global__ void __launch_bounds__(kAppendThreads) hlwq_kv_paged_append_kernel(const AppendArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = threadIdx.x & (kAppendLanes - 1);
   const int side = blockIdx.y;
-  const int64_t row64 = unit / a.heads;
-  if (row64 >= a.rows) return;
-  const int32_t row = static_cast<int32_t>(row64), head = static_cast<int32_t>(unit - row64 * a.heads);
+  const uint32_t unit = blockIdx.x * (kAppendThreads / kAppendLanes) + threadIdx.x / kAppendLanes;
+  const int32_t row = static_cast<int32_t>(unit / static_cast<uint32_t>(a.heads));
+  if (row >= a.rows) return;
+  const int32_t head = static_cast<int32_t>(unit - static_cast<uint32_t>(row) * static_cast<uint32_t>(a.heads));
   const int32_t b = a.row_request[row];
   if (b < 0 || b >= a.requests) return;
   const RowRange rr = row_range(a.cu, b, a.rows);
@@ -280,25 +332,35 @@ __global__ void __launch_bounds__(kAppendThreads) hlwq_kv_paged_append_kernel(co
   const int64_t n = rr.end - rr.begin;
   const int64_t total = max(static_cast<int64_t>(a.lens[b]), n), held = total - n;
   const int64_t t = held + (row - rr.begin), old = t - a.n_res;
-  const uint16_t* src = a.src[side] + head * kDim + 4 * lane;
-  uint16_t* ring = a.window[side] + (static_cast<int64_t>(b) * a.heads + head) * a.ring * kDim + 4 * lane;
   const int64_t stay = max(held, total - a.n_res);  // first new token that stays in the window
+  const uint16_t* src = a.src[side] + head * kDim + 32 * i;
+  uint16_t* ring = a.window[side] + (static_cast<int64_t>(b) * a.heads + head) * a.ring * kDim + 32 * i;
+  const auto load = [](const uint16_t* p, u32x4(&w)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = reinterpret_cast<const u32x4*>(p)[k];
+  };
+  const auto store = [](uint16_t* p, const u32x4(&w)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) reinterpret_cast<u32x4*>(p)[k] = w[k];
+  };
 
   if (old >= 0) {
     const bool ringed = old < held;
+    uint16_t* place = ringed ? ring + static_cast<int64_t>(floor_mod(old, a.ring)) * kDim : nullptr;
     const int64_t slot = a.slots[row];
     if (slot >= 0 && slot < a.n_slots) {
-      const uint16_t* p = ringed ? ring + old % a.ring * kDim : src + (row - a.n_res) * a.stride[side];
-      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      u32x4 w[4];
+      load(ringed ? place : src + (row - a.n_res) * a.stride[side], w);
       const int64_t vec = (((slot >> a.page_shift) * a.heads + head) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
-      encode_wave<BITS>(w, a.packed[side], a.norms[side], vec, lane);
+      encode<BITS>(w, a.packed[side] + vec * (32 * BITS), a.norms[side] + vec, i);
     }
     if (ringed) {
       // the token that stays in the slot just read, if one does
       const int64_t t2 = stay + floor_mod(old - stay, a.ring);
       if (t2 < total) {
-        const uint2 v = *reinterpret_cast<const uint2*>(src + (rr.begin + (t2 - held)) * a.stride[side]);
-        *reinterpret_cast<uint2*>(ring + old % a.ring * kDim) = v;
+        u32x4 w[4];
+        load(src + (rr.begin + (t2 - held)) * a.stride[side], w);
+        store(place, w);
       }
     }
   }
@@ -308,8 +370,9 @@ __global__ void __launch_bounds__(kAppendThreads) hlwq_kv_paged_append_kernel(co
     const int64_t u = held - 1 - floor_mod(held - 1 - t, a.ring);
     const bool other = u >= 0 && u >= held - a.n_res && u < total - a.n_res;
     if (!other) {
-      const uint2 v = *reinterpret_cast<const uint2*>(src + row * a.stride[side]);
-      *reinterpret_cast<uint2*>(ring + t % a.ring * kDim) = v;
+      u32x4 w[4];
+      load(src + row * a.stride[side], w);
+      store(ring + static_cast<int64_t>(floor_mod(t, a.ring)) * kDim, w);
     }
   }
 }
@@ -378,7 +441,7 @@ int run_append(const hlwq_kv_cache* c, const void* k, int64_t k_stride, const vo
   if (rows < 0) return HLWQ_ERR_SHAPE;
   if (rows == 0 || c->requests == 0 || c->kv_heads == 0) return HLWQ_OK;
   int64_t units;
-  if (rows > 0x7fffffff || !mul_ok(rows, c->kv_heads, &units) || ceil_div(units, kAppendThreads / 64) > 0x7fffff)
+  if (rows > 0x7fffffff || !mul_ok(rows, c->kv_heads, &units) || units > 0x7fffffff)
     return HLWQ_ERR_LIMIT;
   int64_t ke, ve;
   if ((st = check_rows(k, k_stride, rows, c->kv_heads, &ke)) != HLWQ_OK ||
@@ -414,8 +477,8 @@ int run_append(const hlwq_kv_cache* c, const void* k, int64_t k_stride, const vo
   a.heads = static_cast<int32_t>(c->kv_heads);
   a.page_shift = __builtin_ctzll(static_cast<uint64_t>(c->page_size));
   a.n_res = c->n_residual;
-  a.ring = c->ring;
-  const dim3 grid(static_cast<uint32_t>(ceil_div(units, kAppendThreads / 64)), 2);
+  a.ring = static_cast<int32_t>(c->ring);
+  const dim3 grid(static_cast<uint32_t>(ceil_div(units, kAppendThreads / kAppendLanes)), 2);
   return launch(c->bits == 3 ? hlwq_kv_paged_append_kernel<3> : hlwq_kv_paged_append_kernel<2>, grid, dim3(kAppendThreads),
                 stream, a);
 }

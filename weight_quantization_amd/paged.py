@@ -15,35 +15,20 @@ current stream to the C function of the same name and raises on a status.
 from __future__ import annotations
 
 import ctypes
-import math
+import struct
 from typing import TYPE_CHECKING, NamedTuple
 
 from . import binding
-from .binding import KV_DIM, _check, _i64, _int, _ptr, _stream_handle, _torch, _vp, load_library
+from .binding import KV_DIM, _check, _i64, _int, _stream_handle, _torch, _vp, load_library
 
 if TYPE_CHECKING:
     import torch
 
 
-class KvStore(ctypes.Structure):
-    _fields_ = [("packed", _vp), ("norms", _vp), ("window", _vp)]
-
-
-class KvCache(ctypes.Structure):
-    _fields_ = [("k", KvStore), ("v", KvStore), ("n_pages", _i64), ("requests", _i64), ("kv_heads", _i64),
-                ("page_size", _i64), ("n_residual", _i64), ("ring", _i64), ("head_dim", _int), ("bits", _int)]
-
-
-class KvPlanArgs(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("tokens", "n_new", "reset", "n_free", "free_pages", "block_table", "cu_new", "lens",
-                                   "row_request", "positions", "slots", "n_free_after", "status")]
-    _fields_ += [(n, _i64) for n in ("requests", "rows", "max_pages", "n_pages", "page_size", "n_residual")]
-
-
 binding._SIGNATURES.update({
-    "hlwq_kv_page_plan": (_int, [ctypes.POINTER(KvPlanArgs), _vp]),
-    "hlwq_kv_paged_append": (_int, [ctypes.POINTER(KvCache), _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
-    "hlwq_kv_paged_attention": (_int, [ctypes.POINTER(KvCache), _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+    "hlwq_kv_page_plan": (_int, [_vp, _vp]),
+    "hlwq_kv_paged_append": (_int, [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "hlwq_kv_paged_attention": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
                                        _i64, _i64, ctypes.c_float, _vp, _vp, ctypes.c_size_t, _vp]),
     "hlwq_kv_paged_attention_workspace": (ctypes.c_size_t, [_i64, _i64, _i64, _i64]),
     "hlwq_prompt_attention": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, ctypes.c_float,
@@ -62,6 +47,81 @@ class KvPagePlan(NamedTuple):
     status: torch.Tensor       # [1] 0, the number of missing pages, or -1
 
 
+# A decode step makes these calls once per layer, so what they cost on the host
+# counts: every tensor is checked in one expression, and only a call that is to
+# be refused finds out why.
+
+def _fail(t, dtype, name, shape=None):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be in device memory")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _shape(t, dims, name):
+    """The shape of a tensor of this many dimensions."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    s = t.shape
+    if len(s) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {list(s)}")
+    return s
+
+
+def _at(t, dtype, shape, name):
+    """The address of a contiguous device tensor of this type and shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _fail(t, dtype, name, shape)
+
+
+def _rows(t, rows, heads, bf16, name):
+    """Token rows [rows, heads, 256] in bf16: whole head vectors side by side, any row stride that is a multiple
+    of 8 (a slice of a fused projection's output will do).  Returns the address and the row stride in elements."""
+    try:
+        ok = t.dtype is bf16 and t.shape == (rows, heads, KV_DIM) and t.is_cuda
+    except AttributeError:
+        ok = False
+    if not ok:
+        s = _shape(t, 3, name)
+        if t.dtype is bf16 and t.is_cuda:
+            raise ValueError(f"{name} must have {rows} rows of {heads} x {KV_DIM}, got {list(s)}")
+        _fail(t, bf16, name)
+    row, head, one = t.stride()
+    if rows <= 1 or heads == 0:
+        row = heads * KV_DIM  # there is no next row
+    elif row < heads * KV_DIM or row % 8:
+        one = 0
+    if (one != 1 or (heads > 1 and head != KV_DIM)) and t.numel():
+        raise ValueError(f"{name} must hold each row's heads side by side, rows a multiple of 8 elements apart; "
+                         f"its strides are {t.stride()}")
+    return t.data_ptr(), row
+
+
+_one_device = None  # whether the process sees a single device
+
+
+def _stream(stream, tensors):
+    """The stream to launch on (of the current device, as every tensor must be)."""
+    global _one_device
+    torch = _torch()
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
+    if stream is None and _one_device:
+        return torch.cuda.current_stream().cuda_stream
+    return _stream_handle(stream, *tensors)
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor that the call's stream uses first: the allocator hands memory out in the order of one stream."""
     torch = _torch()
@@ -71,63 +131,23 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _buf(t, dtype, shape, name):
-    """A contiguous device tensor of this type and shape (None: any extent)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be in device memory")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    s = t.shape
-    if len(s) != len(shape) or any(w is not None and g != w for g, w in zip(s, shape)):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(s)}")
-    return t
+_CACHE = struct.Struct("6P6q2i")  # hlwq_kv_cache
+_PLAN = struct.Struct("13P6q")    # hlwq_kv_plan
 
 
-def _rows(t, heads, name):
-    """Token rows [rows, heads, 256] in bf16: whole head vectors side by side, any row stride that is a multiple
-    of 8 (a slice of a fused projection's output will do).  Returns the row stride in elements."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be in device memory")
-    s = t.shape
-    if len(s) != 3 or s[2] != KV_DIM or (heads is not None and s[1] != heads):
-        raise ValueError(f"{name} must be [rows, {'heads' if heads is None else heads}, {KV_DIM}], got {list(s)}")
-    row, head, one = t.stride()
-    if t.numel() == 0 or s[0] == 1:
-        row = max(row, s[1] * KV_DIM)
-        row += -row % 8
-    if t.numel() and (one != 1 or (s[1] > 1 and head != KV_DIM) or row < s[1] * KV_DIM or row % 8):
-        raise ValueError(f"{name} must hold each row's heads side by side, rows a multiple of 8 elements apart; "
-                         f"its strides are {t.stride()}")
-    return row
-
-
-def _cache(k_packed, k_norms, v_packed, v_norms, k_window, v_window, requests, n_residual, bits):
-    torch = _torch()
+def _cache(torch, k_packed, k_norms, v_packed, v_norms, k_window, v_window, requests, n_residual, bits):
     if bits not in (2, 3):
         raise ValueError("bits must be 3 or 2")
-    _buf(k_packed, torch.uint8, (None, None, None, 32 * bits), "k_packed")
-    pages, heads, page, _ = k_packed.shape
-    _buf(v_packed, torch.uint8, (pages, heads, page, 32 * bits), "v_packed")
-    _buf(k_norms, torch.float16, (pages, heads, page), "k_norms")
-    _buf(v_norms, torch.float16, (pages, heads, page), "v_norms")
-    ring = 0
+    pages, heads, page, _ = _shape(k_packed, 4, "k_packed")
+    codes, norms, u8, f16 = (pages, heads, page, 32 * bits), (pages, heads, page), torch.uint8, torch.float16
+    kw = vw = ring = 0
     if k_window is not None or v_window is not None or n_residual:
-        _buf(k_window, torch.bfloat16, (requests, heads, None, KV_DIM), "k_window")
-        ring = k_window.shape[2]
-        _buf(v_window, torch.bfloat16, (requests, heads, ring, KV_DIM), "v_window")
-    return KvCache(KvStore(_ptr(k_packed), _ptr(k_norms), _ptr(k_window)),
-                   KvStore(_ptr(v_packed), _ptr(v_norms), _ptr(v_window)),
-                   pages, requests, heads, page, n_residual, ring, KV_DIM, bits), heads
+        ring = _shape(k_window, 4, "k_window")[2]
+        window, bf16 = (requests, heads, ring, KV_DIM), torch.bfloat16
+        kw, vw = _at(k_window, bf16, window, "k_window"), _at(v_window, bf16, window, "v_window")
+    return _CACHE.pack(_at(k_packed, u8, codes, "k_packed"), _at(k_norms, f16, norms, "k_norms"), kw,
+                       _at(v_packed, u8, codes, "v_packed"), _at(v_norms, f16, norms, "v_norms"), vw, pages, requests,
+                       heads, page, n_residual, ring, KV_DIM, bits), heads
 
 
 def hlwq_kv_page_plan(tokens, n_new, free_pages, n_free, block_table, rows: int, page_size: int = 64,
@@ -137,26 +157,24 @@ def hlwq_kv_page_plan(tokens, n_new, free_pages, n_free, block_table, rows: int,
     step's tensors, at least the sum of n_new (rows past it are padding); reset uint8 [requests]: nonzero where the
     slot's request has ended, whose pages go back first.  free_pages and block_table are updated in place."""
     torch = _torch()
-    _buf(tokens, torch.int32, (None,), "tokens")
-    n = tokens.shape[0]
-    _buf(n_new, torch.int32, (n,), "n_new")
-    _buf(free_pages, torch.int32, (None,), "free_pages")
-    _buf(n_free, torch.int32, (1,), "n_free")
-    _buf(block_table, torch.int32, (n, None), "block_table")
-    if reset is not None:
-        _buf(reset, torch.uint8, (n,), "reset")
+    i32 = torch.int32
+    n, = _shape(tokens, 1, "tokens")
+    pages, = _shape(free_pages, 1, "free_pages")
+    width = _shape(block_table, 2, "block_table")[1]
     if rows < 0:
         raise ValueError("rows must not be negative")
-    out = _empty(2 * n + 3 + 3 * rows, torch.int32, tokens.device, stream)
-    plan = KvPagePlan(*out.split_with_sizes([n + 1, n, rows, rows, rows, 1, 1]))
-    at = out.data_ptr()
-    ends = [at + 4 * k for k in (0, n + 1, 2 * n + 1, 2 * n + 1 + rows, 2 * n + 1 + 2 * rows, 2 * n + 1 + 3 * rows,
-                                 2 * n + 2 + 3 * rows)]
-    args = KvPlanArgs(_ptr(tokens), _ptr(n_new), _ptr(reset), _ptr(n_free), _ptr(free_pages), _ptr(block_table), *ends,
-                      n, rows, block_table.shape[1], free_pages.shape[0], page_size, n_residual)
-    st = load_library().hlwq_kv_page_plan(
-        ctypes.byref(args), _stream_handle(stream, tokens, n_new, free_pages, n_free, block_table, reset))
-    _check("hlwq_kv_page_plan", st)
+    read = (_at(tokens, i32, (n,), "tokens"), _at(n_new, i32, (n,), "n_new"),
+            0 if reset is None else _at(reset, torch.uint8, (n,), "reset"), _at(n_free, i32, (1,), "n_free"),
+            _at(free_pages, i32, (pages,), "free_pages"), _at(block_table, i32, (n, width), "block_table"))
+    out = _empty(2 * n + 3 + 3 * rows, i32, tokens.device, stream)
+    plan = KvPagePlan(*out.split_with_sizes((n + 1, n, rows, rows, rows, 1, 1)))
+    lens = out.data_ptr() + 4 * (n + 1)
+    maps, end = lens + 4 * n, lens + 4 * (n + 3 * rows)
+    args = _PLAN.pack(*read, lens - 4 * (n + 1), lens, maps, maps + 4 * rows, maps + 8 * rows, end, end + 4, n, rows, width,
+                      pages, page_size, n_residual)
+    st = load_library().hlwq_kv_page_plan(args, _stream(stream, (tokens, n_new, free_pages, n_free, block_table, reset)))
+    if st:
+        _check("hlwq_kv_page_plan", st)
     return plan
 
 
@@ -166,31 +184,24 @@ def hlwq_kv_paged_append(k_new, v_new, cu_new, lens, row_request, slots, k_packe
     [n_pages, kv_heads, page_size, 32 * bits], norms fp16 [n_pages, kv_heads, page_size], windows bf16
     [requests, kv_heads, ring, 256] (None when n_residual = 0); cu_new, lens, row_request, slots from the plan."""
     torch = _torch()
-    _buf(lens, torch.int32, (None,), "lens")
-    n = lens.shape[0]
-    cache, heads = _cache(k_packed, k_norms, v_packed, v_norms, k_window, v_window, n, n_residual, bits)
-    ks = _rows(k_new, heads, "k_new")
-    rows = k_new.shape[0]
-    vs = _rows(v_new, heads, "v_new")
-    _same_rows(rows, v_new, "v_new")
-    _buf(cu_new, torch.int32, (n + 1,), "cu_new")
-    _buf(row_request, torch.int32, (rows,), "row_request")
-    _buf(slots, torch.int32, (rows,), "slots")
+    i32, bf16 = torch.int32, torch.bfloat16
+    n, = _shape(lens, 1, "lens")
+    cache, heads = _cache(torch, k_packed, k_norms, v_packed, v_norms, k_window, v_window, n, n_residual, bits)
+    rows = _shape(k_new, 3, "k_new")[0]
+    k, ks = _rows(k_new, rows, heads, bf16, "k_new")
+    v, vs = _rows(v_new, rows, heads, bf16, "v_new")
     st = load_library().hlwq_kv_paged_append(
-        ctypes.byref(cache), _ptr(k_new), ks, _ptr(v_new), vs, _ptr(cu_new), _ptr(lens), _ptr(row_request), _ptr(slots),
-        rows, _stream_handle(stream, k_new, v_new, cu_new, lens, row_request, slots, k_packed, k_norms, v_packed, v_norms,
-                             k_window, v_window))
-    _check("hlwq_kv_paged_append", st)
+        cache, k, ks, v, vs, _at(cu_new, i32, (n + 1,), "cu_new"), _at(lens, i32, (n,), "lens"),
+        _at(row_request, i32, (rows,), "row_request"), _at(slots, i32, (rows,), "slots"), rows,
+        _stream(stream, (k_new, v_new, cu_new, lens, row_request, slots, k_packed, k_norms, v_packed, v_norms, k_window,
+                         v_window)))
+    if st:
+        _check("hlwq_kv_paged_append", st)
 
 
-def _same_rows(rows, t, name):
-    if t.shape[0] != rows:
-        raise ValueError(f"{name} must have {rows} rows, got {t.shape[0]}")
-
-
-def _heads(q, kv_heads):
-    if q.shape[1] and (not kv_heads or q.shape[1] % kv_heads):
-        raise ValueError(f"{q.shape[1]} query heads do not divide over {kv_heads} KV heads")
+def _heads(q_heads, kv_heads):
+    if q_heads and (not kv_heads or q_heads % kv_heads):
+        raise ValueError(f"{q_heads} query heads do not divide over {kv_heads} KV heads")
 
 
 def hlwq_kv_paged_attention_workspace(requests: int, rows: int, q_heads: int, kv_heads: int) -> int:
@@ -207,33 +218,31 @@ def hlwq_kv_paged_attention(q, k_new, v_new, cu_new, lens, block_table, k_packed
     [rows, q_heads, 256]; rows past cu_new[requests] are left as they were (undefined in a new `out`).  workspace:
     uint8, hlwq_kv_paged_attention_workspace bytes; allocated for the call by default."""
     torch = _torch()
-    _buf(lens, torch.int32, (None,), "lens")
-    n = lens.shape[0]
-    cache, heads = _cache(k_packed, k_norms, v_packed, v_norms, k_window, v_window, n, n_residual, bits)
-    qs = _rows(q, None, "q")
-    rows, q_heads, _ = q.shape
-    _heads(q, heads)
-    ks, vs = _rows(k_new, heads, "k_new"), _rows(v_new, heads, "v_new")
-    _same_rows(rows, k_new, "k_new")
-    _same_rows(rows, v_new, "v_new")
-    _buf(cu_new, torch.int32, (n + 1,), "cu_new")
-    _buf(block_table, torch.int32, (n, None), "block_table")
+    i32, bf16 = torch.int32, torch.bfloat16
+    n, = _shape(lens, 1, "lens")
+    cache, heads = _cache(torch, k_packed, k_norms, v_packed, v_norms, k_window, v_window, n, n_residual, bits)
+    rows, q_heads, _ = _shape(q, 3, "q")
+    _heads(q_heads, heads)
+    width = _shape(block_table, 2, "block_table")[1]
+    qp, qs = _rows(q, rows, q_heads, bf16, "q")
+    k, ks = _rows(k_new, rows, heads, bf16, "k_new")
+    v, vs = _rows(v_new, rows, heads, bf16, "v_new")
+    cu, le, table = (_at(cu_new, i32, (n + 1,), "cu_new"), _at(lens, i32, (n,), "lens"),
+                     _at(block_table, i32, (n, width), "block_table"))
     if out is None:
-        out = _empty((rows, q_heads, KV_DIM), torch.bfloat16, q.device, stream)
-    else:
-        _buf(out, torch.bfloat16, (rows, q_heads, KV_DIM), "out")
+        out = _empty((rows, q_heads, KV_DIM), bf16, q.device, stream)
+    to = _at(out, bf16, (rows, q_heads, KV_DIM), "out")
     lib = load_library()
     if workspace is None:
         workspace = _empty(lib.hlwq_kv_paged_attention_workspace(n, rows, q_heads, heads), torch.uint8, q.device, stream)
-    else:
-        _buf(workspace, torch.uint8, (None,), "workspace")
+    size, = _shape(workspace, 1, "workspace")
     st = lib.hlwq_kv_paged_attention(
-        ctypes.byref(cache), _ptr(q), qs, q_heads, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(cu_new), _ptr(lens),
-        _ptr(block_table), block_table.shape[1], rows, 1 / math.sqrt(KV_DIM) if scale is None else scale, _ptr(out),
-        _ptr(workspace), workspace.numel(),
-        _stream_handle(stream, q, k_new, v_new, cu_new, lens, block_table, k_packed, k_norms, v_packed, v_norms, k_window,
-                       v_window, out, workspace))
-    _check("hlwq_kv_paged_attention", st)
+        cache, qp, qs, q_heads, k, ks, v, vs, cu, le, table, width, rows, 0.0625 if scale is None else scale, to,
+        _at(workspace, torch.uint8, (size,), "workspace"), size,
+        _stream(stream, (q, k_new, v_new, cu_new, lens, block_table, k_packed, k_norms, v_packed, v_norms, k_window,
+                         v_window, out, workspace)))
+    if st:
+        _check("hlwq_kv_paged_attention", st)
     return out
 
 
@@ -242,23 +251,22 @@ def hlwq_prompt_attention(q, k, v, cu_seqlens, scale: float | None = None, out=N
     [rows, kv_heads, 256], cu_seqlens int32 [sequences + 1]; scale 1 / 16 by default.  Returns bf16
     [rows, q_heads, 256]; rows past cu_seqlens[-1] are left as they were (undefined in a new `out`)."""
     torch = _torch()
-    qs = _rows(q, None, "q")
-    rows, q_heads, _ = q.shape
-    ks = _rows(k, None, "k")
-    heads = k.shape[1]
-    _heads(q, heads)
-    vs = _rows(v, heads, "v")
-    _same_rows(rows, k, "k")
-    _same_rows(rows, v, "v")
-    _buf(cu_seqlens, torch.int32, (None,), "cu_seqlens")
-    if cu_seqlens.shape[0] < 1:
+    i32, bf16 = torch.int32, torch.bfloat16
+    rows, q_heads, _ = _shape(q, 3, "q")
+    heads = _shape(k, 3, "k")[1]
+    _heads(q_heads, heads)
+    qp, qs = _rows(q, rows, q_heads, bf16, "q")
+    kp, ks = _rows(k, rows, heads, bf16, "k")
+    vp, vs = _rows(v, rows, heads, bf16, "v")
+    ends, = _shape(cu_seqlens, 1, "cu_seqlens")
+    if ends < 1:
         raise ValueError("cu_seqlens must have at least one entry")
+    cu = _at(cu_seqlens, i32, (ends,), "cu_seqlens")
     if out is None:
-        out = _empty((rows, q_heads, KV_DIM), torch.bfloat16, q.device, stream)
-    else:
-        _buf(out, torch.bfloat16, (rows, q_heads, KV_DIM), "out")
+        out = _empty((rows, q_heads, KV_DIM), bf16, q.device, stream)
     st = load_library().hlwq_prompt_attention(
-        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(cu_seqlens), cu_seqlens.shape[0] - 1, rows, q_heads, heads, KV_DIM,
-        1 / math.sqrt(KV_DIM) if scale is None else scale, _ptr(out), _stream_handle(stream, q, k, v, cu_seqlens, out))
-    _check("hlwq_prompt_attention", st)
+        qp, qs, kp, ks, vp, vs, cu, ends - 1, rows, q_heads, heads, KV_DIM, 0.0625 if scale is None else scale,
+        _at(out, bf16, (rows, q_heads, KV_DIM), "out"), _stream(stream, (q, k, v, cu_seqlens, out)))
+    if st:
+        _check("hlwq_prompt_attention", st)
     return out
