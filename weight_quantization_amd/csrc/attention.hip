@@ -187,6 +187,7 @@ int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q
   a.n_pages = static_cast<int32_t>(c->n_pages);
   a.page_shift = __builtin_ctzll(static_cast<uint64_t>(c->page_size));
   a.scale = scale;
+  a.factor = std::fmax(std::fabs(scale) * kLog2e, __FLT_DENORM_MIN__);
   return launch_paged(c->bits, a, ws, stream);
 }
 
@@ -229,6 +230,7 @@ int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
   a.kv_heads = static_cast<int32_t>(kv_heads);
   a.group = static_cast<int32_t>(q_heads / kv_heads);
   a.scale = scale;
+  a.factor = std::fmax(std::fabs(scale) * kLog2e, __FLT_DENORM_MIN__);
   return launch_prompt(a, stream);
 }
 

@@ -1,11 +1,11 @@
 // attention_chunk.h — attention of many new tokens over a paged cache: the tile
 // kernel of attention_tile.h with a first phase over pages of codes.
 //
-// Pages are worked on in the rotated domain (attention_split.h): the 512
-// work-items unpack 64 tokens' codes into LDS as fp16 centroids while the
-// previous 64 are multiplied, so that 256 query rows share one unpacking; then
-// the sums are rotated in registers and the window's and the step's own tokens
-// follow in bf16.
+// Pages are worked on in the rotated domain (attention_split.h): the codes of 64
+// tokens go to LDS as they are, the 512 work-items unpack them there to fp16
+// centroids while the 64 before are multiplied, so that 256 query rows share
+// one unpacking; then the sums are rotated in registers and the window's and
+// the step's own tokens follow in bf16.
 #pragma once
 
 #include "attention_split.h"
@@ -71,246 +71,334 @@ __device__ __forceinline__ u32x4 run_chunk(const Run<BITS>& r, int g) {
   return u32x4{a[0], a[1], b[0], b[1]};
 }
 
+// Where a lane's row of the tile stands: the wave's 32 rows begin at w0 of the
+// request's `rows`.  Worked out anew for each phase from a lane number that the
+// compiler cannot follow, as what it would keep between them costs registers
+// that the loops need.
+struct ChunkRow {
+  int lane, col, h;
+  int32_t tok, q_head;
+  __device__ __forceinline__ ChunkRow(const AttnArgs& a, int32_t head, int32_t w0, int32_t rows) {
+    lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    col = lane & 31;
+    h = lane >> 5;
+    const int32_t row = min(w0 + col, rows - 1);
+    tok = token_of(row, a.group);
+    q_head = head * a.group + (row - tok * a.group);
+  }
+  __device__ __forceinline__ const uint16_t* q(const AttnArgs& a, int32_t begin) const {
+    return a.q + (begin + static_cast<int64_t>(tok)) * a.q_stride + q_head * kDim + 8 * h;
+  }
+};
+
+// LDS of the chunk kernel: two stages of 64 tokens' K and V (fp16 or bf16), two
+// of their packed codes, and of their norms as they are in memory, four of the
+// ids of their pages, and for each stage the K norms, the V norms, whether some
+// token is missing and the V norms' exponent.
+template <int BITS>
+struct ChunkLds {
+  static constexpr uint32_t kStage = kChunkBlock * 1024, kCodes = kChunkBlock * 32 * BITS, kLine = kChunkBlock * 4;
+  static constexpr uint32_t kSide = 2 * kLine + 16;
+  static constexpr uint32_t raw = 2 * kStage, norms = raw + 4 * kCodes, ids = norms + 4 * kLine, side = ids + 4 * kLine,
+                            flag = side + 2 * kSide, bytes = flag + 16;
+};
+
+// Vector of token t, which lies in page `id` of its request.
+__device__ __forceinline__ int64_t place(const AttnArgs& a, int32_t head, int32_t id, int32_t t) {
+  int32_t zero;  // for the upper half: one that the compiler does not keep
+  asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
+  int64_t at = ((static_cast<int64_t>(id) * a.kv_heads + head) << a.page_shift) +
+               (static_cast<int64_t>(zero) << 32 | static_cast<uint32_t>(t & ((1 << a.page_shift) - 1)));
+  asm volatile("" : "+v"(at));
+  return at;
+}
+
+// The lane's number, which the compiler takes for a new one each time: what it
+// computes from it stays in no register from one use to the next.
+__device__ __forceinline__ int lane_now() {
+  int lane;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane));
+  return lane;
+}
+
+// Pages [u0, u1) of 64 tokens.  At block u the page ids of u + 3 and the codes
+// and norms of u + 2 are on their way to LDS, those of u + 1 are unpacked, and
+// u is multiplied; the lower waves unpack before they multiply, the upper ones
+// (on the same SIMDs) after, so that one's VALU work meets the other's products.
+// Whatever a lane would keep from block to block is in LDS: the sums, the query
+// and the step's operands fill the registers, and one reload from scratch
+// memory waits for every load that is under way.
+template <int BITS>
+__device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Extent& e, int32_t b, int32_t head, int32_t w0, int32_t u0,
+                                            int32_t u1, uint32_t base, int wave) {
+  using L = ChunkLds<BITS>;
+  constexpr int KT = kChunkBlock, kWaves = 2 * BITS;  // waves that fetch codes: 16 bytes a lane
+  const int32_t rows = e.n * a.group;
+  const int32_t paged = static_cast<int32_t>(e.paged);  // at most 2^20 pages of 2^8 tokens
+  const int32_t* const table = a.table + static_cast<int64_t>(b) * a.width;
+  // lane = token of the block
+  const auto ids = [&](int32_t u) {
+    if (u < u1 && wave == 6)
+      stage4(table + (min(u * KT + lane_now(), paged - 1) >> a.page_shift), base + L::ids + (u & 3) * L::kLine);
+  };
+  const auto id_of = [&](int32_t u, int token) {
+    const int32_t id = lds_at<int32_t>(base + L::ids + (u & 3) * L::kLine + 4 * token);
+    return u * KT + token < paged && id < a.n_pages ? id : -1;
+  };
+  // Waves 0 .. 2 BITS - 1 fetch 1 KB of K codes and of V codes each, lane by
+  // lane 16 bytes of a token; waves 6 and 7 the norms of token `lane`, K and V.
+  // Of a page that is not there the first one's, which no row comes to see.
+  const auto fetch = [&](int32_t u) {
+    if (u >= u1) return;
+    const int lane = lane_now();
+    if (wave < kWaves) {
+      const int piece = wave * 64 + lane, token = piece / (2 * BITS), part = piece - token * (2 * BITS);
+      const int64_t vec = place(a, head, max(id_of(u, token), 0), u * KT + token) * (32 * BITS) + 16 * part;
+      const uint32_t to = base + L::raw + (u & 1) * 2 * L::kCodes + wave * 1024;
+      stage16(a.k_packed + vec, to);
+      stage16(a.v_packed + vec, to + L::kCodes);
+    }
+    if (wave >= 6)
+      stage2((wave == 6 ? a.k_norms : a.v_norms) + place(a, head, max(id_of(u, lane), 0), u * KT + lane),
+             base + L::norms + ((u & 1) * 2 + wave - 6) * L::kLine);
+  };
+  const auto norms = [&](int32_t u, int exponent) {
+    if (u >= u1 || wave < 6) return;
+    const int lane = lane_now();
+    const uint32_t side = base + L::side + (u & 1) * L::kSide;
+    const bool there = id_of(u, lane) >= 0;
+    const float n = f16_value(static_cast<uint16_t>(lds_at<uint32_t>(base + L::norms + ((u & 1) * 2 + wave - 6) * L::kLine + 4 * lane)));
+    if (wave == 6) {
+      lds_put<float>(side + 4 * lane, there ? n : -1.0f);
+      const bool all = __all(there);
+      if (lane == 0) lds_put<uint32_t>(side + 2 * L::kLine, !all);
+    } else {
+      // as in code_step: norms over a power of two that none met so far exceeds
+      const float top = wave_max(there ? n : 0.0f);
+      if (top > __builtin_ldexpf(1.0f, exponent)) exponent = __builtin_amdgcn_frexp_expf(top);
+      lds_put<float>(side + L::kLine + 4 * lane, there ? __builtin_ldexpf(n, -exponent) : 0.0f);
+      if (lane == 0) lds_put<int32_t>(side + 2 * L::kLine + 4, exponent);
+    }
+  };
+  const auto exponent_of = [&](int32_t u) {
+    return __builtin_amdgcn_readfirstlane(lds_at<int32_t>(base + L::side + (u & 1) * L::kSide + 2 * L::kLine + 4));
+  };
+  // lane = token of the block, wave = which 32 of its 256 codes
+  const auto unpack = [&](int32_t u) {
+    if (u >= u1) return;
+    const int lane = lane_now();
+    const uint32_t raw = base + L::raw + (u & 1) * 2 * L::kCodes + lane * 32 * BITS + wave * 4 * BITS;
+    const uint32_t to = base + (u & 1) * L::kStage + lane * 512 + ((4 * wave) ^ swizzle(lane)) * 16;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      Run<BITS> codes;
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) codes.w[i] = lds_at<uint32_t>(raw + side * L::kCodes + 4 * i);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) lds_put<u32x4>((to ^ (x * 16)) + side * KT * 512, run_chunk<BITS>(codes, x));
+    }
+  };
+  ids(u0);
+  ids(u0 + 1);
+  ids(u0 + 2);
+  wait_staged();
+  barrier();
+  fetch(u0);
+  fetch(u0 + 1);
+  // q rotated, over a power of two that brings the row's largest value to
+  // [1, 2), as fp16
+  u32x4 q[16];
+  float factor;
+  {
+    float x[128];
+    const uint16_t* qp = ChunkRow(a, head, w0, rows).q(a, e.begin);
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(qp + 16 * s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[8 * s + 2 * j] = bf16_lo(v[j]);
+        x[8 * s + 2 * j + 1] = bf16_hi(v[j]);
+      }
+    }
+    fwht_halves(x);
+    float mx = 0;
+#pragma unroll
+    for (int i = 0; i < 128; ++i) mx = fmaxf(mx, fabsf(x[i]));
+    mx = fmaxf(mx, half_swap(mx));
+    const int ex = mx > 0 ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
+    const float f = __builtin_ldexpf(a.scale < 0 ? -1.0f : 1.0f, -ex);
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[s][j] = pack_f16x2(x[8 * s + 2 * j] * f, x[8 * s + 2 * j + 1] * f);
+    factor = fmaxf(__builtin_ldexpf(a.factor, ex - 8), __FLT_DENORM_MIN__);
+  }
+  clear(r);
+  wait_staged();
+  barrier();
+  norms(u0, -64);
+  unpack(u0);
+  int scaled = -64;
+  const bool first_half = wave < 4, idle = w0 >= rows;
+  TileLane at = tile_lane(lane_now());
+  asm volatile("" : "+v"(at.k), "+v"(at.v));
+  for (int32_t u = u0; u < u1; ++u) {
+    wait_staged();
+    wait_lds();
+    barrier();
+    const int ex = exponent_of(u);
+    norms(u + 1, ex);
+    fetch(u + 2);
+    ids(u + 3);
+#pragma clang loop unroll(disable)
+    for (int turn = 0; turn < 2; ++turn) {
+      if (first_half == (turn == 0)) {
+        unpack(u + 1);
+        continue;
+      }
+      if (idle) continue;
+      const uint32_t side = base + L::side + (u & 1) * L::kSide;
+      const bool masked = __builtin_amdgcn_readfirstlane(lds_at<uint32_t>(side + 2 * L::kLine)) != 0;
+      if (ex != scaled) {
+        scale_rows(r, __builtin_ldexpf(1.0f, max(scaled - ex, -126)));
+        scaled = ex;
+      }
+#pragma unroll
+      for (int s = 0; s < KT / 32; ++s) {
+        uint32_t kb = base + (u & 1) * L::kStage + s * 16384;
+        asm volatile("" : "+s"(kb));  // 16 addresses of each step are not kept
+        key_step<true>(r, q, kb + at.k, kb + KT * 512 + at.v, factor, 0, masked, side + 128 * s, side + L::kLine + 128 * s, lane_now());
+      }
+    }
+  }
+  // the sums over centroids, rotated
+  float x[128];
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[16 * t + i] = r.o[t][i];
+  fwht_halves(x);
+  const float f = __builtin_ldexpf(1.0f, scaled - 8);
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r.o[t][i] = x[16 * t + i] * f;
+}
+
+// The window's and the step's own tokens, blocks [from, to) of 64 of them.
+template <int BITS>
+__device__ __forceinline__ void chunk_tokens(Rows& r, const AttnArgs& a, const Extent& e, int32_t b, int32_t head, int32_t w0,
+                                             int64_t end_key, int32_t from, int32_t to, uint32_t base, int wave) {
+  using L = ChunkLds<BITS>;
+  constexpr int KT = kChunkBlock;
+  const int32_t rows = e.n * a.group;
+  const ChunkRow row(a, head, w0, rows);
+  const TileLane at = tile_lane(row.lane);
+  const Tokens tokens(a, e, b, head);
+  // the keys that all rows see; the last that the wave's first row sees, and its last row
+  const int64_t seen = tokens.near + token_of(w0 - 32 * wave, a.group) + 1;
+  const int64_t first_key = tokens.near + token_of(min(w0, rows - 1), a.group);
+  const int64_t last_key = w0 >= rows ? -1 : tokens.near + token_of(min(w0 + 31, rows - 1), a.group);
+  const auto stage = [&](int buf, int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < KT / 16; ++i) {
+      const int pair = 16 * i + 2 * wave;
+      const int64_t k = t0 + pair + row.h;
+      const uint32_t c = (row.col ^ swizzle(2 * wave + row.h)) * 8;
+      stage16(tokens.at(0, k, end_key) + c, base + buf * L::kStage + pair * 512);
+      stage16(tokens.at(1, k, end_key) + c, base + buf * L::kStage + KT * 512 + pair * 512);
+    }
+  };
+  if (threadIdx.x == 0) lds_put<uint32_t>(base + L::flag, 0);
+  wait_lds();
+  stage(0, static_cast<int64_t>(from) * KT);
+  u32x4 q[16];
+  const uint16_t* qp = row.q(a, e.begin);
+#pragma unroll
+  for (int s = 0; s < 16; ++s) q[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
+#pragma unroll
+  for (int s = 0; s < 16; ++s) {
+    if (a.scale < 0) q[s] ^= 0x80008000u;
+    asm volatile("" : "+v"(q[s]));
+  }
+  for (int32_t u = from; u < to; ++u) {
+    const int buf = (u - from) & 1;
+    wait_staged();
+    barrier();
+    if (u + 1 < to) stage(buf ^ 1, static_cast<int64_t>(u + 1) * KT);
+    if (static_cast<int64_t>(u + 1) * KT > seen) leave_out_nonfinite<512, KT>(base + buf * L::kStage + KT * 512, base + L::flag);
+#pragma clang loop unroll(disable)
+    for (int s = 0; s < KT / 32; ++s) {
+      const int64_t k0 = static_cast<int64_t>(u) * KT + 32 * s;
+      if (k0 > last_key) continue;
+      const uint32_t kb = base + buf * L::kStage + s * 16384;
+      key_step<false>(r, q, kb + at.k, kb + KT * 512 + at.v, a.factor,
+                      static_cast<int>(min(tokens.near + row.tok - k0, int64_t{64})), k0 + 31 > first_key, 0, 0, row.lane);
+    }
+  }
+  add_nonfinite(r, base + L::flag, max(seen / KT * KT, static_cast<int64_t>(from) * KT), min(last_key, static_cast<int64_t>(to) * KT - 1),
+                tokens.near + row.tok, row.h, [&](int64_t key) { return tokens.at(1, key, end_key); });
+}
+
 template <int BITS>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) hlwq_chunk_attention_kernel(const AttnArgs a) {
   constexpr int M = kChunkRows, KT = kChunkBlock;
-  constexpr uint32_t kStage = KT * 1024;
-  // two stages of K and V, then for each: K norms, V norms, {some token missing, V's exponent}
-  constexpr uint32_t kSide = 2 * KT * 4 + 16;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage + 2 * kSide];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 31, h = lane >> 5;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ChunkLds<BITS>::bytes];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
-  const TileLane at = tile_lane(lane);
 
   const auto cost = [&](const Extent& e) { return Work<M, KT>(a, e).head_cost() * a.kv_heads; };
   Finder<decltype(cost), Nothing> finder(a, cost, Nothing{});
   const Share share(finder.total, a.workers, kChunkLeast);
-  if (finder.total == 0 || blockIdx.x >= share.workers) return;
+  if (finder.total == 0 || static_cast<int32_t>(blockIdx.x) >= share.workers) return;
   // Workgroups of one XCD (every eighth) take neighbouring stretches, which
   // share a KV head's keys in its L2.
   const int32_t worker = share.workers % 8 == 0 ? (blockIdx.x % 8) * (share.workers / 8) + blockIdx.x / 8 : blockIdx.x;
   const Found first = finder.find(share.bound(worker));
 
   for_segments<M, KT>(a, share, first, worker, [&](const Work<M, KT>& w, const Segment& g) {
-    const Extent& e = w.e;
     const int32_t rows = w.rows(a), w0 = g.tile * M + 32 * wave;
     const int32_t blocks = w.blocks(a, g.tile);
     const int32_t u0 = w.block_at(g.from, blocks, g.cost), u1 = w.block_at(g.to, blocks, g.cost);
-    const int64_t near = e.held - e.enc;
-    const int32_t tok = token_of(min(w0 + col, rows - 1), a.group);
-    const auto q_head = [&]() { return g.head * a.group + (min(w0 + col, rows - 1) - tok * a.group); };
-    const auto q_ptr = [&]() { return a.q + (e.begin + static_cast<int64_t>(tok)) * a.q_stride + q_head() * kDim + 8 * h; };
     Rows r;
     r.m = -FLT_MAX;
     r.l = 0;
-    r.left = 0;
-    const bool idle = w0 >= rows;  // none of the wave's rows exists: it only stages
-
     if (u0 < w.page_blocks && u0 < u1) {
-      const int64_t end = min(u1, w.page_blocks);
-      // lane = token of the block, wave = which 32 of its 256 codes; wave 0 has
-      // the K norms, wave 1 the V norms
-      const auto page_of = [&](int64_t u) {
-        const int64_t t = u * KT + lane;
-        return t < e.paged ? a.table[static_cast<int64_t>(g.b) * a.width + (t >> a.page_shift)] : -1;
-      };
-      Run<BITS> ck, cv;
-      uint16_t norm = 0;
-      bool there = false;
-      const auto fetch = [&](int64_t u, int32_t id) {
-        there = id >= 0 && id < a.n_pages;
-        const int64_t vec = (((there ? static_cast<int64_t>(id) : 0) * a.kv_heads + g.head) << a.page_shift) +
-                            ((u * KT + lane) & ((1 << a.page_shift) - 1));
-        const uint32_t* kp = reinterpret_cast<const uint32_t*>(a.k_packed + vec * (32 * BITS)) + BITS * wave;
-        const uint32_t* vp = reinterpret_cast<const uint32_t*>(a.v_packed + vec * (32 * BITS)) + BITS * wave;
-        if constexpr (BITS == 3) {
-          const u32x3_4 k = *reinterpret_cast<const u32x3_4*>(kp), v = *reinterpret_cast<const u32x3_4*>(vp);
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            ck.w[i] = k[i];
-            cv.w[i] = v[i];
-          }
-        } else {
-          const u32x2 k = *reinterpret_cast<const u32x2*>(kp), v = *reinterpret_cast<const u32x2*>(vp);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            ck.w[i] = k[i];
-            cv.w[i] = v[i];
-          }
-        }
-        if (wave == 0) norm = a.k_norms[vec];
-        if (wave == 1) norm = a.v_norms[vec];
-      };
-      int exponent = -64;  // wave 1's
-      const auto unpack = [&](int buf) {
-        const uint32_t k = base + buf * kStage + lane * 512, v = k + KT * 512;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t c = ((4 * wave + x) ^ swizzle(lane)) * 16;
-          *reinterpret_cast<lds_u32x4*>(static_cast<uintptr_t>(k + c)) = run_chunk<BITS>(ck, x);
-          *reinterpret_cast<lds_u32x4*>(static_cast<uintptr_t>(v + c)) = run_chunk<BITS>(cv, x);
-        }
-        const uint32_t side = base + 2 * kStage + buf * kSide;
-        if (wave == 0) {
-          *reinterpret_cast<lds_f32*>(static_cast<uintptr_t>(side + 4 * lane)) = there ? f16_value(norm) : -1.0f;
-          const bool all = __all(there);
-          if (lane == 0) *reinterpret_cast<lds_u32*>(static_cast<uintptr_t>(side + 8 * KT)) = !all;
-        }
-        if (wave == 1) {
-          // as in code_step: norms over a power of two that none met so far exceeds
-          const float n = there ? f16_value(norm) : 0.0f;
-          const float top = wave_max(n);
-          if (top > __builtin_ldexpf(1.0f, exponent)) exponent = __builtin_amdgcn_frexp_expf(top);
-          *reinterpret_cast<lds_f32*>(static_cast<uintptr_t>(side + 4 * KT + 4 * lane)) = __builtin_ldexpf(n, -exponent);
-          if (lane == 0) *reinterpret_cast<lds_u32*>(static_cast<uintptr_t>(side + 8 * KT + 4)) = exponent;
-        }
-      };
-      fetch(u0, page_of(u0));
-      int32_t id = u0 + 1 < end ? page_of(u0 + 1) : -1;
-
-      // q rotated, over a power of two that brings the row's largest value to
-      // [1, 2), as fp16
-      u32x4 q[16];
-      float factor;
-      {
-        float x[128];
-        const uint16_t* qp = q_ptr();
-#pragma unroll
-        for (int s = 0; s < 16; ++s) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(qp + 16 * s);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[8 * s + 2 * j] = bf16_lo(v[j]);
-            x[8 * s + 2 * j + 1] = bf16_hi(v[j]);
-          }
-        }
-        fwht_halves(x);
-        float mx = 0;
-#pragma unroll
-        for (int i = 0; i < 128; ++i) mx = fmaxf(mx, fabsf(x[i]));
-        mx = fmaxf(mx, half_swap(mx));
-        const int ex = mx > 0 ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
-        const float f = __builtin_ldexpf(a.scale < 0 ? -1.0f : 1.0f, -ex);
-#pragma unroll
-        for (int s = 0; s < 16; ++s)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) q[s][j] = pack_f16x2(x[8 * s + 2 * j] * f, x[8 * s + 2 * j + 1] * f);
-        factor = __builtin_ldexpf(fabsf(a.scale) * kLog2e, ex - 8);
-      }
-      unpack(0);
-      clear(r);
-      int scaled = -64;
-      for (int64_t u = u0; u < end; ++u) {
-        const int buf = (u - u0) & 1;
-        if (u + 1 < end) {
-          fetch(u + 1, id);
-          if (u + 2 < end) id = page_of(u + 2);
-        }
-        wait_lds();
-        barrier();
-        if (!idle) {
-          const uint32_t side = base + 2 * kStage + buf * kSide;
-          const u32x2 info = *reinterpret_cast<const lds_u32x2*>(static_cast<uintptr_t>(side + 8 * KT));
-          const bool masked = __builtin_amdgcn_readfirstlane(info[0]) != 0;
-          const int ex = __builtin_amdgcn_readfirstlane(info[1]);
-          if (ex != scaled) {
-            scale_rows(r, __builtin_ldexpf(1.0f, max(scaled - ex, -126)));
-            scaled = ex;
-          }
-#pragma unroll
-          for (int s = 0; s < KT / 32; ++s) {
-            const uint32_t kb = base + buf * kStage + s * 16384;
-            key_step<true>(r, q, kb + at.k, kb + KT * 512 + at.v, factor, 0, masked, side + 128 * s, side + 4 * KT + 128 * s, lane);
-          }
-        }
-        if (u + 1 < end) unpack(buf ^ 1);
-      }
-      // the sums over centroids, rotated
-      float x[128];
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[16 * t + i] = r.o[t][i];
-      fwht_halves(x);
-      const float f = __builtin_ldexpf(1.0f, scaled - 8);
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) r.o[t][i] = x[16 * t + i] * f;
+      chunk_pages<BITS>(r, a, w.e, g.b, g.head, w0, u0, min(u1, w.page_blocks), base, wave);
       barrier();  // every wave is done with LDS
     } else {
       clear(r);
     }
-
     if (u1 > w.page_blocks) {
-      const int64_t from = max(u0, w.page_blocks) - w.page_blocks, to = u1 - w.page_blocks;
-      const int64_t first_key = near + token_of(min(w0, rows - 1), a.group);               // the last that the wave's first row sees
-      const int64_t last_key = idle ? -1 : near + token_of(min(w0 + 31, rows - 1), a.group);  // and its last
-      const int64_t end_key = near + w.last_token(a, g.tile);                      // and the tile's last
-      const Tokens tokens(a, e, g.b, g.head);
-      const auto stage = [&](int buf, int64_t t0) {
-#pragma unroll
-        for (int i = 0; i < KT / 16; ++i) {
-          const int pair = 16 * i + 2 * wave;
-          const int64_t k = t0 + pair + h;
-          const uint32_t c = (col ^ swizzle(2 * wave + h)) * 8;
-          stage16(tokens.at(0, k, end_key) + c, base + buf * kStage + pair * 512);
-          stage16(tokens.at(1, k, end_key) + c, base + buf * kStage + KT * 512 + pair * 512);
-        }
-      };
-      u32x4 q[16];
-      const uint16_t* qp = q_ptr();
-#pragma unroll
-      for (int s = 0; s < 16; ++s) q[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
-      stage(0, from * KT);
-#pragma unroll
-      for (int s = 0; s < 16; ++s) {
-        if (a.scale < 0) q[s] ^= 0x80008000u;
-        asm volatile("" : "+v"(q[s]));
-      }
-      for (int64_t u = from; u < to; ++u) {
-        const int buf = (u - from) & 1;
-        wait_staged();
-        barrier();
-        if (u + 1 < to) stage(buf ^ 1, (u + 1) * KT);
-#pragma unroll
-        for (int s = 0; s < KT / 32; ++s) {
-          const int64_t k0 = u * KT + 32 * s;
-          if (k0 > last_key) continue;
-          const uint32_t kb = base + buf * kStage + s * 16384;
-          key_step<false>(r, q, kb + at.k, kb + KT * 512 + at.v, fabsf(a.scale) * kLog2e,
-                          static_cast<int>(min(near + tok - k0, int64_t{64})), k0 + 31 > first_key, 0, 0, lane);
-        }
-      }
-      add_nonfinite(r, max((first_key + 1) / 32 * 32, from * KT), min(last_key, to * KT - 1), near + tok, h,
-                    [&](int64_t key) { return tokens.at(1, key, end_key); });
+      chunk_tokens<BITS>(r, a, w.e, g.b, g.head, w0, w.e.held - w.e.enc + w.last_token(a, g.tile),
+                         max(u0, w.page_blocks) - w.page_blocks, u1 - w.page_blocks, base, wave);
       barrier();
     }
-
     r.l += half_swap(r.l);
-    if (w0 + col < rows) {
-      if (g.from == 0 && g.to == g.cost) {
-        const float inv = 1.0f / r.l;
-        uint16_t* op = a.out + ((e.begin + static_cast<int64_t>(tok)) * a.q_heads + q_head()) * kDim;
+    const ChunkRow row(a, g.head, w0, rows);
+    if (w0 + row.col >= rows) return;
+    if (g.from == 0 && g.to == g.cost) {
+      const float inv = 1.0f / r.l;
+      uint16_t* op = a.out + ((w.e.begin + static_cast<int64_t>(row.tok)) * a.q_heads + row.q_head) * kDim + 4 * row.h;
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+      for (int t = 0; t < 8; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint2 v = {pack_bf16x2(r.o[t][4 * i] * inv, r.o[t][4 * i + 1] * inv),
-                             pack_bf16x2(r.o[t][4 * i + 2] * inv, r.o[t][4 * i + 3] * inv)};
-            *reinterpret_cast<uint2*>(op + 32 * t + 8 * i + 4 * h) = v;
-          }
-      } else {
-        const int slot = g.from > 0 ? 0 : 1, at_row = 32 * wave + col;
-        float* op = partial_row<M>(a, 2 * worker + slot, at_row);
+        for (int i = 0; i < 4; ++i) {
+          const uint2 v = {pack_bf16x2(r.o[t][4 * i] * inv, r.o[t][4 * i + 1] * inv),
+                           pack_bf16x2(r.o[t][4 * i + 2] * inv, r.o[t][4 * i + 3] * inv)};
+          *reinterpret_cast<uint2*>(op + 32 * t + 8 * i) = v;
+        }
+    } else {
+      const int slot = 2 * worker + (g.from > 0 ? 0 : 1), at_row = 32 * wave + row.col;
+      float* op = partial_row<M>(a, slot, at_row) + 4 * row.h;
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+      for (int t = 0; t < 8; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<f32x4*>(op + 32 * t + 8 * i + 4 * h) = f32x4{r.o[t][4 * i], r.o[t][4 * i + 1], r.o[t][4 * i + 2], r.o[t][4 * i + 3]};
-        if (h == 0) *partial_stat<M>(a, 2 * worker + slot, at_row) = float2{r.m, r.l};
-      }
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<f32x4*>(op + 32 * t + 8 * i) = f32x4{r.o[t][4 * i], r.o[t][4 * i + 1], r.o[t][4 * i + 2], r.o[t][4 * i + 3]};
+      if (row.h == 0) *partial_stat<M>(a, slot, at_row) = float2{r.m, r.l};
     }
   });
 }

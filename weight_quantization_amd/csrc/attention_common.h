@@ -53,7 +53,8 @@ struct AttnArgs {
   int32_t slots;    // of partial sums
   int32_t least, most;  // requests with rows * group in [least, most] are this kernel's
   int32_t cost_shift;
-  float scale;
+  float scale;   // its sign is given to the queries
+  float factor;  // |scale| log2 e, above 0: a masked score, minus infinity, stays that
 };
 
 // One request's part of a step.
@@ -265,7 +266,7 @@ struct Work {
   __device__ __forceinline__ static int32_t block_at(int32_t x, int32_t blocks, int32_t cost) {
     if (cost == blocks * kBlockCost) return x / kBlockCost;
     if (x == cost) return blocks;
-    return static_cast<int32_t>(static_cast<double>(x) * blocks / cost);
+    return __builtin_amdgcn_readfirstlane(static_cast<int32_t>(static_cast<double>(x) * blocks / cost));
   }
 };
 
@@ -322,7 +323,7 @@ __device__ __forceinline__ void for_segments(const AttnArgs& a, const Share& s, 
       continue;
     }
     const int32_t x = rest - g.head * head_cost;
-    g.tile = w.tile_at(x);
+    g.tile = __builtin_amdgcn_readfirstlane(w.tile_at(x));
     g.cost = w.cost(g.tile);
     g.from = x - w.cost_before(g.tile);
     g.to = min(g.from + left, g.cost);

@@ -561,7 +561,7 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
     const int ex = mx > 0 ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
     const float f = __builtin_ldexpf(a.scale < 0 ? -1.0f : 1.0f, -ex);
     *reinterpret_cast<uint2*>(ql + row * kQPitch + 4 * lane) = uint2{pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f)};
-    if (lane == 0) qf[row] = __builtin_ldexpf(fabsf(a.scale) * kLog2e, ex - 8);
+    if (lane == 0) qf[row] = __builtin_ldexpf(a.factor, ex - 8);
   }
   __syncthreads();
   u32x4 q[NR][8];
@@ -616,7 +616,7 @@ __device__ __forceinline__ void attend_tokens(const AttnArgs& a, const Extent& e
   SplitRows<NR> r;
   clear(r);
   for (int64_t k0 = 32 * wave; k0 <= last; k0 += kSplitBlock)
-    token_step<NR>(r, q, fabsf(a.scale) * kLog2e, k0, last, lim, k0 + 31 > first, k0 + 31 > first && first < last, tokens, lane);
+    token_step<NR>(r, q, a.factor, k0, last, lim, k0 + 31 > first, k0 + 31 > first && first < last, tokens, lane);
   join_waves<NR>(r, false, rows - r0, lds, lane, wave, write);
 }
 

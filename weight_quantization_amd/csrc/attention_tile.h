@@ -33,11 +33,22 @@ __device__ __forceinline__ u32x4 buffer_of(const void* p, int64_t bytes) {
 // stands before the barrier that publishes them (wait_staged).  M0, which
 // holds the LDS address, is used by nothing else in these kernels.
 __device__ __forceinline__ void stage16(u32x4 buffer, uint32_t offset, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer)
                : "memory");
 }
 __device__ __forceinline__ void stage16(const void* p, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+// 4 bytes, or 2 and two of zeroes: lane l's land at lds + 4 l.
+__device__ __forceinline__ void stage4(const void* p, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+__device__ __forceinline__ void stage2(const void* p, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" ::"s"(lds), "v"(p) : "memory");
 }
 __device__ __forceinline__ void wait_staged() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
@@ -45,6 +56,15 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+template <class T>
+__device__ __forceinline__ T lds_at(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) T*>(static_cast<uintptr_t>(at));
+}
+template <class T>
+__device__ __forceinline__ void lds_put(uint32_t at, T v) {
+  *reinterpret_cast<__attribute__((address_space(3))) T*>(static_cast<uintptr_t>(at)) = v;
 }
 
 // LDS tile of keys (or values): key k's 256 values in 32 chunks of 16 bytes at
@@ -57,7 +77,6 @@ __device__ __forceinline__ int swizzle(int key) { return ((key & 3) << 2) | ((ke
 struct Rows {
   f32x16 o[8];  // o[t][i]: value 32 t + 8 (i / 4) + 4 (lane / 32) + i % 4 of row lane % 32
   float m, l;   // running maximum (of scores times log2 e) and this lane's share of the sum
-  uint32_t left;  // nonzero: infinite or NaN values were left out of the sums
 };
 
 __device__ __forceinline__ void clear(Rows& r) {
@@ -82,7 +101,12 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Lane constants of the LDS reads.
+// In a rare branch: keeps the compiler from doing its work always and selecting.
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
+// Lane constants of the LDS reads.  What distinguishes the reads of a step is
+// three bits of the address, to be exclusive-ored in (they meet the swizzle),
+// and an offset that the instruction adds.
 struct TileLane {
   uint32_t k;  // chunk 0 (or 1, upper half) of key lane % 32
   uint32_t v;  // transposed read of value block 0, keys 0 .. 3 (4 .. 7, upper half)
@@ -95,15 +119,19 @@ __device__ __forceinline__ TileLane tile_lane(int lane) {
   return t;
 }
 
+// Fragment x of K for S^T's products over values 16 x .. of the 32 keys at `k`.
+__device__ __forceinline__ u32x4 k_fragment(uint32_t k, int x) {
+  return lds_at<u32x4>((k ^ ((x & 7) * 32)) + (x >> 3) * 256);
+}
+
 // Fragment x = 2 t + s of V^T for O^T's rows 32 t .. and keys 16 s .. of the 32
 // at `v`: ds_read_tr16_b64 gives lane i of sixteen the element i % 4 of the
 // four lanes i / 4 + 4 j, so with lane r pointing at key r / 4, values 4 (r %
 // 4) .. the lane gets value i of four keys.
 __device__ __forceinline__ u32x4 v_fragment(uint32_t v, int x) {
-  const int t = x >> 1, s = x & 1;
-  const uint32_t ad = (v ^ ((t & 3) << 6)) + (t >> 2) * 256 + s * 8192;
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)static_cast<uintptr_t>(ad));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)static_cast<uintptr_t>((ad ^ 32) + 4096));
+  const int t = x >> 1, off = (t >> 2) * 256 + (x & 1) * 8192;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)static_cast<uintptr_t>((v ^ ((t & 3) * 64)) + off));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)static_cast<uintptr_t>((v ^ ((t & 3) * 64 + 32)) + (off + 4096)));
   return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -117,15 +145,13 @@ __device__ __forceinline__ u32x4 v_fragment(uint32_t v, int x) {
 template <bool ENC>
 __device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t k, uint32_t v, float factor,
                                          int lim, bool masked, uint32_t kn, uint32_t vn, int lane) {
-  constexpr int PK = 3, PV = 2;  // fragments in flight: what fits the registers beside the sums
+  constexpr int PK = 3, PV = 3;  // fragments in flight: what fits the registers beside the sums
   const int h = lane >> 5;
   f32x16 s;
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] = 0;
   u32x4 kf[PK];
-  const auto k_read = [&](int x) {
-    kf[x % PK] = *reinterpret_cast<const lds_u32x4*>(static_cast<uintptr_t>((k ^ ((x & 7) * 32)) + (x >> 3) * 256));
-  };
+  const auto k_read = [&](int x) { kf[x % PK] = k_fragment(k, x); };
 #pragma unroll
   for (int x = 0; x < PK; ++x) k_read(x);
   __builtin_amdgcn_sched_group_barrier(0x100, PK, 0);
@@ -138,26 +164,30 @@ __device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
   }
-  u32x4 vf[PV];
-  if constexpr (ENC) {
-#pragma unroll
-    for (int x = 0; x < PV; ++x) vf[x] = v_fragment(v, x);
-    __builtin_amdgcn_sched_group_barrier(0x100, 2 * PV, 0);
-  }
   // score i of a lane is key 8 (i / 4) + 4 h + i % 4
   if constexpr (ENC) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const f32x4 n = *reinterpret_cast<const lds_f32x4*>(static_cast<uintptr_t>(kn + 32 * i + 16 * h));
+      const f32x4 n = lds_at<f32x4>(kn + 32 * i + 16 * h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         s[4 * i + j] *= n[j];
-        if (masked) s[4 * i + j] = n[j] < 0 ? -FLT_MAX : s[4 * i + j];
+      }
+    }
+    if (masked) {
+      keep_branch();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 n = lds_at<f32x4>(kn + 32 * i + 16 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[4 * i + j] = n[j] < 0 ? -HUGE_VALF : s[4 * i + j];
       }
     }
   } else if (masked) {
+    int mine = lim - 4 * h;
+    asm volatile("" : "+v"(mine));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + 4 * h + i % 4 > lim ? -FLT_MAX : s[i];
+    for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + i % 4 > mine ? -HUGE_VALF : s[i];
   }
   float mx = s[0];
 #pragma unroll
@@ -173,67 +203,67 @@ __device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t
   float p[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) p[i] = fast_exp2(__builtin_fmaf(s[i], factor, -r.m));
-  if constexpr (!ENC) {
-    // a score of -FLT_MAX is no 0 where the factor is 0 or the maximum too
-    if (masked) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) p[i] = 8 * (i / 4) + 4 * h + i % 4 > lim ? 0.0f : p[i];
-    }
-  }
+  u32x4 pf[2];
   if constexpr (ENC) {
-    u32x4 pf[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (masked) {
-        const f32x4 n = *reinterpret_cast<const lds_f32x4*>(static_cast<uintptr_t>(kn + 32 * i + 16 * h));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[4 * i + j] = n[j] < 0 ? 0.0f : p[4 * i + j];
-      }
-      const f32x4 n = *reinterpret_cast<const lds_f32x4*>(static_cast<uintptr_t>(vn + 32 * i + 16 * h));
+      const f32x4 n = lds_at<f32x4>(vn + 32 * i + 16 * h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) r.l += p[4 * i + j];
       pf[i >> 1][2 * (i & 1)] = pack_f16x2(p[4 * i] * n[0], p[4 * i + 1] * n[1]);
       pf[i >> 1][2 * (i & 1) + 1] = pack_f16x2(p[4 * i + 2] * n[2], p[4 * i + 3] * n[3]);
     }
-#pragma unroll
-    for (int x = 0; x < 16; ++x) {
-      r.o[x >> 1] = mfma32<true>(vf[x % PV], pf[x & 1], r.o[x >> 1]);
-      __builtin_amdgcn_sched_group_barrier(0x8, 1, 1);
-      if (x + PV < 16) {
-        vf[x % PV] = v_fragment(v, x + PV);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
-      }
-    }
   } else {
-    u32x4 pf[2];
 #pragma unroll
     for (int i = 0; i < 16; ++i) r.l += p[i];
 #pragma unroll
     for (int i = 0; i < 8; ++i) pf[i >> 2][i & 3] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+  }
+  u32x4 vf[PV];
 #pragma unroll
-    for (int x = 0; x < PV; ++x) vf[x] = v_fragment(v, x);
+  for (int x = 0; x < PV; ++x) vf[x] = v_fragment(v, x);
 #pragma unroll
-    for (int x = 0; x < 16; ++x) {
-      u32x4 f = vf[x % PV];
-      if (x + PV < 16) vf[x % PV] = v_fragment(v, x + PV);
-      // a masked key's value times its probability 0 is NaN where the value is
-      // infinite or NaN: in these steps such values are left out, and added at
-      // the end to the rows that see them (add_nonfinite)
-      if (masked) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = finite_pair(f[j], r.left);
-      }
-      r.o[x >> 1] = mfma32<false>(f, pf[x & 1], r.o[x >> 1]);
+  for (int x = 0; x < 16; ++x) {
+    r.o[x >> 1] = mfma32<ENC>(vf[x % PV], pf[x & 1], r.o[x >> 1]);
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 1);
+    if (x + PV < 16) {
+      vf[x % PV] = v_fragment(v, x + PV);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
     }
   }
 }
 
-// The infinite and NaN values that the masked steps left out, of keys [from,
-// to]: added to the row if it sees their key (key <= lim).  value(key): the
-// key's 256 values in memory.
+// A masked key's value times its probability 0 is NaN where the value is
+// infinite or NaN.  So before a block of `keys` values of which some row does
+// not see some is worked on, the workgroup's T threads set such values in LDS
+// to zero, with a note at `flag`; they are added at the end to the rows that
+// see them (add_nonfinite).  (A branch to that work at each fragment of the
+// products takes longer: few of the blocks are masked, but none of the others
+// could then be scheduled as a whole.)
+template <int T, int KEYS>
+__device__ __forceinline__ void leave_out_nonfinite(uint32_t values, uint32_t flag) {
+#pragma unroll
+  for (int i = 0; i < KEYS * 32 / T; ++i) {
+    const uint32_t at = values + (i * T + threadIdx.x) * 16;
+    u32x4 v = lds_at<u32x4>(at);
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = finite_pair(v[j], any);
+    if (any != 0) {
+      lds_put<u32x4>(at, v);
+      lds_put<uint32_t>(flag, 1);
+    }
+  }
+  wait_lds();
+  barrier();
+}
+
+// The infinite and NaN values that were left out, of keys [from, to]: added to
+// the row if it sees their key (key <= lim).  value(key): the key's 256 values
+// in memory.
 template <class F>
-__device__ __forceinline__ void add_nonfinite(Rows& r, int64_t from, int64_t to, int64_t lim, int h, F value) {
-  if (!__any(r.left != 0)) return;
+__device__ __forceinline__ void add_nonfinite(Rows& r, uint32_t flag, int64_t from, int64_t to, int64_t lim, int h, F value) {
+  if (__builtin_amdgcn_readfirstlane(lds_at<uint32_t>(flag)) == 0) return;
   for (int64_t key = from; key <= to; ++key) {
     const uint16_t* p = value(key);
 #pragma unroll
@@ -259,7 +289,7 @@ template <int NW, int KT>
 __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) hlwq_prompt_attention_kernel(const AttnArgs a) {
   constexpr int kRows = 32 * NW;
   constexpr uint32_t kStage = KT * 1024;  // K and V of one stage
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage + 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, h = lane >> 5;
   const int head = blockIdx.x % a.kv_heads;
@@ -275,6 +305,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
   // tokens of the lane's row, of the wave's first and last, of the tile's last
   const int32_t tok = token_of(min(w0 + col, rows - 1), g);
   const auto q_head = [&]() { return head * g + (min(w0 + col, rows - 1) - tok * g); };
+  const int32_t seen = token_of(r0, g) + 1;  // keys that every row of the tile sees
   const int32_t first = token_of(min(w0, rows - 1), g), last = w0 < rows ? token_of(min(w0 + 31, rows - 1), g) : -1;
   const int32_t end = token_of(min(r0 + kRows - 1, rows - 1), g) + 1;
 
@@ -288,8 +319,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
   clear(r);
   r.m = -FLT_MAX;
   r.l = 0;
-  r.left = 0;
-  const float factor = fabsf(a.scale) * kLog2e;
+  const float factor = a.factor;
 
   // Stage i of a wave's KT / (2 NW): keys 2 NW i + 2 wave and the one after,
   // 512 bytes each, lane l the chunk that belongs in place l % 32.  Rows past
@@ -312,6 +342,9 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
     }
   };
   const TileLane at = tile_lane(lane);
+  const uint32_t flag = base + 2 * kStage;
+  if (threadIdx.x == 0) lds_put<uint32_t>(flag, 0);
+  wait_lds();
   stage(0, 0);
   // settle Q before the loop (and turn it round for a negative scale), so that
   // no wait on its loads stands inside
@@ -324,6 +357,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
     wait_staged();
     barrier();
     if (t0 + KT < end) stage(buf ^ 1, t0 + KT);
+    if (t0 + KT > seen) leave_out_nonfinite<64 * NW, KT>(base + buf * kStage + KT * 512, flag);
 #pragma unroll
     for (int u = 0; u < KT / 32; ++u) {
       const int32_t k0 = t0 + 32 * u;
@@ -332,7 +366,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
       key_step<false>(r, q, kb + at.k, vb + at.v, factor, tok - k0, k0 + 31 > first, 0, 0, lane);
     }
   }
-  add_nonfinite(r, (first + 1) / 32 * 32, last, tok, h, [&](int64_t key) {
+  add_nonfinite(r, flag, seen / KT * KT, last, tok, h, [&](int64_t key) {
     return a.v_new + (begin + key) * a.v_stride + head * kDim;
   });
   r.l += half_swap(r.l);
