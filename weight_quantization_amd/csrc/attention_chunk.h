@@ -114,14 +114,6 @@ __device__ __forceinline__ int64_t place(const AttnArgs& a, int32_t head, int32_
   return at;
 }
 
-// The lane's number, which the compiler takes for a new one each time: what it
-// computes from it stays in no register from one use to the next.
-__device__ __forceinline__ int lane_now() {
-  int lane;
-  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane));
-  return lane;
-}
-
 // Pages [u0, u1) of 64 tokens.  At block u the page ids of u + 3 and the codes
 // and norms of u + 2 are on their way to LDS, those of u + 1 are unpacked, and
 // u is multiplied; the lower waves unpack before they multiply, the upper ones
@@ -269,7 +261,7 @@ __device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Ex
       for (int s = 0; s < KT / 32; ++s) {
         uint32_t kb = base + (u & 1) * L::kStage + s * 16384;
         asm volatile("" : "+s"(kb));  // 16 addresses of each step are not kept
-        key_step<true>(r, q, kb + at.k, kb + KT * 512 + at.v, factor, 0, masked, side + 128 * s, side + L::kLine + 128 * s, lane_now());
+        key_step<true>(r, q, kb + at.k, kb + KT * 512 + at.v, factor, 0, masked, side + 128 * s, side + L::kLine + 128 * s);
       }
     }
   }
@@ -335,7 +327,7 @@ __device__ __forceinline__ void chunk_tokens(Rows& r, const AttnArgs& a, const E
       if (k0 > last_key) continue;
       const uint32_t kb = base + buf * L::kStage + s * 16384;
       key_step<false>(r, q, kb + at.k, kb + KT * 512 + at.v, a.factor,
-                      static_cast<int>(min(tokens.near + row.tok - k0, int64_t{64})), k0 + 31 > first_key, 0, 0, row.lane);
+                      static_cast<int>(min(tokens.near + row.tok - k0, int64_t{64})), k0 + 31 > first_key, 0, 0);
     }
   }
   add_nonfinite(r, base + L::flag, max(seen / KT * KT, static_cast<int64_t>(from) * KT), min(last_key, static_cast<int64_t>(to) * KT - 1),

@@ -101,6 +101,14 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// The lane's number, which the compiler takes for a new one each time: what it
+// computes from it stays in no register from one use to the next.
+__device__ __forceinline__ int lane_now() {
+  int lane;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane));
+  return lane;
+}
+
 // In a rare branch: keeps the compiler from doing its work always and selecting.
 __device__ __forceinline__ void keep_branch() { asm volatile(""); }
 
@@ -144,9 +152,8 @@ __device__ __forceinline__ u32x4 v_fragment(uint32_t v, int x) {
 // factor turns a product into a score times log2 e.
 template <bool ENC>
 __device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t k, uint32_t v, float factor,
-                                         int lim, bool masked, uint32_t kn, uint32_t vn, int lane) {
-  constexpr int PK = 3, PV = 3;  // fragments in flight: what fits the registers beside the sums
-  const int h = lane >> 5;
+                                         int lim, bool masked, uint32_t kn, uint32_t vn) {
+  constexpr int PK = 4, PV = 4;  // fragments in flight: what fits the registers beside the sums
   f32x16 s;
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] = 0;
@@ -166,6 +173,7 @@ __device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t
   }
   // score i of a lane is key 8 (i / 4) + 4 h + i % 4
   if constexpr (ENC) {
+    const int h = lane_now() >> 5;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4 n = lds_at<f32x4>(kn + 32 * i + 16 * h);
@@ -184,8 +192,7 @@ __device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t
       }
     }
   } else if (masked) {
-    int mine = lim - 4 * h;
-    asm volatile("" : "+v"(mine));
+    const int mine = lim - 4 * (lane_now() >> 5);
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + i % 4 > mine ? -HUGE_VALF : s[i];
   }
@@ -203,19 +210,21 @@ __device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t
   float p[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) p[i] = fast_exp2(__builtin_fmaf(s[i], factor, -r.m));
+  float sum = 0;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) sum += (p[i] + p[i + 1]) + (p[i + 2] + p[i + 3]);
+  r.l += sum;
+  asm volatile("" : "+v"(r.l));  // now, so that the sixteen end here
   u32x4 pf[2];
   if constexpr (ENC) {
+    const int h = lane_now() >> 5;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4 n = lds_at<f32x4>(vn + 32 * i + 16 * h);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r.l += p[4 * i + j];
       pf[i >> 1][2 * (i & 1)] = pack_f16x2(p[4 * i] * n[0], p[4 * i + 1] * n[1]);
       pf[i >> 1][2 * (i & 1) + 1] = pack_f16x2(p[4 * i + 2] * n[2], p[4 * i + 3] * n[3]);
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r.l += p[i];
 #pragma unroll
     for (int i = 0; i < 8; ++i) pf[i >> 2][i & 3] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
   }
@@ -224,12 +233,9 @@ __device__ __forceinline__ void key_step(Rows& r, const u32x4 (&q)[16], uint32_t
   for (int x = 0; x < PV; ++x) vf[x] = v_fragment(v, x);
 #pragma unroll
   for (int x = 0; x < 16; ++x) {
+    __builtin_amdgcn_sched_barrier(0);  // else each read would move to right before its product
     r.o[x >> 1] = mfma32<ENC>(vf[x % PV], pf[x & 1], r.o[x >> 1]);
-    __builtin_amdgcn_sched_group_barrier(0x8, 1, 1);
-    if (x + PV < 16) {
-      vf[x % PV] = v_fragment(v, x + PV);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
-    }
+    if (x + PV < 16) vf[x % PV] = v_fragment(v, x + PV);
   }
 }
 
@@ -325,13 +331,13 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
   // 512 bytes each, lane l the chunk that belongs in place l % 32.  Rows past
   // the sequence read as zeros.
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
-  const uint32_t place = (col ^ swizzle(2 * wave + h)) * 16;
-  uint32_t ko = (2 * wave + h) * static_cast<uint32_t>(a.k_stride) * 2, vo = (2 * wave + h) * static_cast<uint32_t>(a.v_stride) * 2;
   const auto stage = [&](int buf, int32_t t0) {
     const int64_t at = begin + static_cast<int64_t>(t0);
     const u32x4 kb = buffer_of(a.k_new + at * a.k_stride + head * kDim, ((n - t0 - 1) * a.k_stride + kDim) * 2);
     const u32x4 vb = buffer_of(a.v_new + at * a.v_stride + head * kDim, ((n - t0 - 1) * a.v_stride + kDim) * 2);
-    asm volatile("" : "+v"(ko), "+v"(vo));  // the sums below are made each time, not kept in registers
+    const int now = lane_now(), key = 2 * wave + (now >> 5);
+    const uint32_t place = ((now & 31) ^ swizzle(key)) * 16;
+    const uint32_t ko = key * static_cast<uint32_t>(a.k_stride) * 2, vo = key * static_cast<uint32_t>(a.v_stride) * 2;
 #pragma unroll
     for (int i = 0; i < KT / (2 * NW); ++i) {
       const int pair = 2 * NW * i + 2 * wave;
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
       const int32_t k0 = t0 + 32 * u;
       if (k0 > last) continue;
       const uint32_t kb = base + buf * kStage + u * 16384, vb = kb + KT * 512;
-      key_step<false>(r, q, kb + at.k, vb + at.v, factor, tok - k0, k0 + 31 > first, 0, 0, lane);
+      key_step<false>(r, q, kb + at.k, vb + at.v, factor, tok - k0, k0 + 31 > first, 0, 0);
     }
   }
   add_nonfinite(r, flag, seen / KT * KT, last, tok, h, [&](int64_t key) {
