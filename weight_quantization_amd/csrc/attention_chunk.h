@@ -92,6 +92,14 @@ struct ChunkRow {
   }
 };
 
+// Zeros that no other code takes a zero from: the compiler would keep sixteen
+// of them for the upper half of a 64-bit address.
+__device__ __forceinline__ void clear_apart(Rows& r) {
+  clear(r);
+#pragma unroll
+  for (int t = 0; t < 8; ++t) asm volatile("" : "+v"(r.o[t]));
+}
+
 // LDS of the chunk kernel: two stages of 64 tokens' K and V (fp16 or bf16), two
 // of their packed codes, and of their norms as they are in memory, four of the
 // ids of their pages, and for each stage the K norms, the V norms, whether some
@@ -106,12 +114,9 @@ struct ChunkLds {
 
 // Vector of token t, which lies in page `id` of its request.
 __device__ __forceinline__ int64_t place(const AttnArgs& a, int32_t head, int32_t id, int32_t t) {
-  int32_t zero;  // for the upper half: one that the compiler does not keep
-  asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
-  int64_t at = ((static_cast<int64_t>(id) * a.kv_heads + head) << a.page_shift) +
-               (static_cast<int64_t>(zero) << 32 | static_cast<uint32_t>(t & ((1 << a.page_shift) - 1)));
-  asm volatile("" : "+v"(at));
-  return at;
+  int32_t within = t & ((1 << a.page_shift) - 1);
+  asm volatile("" : "+v"(within));  // its upper half is computed: a register with a zero for it would be kept, and spilled
+  return ((static_cast<int64_t>(id) * a.kv_heads + head) << a.page_shift) + within;
 }
 
 // Pages [u0, u1) of 64 tokens.  At block u the page ids of u + 3 and the codes
@@ -227,7 +232,7 @@ __device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Ex
       for (int j = 0; j < 4; ++j) q[s][j] = pack_f16x2(x[8 * s + 2 * j] * f, x[8 * s + 2 * j + 1] * f);
     factor = fmaxf(__builtin_ldexpf(a.factor, ex - 8), __FLT_DENORM_MIN__);
   }
-  clear(r);
+  clear_apart(r);
   wait_staged();
   barrier();
   norms(u0, -64);
@@ -286,28 +291,45 @@ __device__ __forceinline__ void chunk_tokens(Rows& r, const AttnArgs& a, const E
   using L = ChunkLds<BITS>;
   constexpr int KT = kChunkBlock;
   const int32_t rows = e.n * a.group;
-  const ChunkRow row(a, head, w0, rows);
-  const TileLane at = tile_lane(row.lane);
   const Tokens tokens(a, e, b, head);
   // the keys that all rows see; the last that the wave's first row sees, and its last row
   const int64_t seen = tokens.near + token_of(w0 - 32 * wave, a.group) + 1;
   const int64_t first_key = tokens.near + token_of(min(w0, rows - 1), a.group);
   const int64_t last_key = w0 >= rows ? -1 : tokens.near + token_of(min(w0 + 31, rows - 1), a.group);
+  // Tokens t0 .. t0 + 63, from window and step; the last one again for what is
+  // past it, which is masked.
   const auto stage = [&](int buf, int64_t t0) {
+    const int lane = lane_now(), pair = 2 * wave + (lane >> 5);
+    const int32_t c = ((lane & 31) ^ swizzle(pair)) * 16;
+    const int window = static_cast<int>(max(min(tokens.near - t0, int64_t{KT}), int64_t{0}));
+    const int last = static_cast<int>(min(end_key - t0, int64_t{KT - 1}));
+    // where token t0 would be in the ring, in the ring after its end, among the step's
+    const int64_t slot = tokens.ring0 + t0;
+    const int until = static_cast<int>(min(tokens.ring - slot, int64_t{KT}));  // may be below 0: all after the end
+    const char* from[2][3];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      from[side][0] = reinterpret_cast<const char*>(tokens.window[side] + slot * kDim);
+      from[side][1] = reinterpret_cast<const char*>(tokens.window[side] + (slot - tokens.ring) * kDim);
+      from[side][2] = reinterpret_cast<const char*>(tokens.rows[side] + (t0 - tokens.near) * tokens.stride[side]);
+    }
 #pragma unroll
     for (int i = 0; i < KT / 16; ++i) {
-      const int pair = 16 * i + 2 * wave;
-      const int64_t k = t0 + pair + row.h;
-      const uint32_t c = (row.col ^ swizzle(2 * wave + row.h)) * 8;
-      stage16(tokens.at(0, k, end_key) + c, base + buf * L::kStage + pair * 512);
-      stage16(tokens.at(1, k, end_key) + c, base + buf * L::kStage + KT * 512 + pair * 512);
+      const int j = min(16 * i + pair, last);
+      const uint32_t to = base + buf * L::kStage + (16 * i + 2 * wave) * 512;
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        // below 2^29 + 2^9: strides are at most 2^22
+        const int32_t off = j * (j < window ? kDim * 2 : static_cast<int32_t>(2 * tokens.stride[side])) + c;
+        stage16((j < window ? j < until ? from[side][0] : from[side][1] : from[side][2]) + off, to + side * KT * 512);
+      }
     }
   };
   if (threadIdx.x == 0) lds_put<uint32_t>(base + L::flag, 0);
   wait_lds();
   stage(0, static_cast<int64_t>(from) * KT);
   u32x4 q[16];
-  const uint16_t* qp = row.q(a, e.begin);
+  const uint16_t* qp = ChunkRow(a, head, w0, rows).q(a, e.begin);
 #pragma unroll
   for (int s = 0; s < 16; ++s) q[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
 #pragma unroll
@@ -315,6 +337,10 @@ __device__ __forceinline__ void chunk_tokens(Rows& r, const AttnArgs& a, const E
     if (a.scale < 0) q[s] ^= 0x80008000u;
     asm volatile("" : "+v"(q[s]));
   }
+  TileLane at = tile_lane(lane_now());
+  asm volatile("" : "+v"(at.k), "+v"(at.v));
+  int32_t tok = ChunkRow(a, head, w0, rows).tok;
+  asm volatile("" : "+v"(tok));
   for (int32_t u = from; u < to; ++u) {
     const int buf = (u - from) & 1;
     wait_staged();
@@ -327,11 +353,11 @@ __device__ __forceinline__ void chunk_tokens(Rows& r, const AttnArgs& a, const E
       if (k0 > last_key) continue;
       const uint32_t kb = base + buf * L::kStage + s * 16384;
       key_step<false>(r, q, kb + at.k, kb + KT * 512 + at.v, a.factor,
-                      static_cast<int>(min(tokens.near + row.tok - k0, int64_t{64})), k0 + 31 > first_key, 0, 0);
+                      static_cast<int>(min(tokens.near - k0 + tok, int64_t{64})), k0 + 31 > first_key, 0, 0);
     }
   }
   add_nonfinite(r, base + L::flag, max(seen / KT * KT, static_cast<int64_t>(from) * KT), min(last_key, static_cast<int64_t>(to) * KT - 1),
-                tokens.near + row.tok, row.h, [&](int64_t key) { return tokens.at(1, key, end_key); });
+                tokens.near + tok, lane_now() >> 5, [&](int64_t key) { return tokens.at(1, key, end_key); });
 }
 
 template <int BITS>
@@ -361,7 +387,7 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
       chunk_pages<BITS>(r, a, w.e, g.b, g.head, w0, u0, min(u1, w.page_blocks), base, wave);
       barrier();  // every wave is done with LDS
     } else {
-      clear(r);
+      clear_apart(r);
     }
     if (u1 > w.page_blocks) {
       chunk_tokens<BITS>(r, a, w.e, g.b, g.head, w0, w.e.held - w.e.enc + w.last_token(a, g.tile),
