@@ -188,15 +188,34 @@ struct Finder {
         f.b = b0 + at;
         f.rest = x - __builtin_amdgcn_readlane(prefix - own, at);
         if (at > 0) f.before += __builtin_amdgcn_readlane(aside, at - 1);
-        f.e = extent_of(args, __builtin_amdgcn_readlane(mine.begin, at), __builtin_amdgcn_readlane(mine.n, at),
-                        static_cast<int32_t>(__builtin_amdgcn_readlane(static_cast<int32_t>(mine.held), at)) +
-                            __builtin_amdgcn_readlane(mine.n, at));
+        f.e = extent_at(at);
         return f;
       }
       x -= __builtin_amdgcn_readlane(prefix, 63);
       f.before += __builtin_amdgcn_readlane(aside, 63);
     }
     return f;
+  }
+  // Place x of up to 64 requests' places taken from the last to the first: all
+  // those of rest >= j come before those of rest = j - 1.
+  __device__ __forceinline__ Found find_from_last(int32_t x) const {
+    const auto beyond = [&](int32_t j) { return __builtin_amdgcn_readlane(wave_scan(max(own - j, 0)), 63); };
+    int32_t j = 0, none = total;  // beyond(j) > x >= beyond(none)
+    while (none - j > 1) {
+      const int32_t mid = j + (none - j) / 2;
+      (beyond(mid) > x ? j : none) = mid;
+    }
+    x -= beyond(j + 1);
+    uint64_t having = __ballot(own > j);
+    for (; x > 0; --x) having &= having - 1;
+    const int at = __builtin_ctzll(having);
+    return Found{at, j, 0, extent_at(at)};
+  }
+  // of lane `at`'s request
+  __device__ __forceinline__ Extent extent_at(int at) const {
+    return extent_of(args, __builtin_amdgcn_readlane(mine.begin, at), __builtin_amdgcn_readlane(mine.n, at),
+                     static_cast<int32_t>(__builtin_amdgcn_readlane(static_cast<int32_t>(mine.held), at)) +
+                         __builtin_amdgcn_readlane(mine.n, at));
   }
 };
 struct Nothing {

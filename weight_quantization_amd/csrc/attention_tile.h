@@ -304,9 +304,16 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
   const auto tiles = [&](const Extent& e) { return static_cast<int32_t>(ceil_div(e.n * g, kRows)); };
   Finder<decltype(tiles), Nothing> finder(a, tiles, Nothing{});
   if (static_cast<int32_t>(blockIdx.x / a.kv_heads) >= finder.total) return;
-  const Found f = finder.find(blockIdx.x / a.kv_heads);
+  const int32_t x = blockIdx.x / a.kv_heads;
+  Found f;
+  if (a.requests <= 64) {
+    f = finder.find_from_last(x);
+  } else {
+    f = finder.find(x);
+    f.rest = tiles(f.e) - 1 - f.rest;
+  }
   const int32_t begin = f.e.begin, n = f.e.n, rows = n * g;
-  const int32_t r0 = (tiles(f.e) - 1 - f.rest) * kRows;  // the tile's first row
+  const int32_t r0 = f.rest * kRows;  // the tile's first row
   const int32_t w0 = r0 + 32 * wave;                                          // the wave's
   // tokens of the lane's row, of the wave's first and last, of the tile's last
   const int32_t tok = token_of(min(w0 + col, rows - 1), g);
