@@ -92,6 +92,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// In a rare branch: keeps the compiler from doing its work always and selecting.
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
 // The pair of bf16 with infinities and NaN replaced by zero; `any` gets a bit
 // set if there was one.  (Adding one to an exponent of all ones carries into
 // the sign's place.)

@@ -212,8 +212,9 @@ __device__ __forceinline__ void clear(SplitRows<NR>& r) {
 template <int NR, class G>
 __device__ __forceinline__ void weigh(SplitRows<NR>& r, int n, float (&s)[8], float factor, bool masked, G gone, float (&p)[8]) {
   if (masked) {
+    keep_branch();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = gone(i) ? -FLT_MAX : s[i];
+    for (int i = 0; i < 8; ++i) s[i] = gone(i) ? -HUGE_VALF : s[i];
   }
   float mx = s[0];
 #pragma unroll
@@ -230,7 +231,6 @@ __device__ __forceinline__ void weigh(SplitRows<NR>& r, int n, float (&s)[8], fl
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     p[i] = fast_exp2(__builtin_fmaf(s[i], factor, -r.m[n]));
-    if (masked) p[i] = gone(i) ? 0.0f : p[i];
     r.l[n] += p[i];
   }
 }
@@ -260,7 +260,11 @@ __device__ __forceinline__ void code_step(SplitRows<NR>& r, const u32x4 (&q)[NR]
     const uint32_t kw = c.kn[i >> 2][(i >> 1) & 1], vw = c.vn[i >> 2][(i >> 1) & 1];
     kn[i] = f16_value(static_cast<uint16_t>(i & 1 ? kw >> 16 : kw));
     vn[i] = f16_value(static_cast<uint16_t>(i & 1 ? vw >> 16 : vw));
-    if (masked && gone(i)) vn[i] = 0;
+  }
+  if (masked) {
+    keep_branch();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) vn[i] = gone(i) ? 0.0f : vn[i];
   }
   // The weights p n are products' operands in fp16, so n is taken over a power
   // of two that no norm met so far exceeds: p n 2^-exponent is at most 2^kLazy,
@@ -539,9 +543,9 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
       load_codes<BITS>(to, a, s, vec, lane);
     }
   };
-  Codes<BITS> cur, next;
-  int there[2], there_next[2] = {0, 0};
-  fetch(u0, cur, there);
+  Codes<BITS> codes[2];
+  int there[2][2];
+  fetch(u0, codes[0], there[0]);
 
   // q rotated, each row over a power of two that brings its largest value to
   // [1, 2), as fp16, while the codes are on their way
@@ -553,7 +557,7 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
     if (r0 + row + 4 < rows && row + 4 < M) v = q_load(row + 4);
     if (r0 + row >= rows) {  // rows that are not there: zeros, and no more to load
       *reinterpret_cast<uint2*>(ql + row * kQPitch + 4 * lane) = uint2{0, 0};
-      if (lane == 0) qf[row] = 0;
+      if (lane == 0) qf[row] = 1;
       continue;
     }
     wave_fwht(x, lane);
@@ -561,7 +565,7 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
     const int ex = mx > 0 ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
     const float f = __builtin_ldexpf(a.scale < 0 ? -1.0f : 1.0f, -ex);
     *reinterpret_cast<uint2*>(ql + row * kQPitch + 4 * lane) = uint2{pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f)};
-    if (lane == 0) qf[row] = __builtin_ldexpf(a.factor, ex - 8);
+    if (lane == 0) qf[row] = fmaxf(__builtin_ldexpf(a.factor, ex - 8), __FLT_DENORM_MIN__);
   }
   __syncthreads();
   u32x4 q[NR][8];
@@ -581,13 +585,15 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
   }
   SplitRows<NR> r;
   clear(r);
-  for (int32_t u = u0; u < u1; ++u) {
-    if (u + 1 < u1) fetch(u + 1, next, there_next);
-    if (there[0] + there[1] > 0) code_step<BITS, NR>(r, q, factor, cur, there[0], there[1], lane);
-    cur = next;
-    there[0] = there_next[0];
-    there[1] = there_next[1];
-  }
+  // block u while the codes of u + 1 are on their way; by twos, as moving them
+  // from one set of registers to the other took a tenth of the step
+  for (int32_t u = u0; u < u1; u += 2)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (u + k >= u1) break;
+      if (u + k + 1 < u1) fetch(u + k + 1, codes[k ^ 1], there[k ^ 1]);
+      if (there[k][0] + there[k][1] > 0) code_step<BITS, NR>(r, q, factor, codes[k], there[k][0], there[k][1], lane);
+    }
   join_waves<NR>(r, true, rows - r0, lds, lane, wave, write);
 }
 

@@ -109,9 +109,6 @@ __device__ __forceinline__ int lane_now() {
   return lane;
 }
 
-// In a rare branch: keeps the compiler from doing its work always and selecting.
-__device__ __forceinline__ void keep_branch() { asm volatile(""); }
-
 // Lane constants of the LDS reads.  What distinguishes the reads of a step is
 // three bits of the address, to be exclusive-ored in (they meet the swizzle),
 // and an offset that the instruction adds.
