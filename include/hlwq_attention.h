@@ -144,7 +144,7 @@ int hlwq_kv_paged_append(const hlwq_kv_cache* cache, const void* k_new_bf16, int
  *
  * A token whose page id lies outside [0, n_pages), or past max_pages, is left
  * out of the sum.  lens[b] below the number of new tokens counts as equal to it.
- * Norms of encoded tokens must be finite; k_new, v_new and window may hold NaN
+ * Norms of encoded tokens must be finite and not negative; k_new, v_new and window may hold NaN
  * and infinities, which reach only rows that attend to them.
  *
  * `workspace` holds partial sums: hlwq_kv_paged_attention_workspace bytes,

@@ -174,7 +174,7 @@ __device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Ex
       // as in code_step: norms over a power of two that none met so far exceeds
       const float top = wave_max(there ? n : 0.0f);
       if (top > __builtin_ldexpf(1.0f, exponent)) exponent = __builtin_amdgcn_frexp_expf(top);
-      lds_put<float>(side + L::kLine + 4 * lane, there ? __builtin_ldexpf(n, -exponent) : 0.0f);
+      lds_put<float>(side + L::kLine + 4 * lane, there ? __builtin_ldexpf(kTopWeight * n, -exponent) : 0.0f);
       if (lane == 0) lds_put<int32_t>(side + 2 * L::kLine + 4, exponent);
     }
   };
@@ -277,7 +277,7 @@ __device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Ex
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[16 * t + i] = r.o[t][i];
   fwht_halves(x);
-  const float f = __builtin_ldexpf(1.0f, scaled - 8);
+  const float f = __builtin_ldexpf(1.0f / kTopWeight, scaled - 8);
 #pragma unroll
   for (int t = 0; t < 8; ++t)
 #pragma unroll

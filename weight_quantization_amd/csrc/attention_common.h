@@ -30,6 +30,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // far inside the range of bf16, fp16 and fp32, and the rescale of 256 sums is
 // paid a few times per row instead of once per tile.
 constexpr float kLazy = 8.0f;
+constexpr float kTopWeight = 128;  // times 2^kLazy still below fp16's largest, 65504
 
 struct AttnArgs {
   const uint16_t* q;

@@ -267,9 +267,9 @@ __device__ __forceinline__ void code_step(SplitRows<NR>& r, const u32x4 (&q)[NR]
     for (int i = 0; i < 8; ++i) vn[i] = gone(i) ? 0.0f : vn[i];
   }
   // The weights p n are products' operands in fp16, so n is taken over a power
-  // of two that no norm met so far exceeds: p n 2^-exponent is at most 2^kLazy,
-  // and a weight is rounded to a subnormal only where it is below 2^-14 of
-  // that.
+  // of two that no norm met so far exceeds, times kTopWeight: a weight is at most
+  // 2^15 and keeps its 2^-11 down to 2^-29 of that.  A token with the row's
+  // largest score thus does up to norms 2^21 times its own.
   float top = vn[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) top = fmaxf(top, vn[i]);
@@ -284,7 +284,7 @@ __device__ __forceinline__ void code_step(SplitRows<NR>& r, const u32x4 (&q)[NR]
 #pragma unroll
       for (int x = 0; x < 16; ++x) r.o[n][x] *= f;
   }
-  const float over = __builtin_ldexpf(1.0f, -r.exponent);
+  const float over = __builtin_ldexpf(kTopWeight, -r.exponent);
   u32x4 pf[NR];
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
@@ -443,7 +443,7 @@ constexpr int kSplitStats = 4 * 16 * 2;  // floats
 template <int NR, class F>
 __device__ __forceinline__ void join_waves(SplitRows<NR>& r, bool enc, int there, float* lds, int lane, int wave, F write) {
   const int c = lane & 15, h4 = lane >> 4;
-  const float f = enc ? __builtin_ldexpf(1.0f, r.exponent - 8) : 1.0f;  // H c n / 256
+  const float f = enc ? __builtin_ldexpf(1.0f / kTopWeight, r.exponent - 8) : 1.0f;  // H c n / 256
   float* stat = lds + 4 * 16 * kSplitPitch;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
