@@ -102,7 +102,9 @@ typedef struct hlwq_kv_plan {
  * given back are pushed in order of (slot, page); pages are popped in order of
  * (request, page).  tokens, n_new and n_free are left as they are (lens and
  * n_free_after are the next step's), so the same step can be planned again
- * unless a reset slot takes pages in it.
+ * unless a reset slot takes pages in it.  A page may stand in several tables (a
+ * common beginning read by several requests); the plan keeps no count of that, so
+ * only one of them may be reset.
  *
  * *status afterwards: 0; or the number of pages missing from the stack; or -1
  * where a device value is out of range (a negative length, more new tokens than
@@ -146,6 +148,10 @@ int hlwq_kv_paged_append(const hlwq_kv_cache* cache, const void* k_new_bf16, int
  * out of the sum.  lens[b] below the number of new tokens counts as equal to it.
  * Norms of encoded tokens must be finite and not negative; k_new, v_new and window may hold NaN
  * and infinities, which reach only rows that attend to them.
+ *
+ * HLWQ_ERR_LIMIT where max_pages * page_size / 128 times the number of tiles (16
+ * or 32 query rows of a request and KV head) reaches 2^31 for requests of few
+ * rows, or the rows make more than 2^24 tiles.
  *
  * `workspace` holds partial sums: hlwq_kv_paged_attention_workspace bytes,
  * 16-byte aligned, contents immaterial before and after. */
