@@ -49,6 +49,29 @@ def test_wide_prompt_tiles(wq, count):
     prompt_case(wq, count, lens, 16, 8, extra=8, pad=5)
 
 
+@pytest.mark.parametrize("lens,q_heads,kv_heads", [([700], 6, 1), ([384], 4, 4), ([513, 300, 400], 5, 1), ([1100, 1], 2, 1)])
+def test_prompt_tiles_with_keys_halved(wq, lens, q_heads, kv_heads):
+    # few tiles of long sequences
+    prompt_case(wq, sum(lens), lens, q_heads, kv_heads, extra=8, pad=2)
+
+
+def test_halved_prompt_tiles_nan_and_infinities(wq):
+    rng = np.random.default_rng(12)
+    n = 450
+    q, kv = bf16_bits(rng, n, 6, D), [bf16_bits(rng, n, 2, D) for _ in range(2)]
+    cu = i32([0, n])
+    clean = wq.hlwq_prompt_attention(dev16(q), dev16(kv[0]), dev16(kv[1]), cu)
+    for row in (0, 31, 32, 63, 64, 200, 449):
+        for i, what in ((0, 0x7FC0), (1, 0x7FC0), (1, 0x7F80)):
+            dirty = [x.copy() for x in kv]
+            dirty[i][row, 1, 250] = what
+            got = wq.hlwq_prompt_attention(dev16(q), dev16(dirty[0]), dev16(dirty[1]), cu)
+            hit = torch.zeros(n, 6, D, dtype=torch.bool, device="cuda")
+            hit[row:, 3:, slice(None) if i == 0 else 250] = True
+            assert torch.equal(got[~hit], clean[~hit]), (row, i, hex(what))
+            assert (torch.isnan(got[hit]) if what == 0x7FC0 else torch.isposinf(got[hit])).all()
+
+
 def test_wide_prompt_tiles_nan_and_infinities(wq):
     rng = np.random.default_rng(11)
     lens = [200] + [60] * 63

@@ -29,12 +29,24 @@ int64_t prompt_groups(const AttnArgs& a, int64_t tile) {
   return tiles_of(a.requests, a.rows, a.group, a.kv_heads, tile);
 }
 
+// Tiles of 256 rows read K and V half as often as tiles of 128, but need twice
+// the rows to fill the device's 256 CUs; and where not even two tiles of 128
+// meet on a CU, what a tile waits for counts, so eight waves split its keys.
+// Measured (24 query heads on 4, one sequence, us):
+//   tokens                100    517    900   1500   2500   4000   8000  16384
+//   256 rows               19     36     52     79    124    214    731   2930
+//   128 rows               13     29     43     71    117    210    727   3023
+//   128 rows, keys halved  16     26     37     55    106    235    767
+// The lengths are on the device, so the host goes by their mean.
 int launch_prompt(const AttnArgs& a, hipStream_t stream) {
-  const bool wide = prompt_groups(a, 256) >= 512;
-  const int64_t groups = prompt_groups(a, wide ? 256 : 128);
+  const int64_t wide = prompt_groups(a, 256), narrow = prompt_groups(a, 128);
+  const bool halved = narrow <= 512 && a.rows >= int64_t{384} * a.requests;
+  const int64_t groups = wide >= 512 ? wide : narrow;
   if (groups > 0x7fffff) return HLWQ_ERR_LIMIT;
-  return launch(wide ? hlwq_prompt_attention_kernel<8, 64> : hlwq_prompt_attention_kernel<4, 32>,
-                dim3(static_cast<uint32_t>(groups)), dim3(wide ? 512 : 256), stream, a);
+  const dim3 grid(static_cast<uint32_t>(groups));
+  if (wide >= 512) return launch(hlwq_prompt_attention_kernel<8, 64, 1>, grid, dim3(512), stream, a);
+  if (halved) return launch(hlwq_prompt_attention_kernel<8, 64, 2>, grid, dim3(512), stream, a);
+  return launch(hlwq_prompt_attention_kernel<4, 32, 1>, grid, dim3(256), stream, a);
 }
 
 // How a paged call is shared among the kernels: requests with at most kFewRows

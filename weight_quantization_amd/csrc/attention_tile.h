@@ -288,11 +288,13 @@ __device__ __forceinline__ void add_nonfinite(Rows& r, uint32_t flag, int64_t fr
 // on different KV heads, so that an XCD's L2 serves as few heads as there are.
 // ---------------------------------------------------------------------------
 
-template <int NW, int KT>
+template <int NW, int KT, int PARTS>
 __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) hlwq_prompt_attention_kernel(const AttnArgs a) {
-  constexpr int kRows = 32 * NW;
+  constexpr int kRows = 32 * NW / PARTS;
   constexpr uint32_t kStage = KT * 1024;  // K and V of one stage
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage + 16];
+  constexpr uint32_t kFlag = 2 * kStage, kStats = kFlag + 16;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStats + (PARTS > 1 ? NW / 2 * 512 : 0)];
+  static_assert(PARTS == 1 || (PARTS == 2 && KT == 64 && NW / 2 * 32768 <= 2 * kStage));
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, h = lane >> 5;
   const int head = blockIdx.x % a.kv_heads;
@@ -311,7 +313,8 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
   }
   const int32_t begin = f.e.begin, n = f.e.n, rows = n * g;
   const int32_t r0 = f.rest * kRows;  // the tile's first row
-  const int32_t w0 = r0 + 32 * wave;                                          // the wave's
+  const int strip = wave % (NW / PARTS), part = wave / (NW / PARTS);
+  const int32_t w0 = r0 + 32 * strip;  // the wave's
   // tokens of the lane's row, of the wave's first and last, of the tile's last
   const int32_t tok = token_of(min(w0 + col, rows - 1), g);
   const auto q_head = [&]() { return head * g + (min(w0 + col, rows - 1) - tok * g); };
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
     }
   };
   const TileLane at = tile_lane(lane);
-  const uint32_t flag = base + 2 * kStage;
+  const uint32_t flag = base + kFlag;
   if (threadIdx.x == 0) lds_put<uint32_t>(flag, 0);
   wait_lds();
   stage(0, 0);
@@ -369,16 +372,48 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
     if (t0 + KT < end) stage(buf ^ 1, t0 + KT);
     if (t0 + KT > seen) leave_out_nonfinite<64 * NW, KT>(base + buf * kStage + KT * 512, flag);
 #pragma unroll
-    for (int u = 0; u < KT / 32; ++u) {
-      const int32_t k0 = t0 + 32 * u;
+    for (int u = 0; u < KT / 32 / PARTS; ++u) {
+      const int step = PARTS > 1 ? part : u;
+      const int32_t k0 = t0 + 32 * step;
       if (k0 > last) continue;
-      const uint32_t kb = base + buf * kStage + u * 16384, vb = kb + KT * 512;
+      const uint32_t kb = base + buf * kStage + step * 16384, vb = kb + KT * 512;
       key_step<false>(r, q, kb + at.k, vb + at.v, factor, tok - k0, k0 + 31 > first, 0, 0);
     }
   }
-  add_nonfinite(r, flag, seen / KT * KT, last, tok, h, [&](int64_t key) {
+  add_nonfinite(r, flag, seen / KT * KT, part > 0 ? -1 : last, tok, h, [&](int64_t key) {
     return a.v_new + (begin + key) * a.v_stride + head * kDim;
   });
+  if constexpr (PARTS > 1) {
+    // the second part's sums to the first, through the stages
+#pragma unroll
+    for (int t = 0; t < 8; ++t) asm volatile("" : "+v"(r.o[t]));  // the loop's registers end here
+    barrier();
+    const uint32_t to = base + strip * 32768 + lane_now() * 16, stat = base + kStats + strip * 512 + lane_now() * 8;
+    if (part > 0) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          lds_put<f32x4>(to + (4 * t + i) * 1024, f32x4{r.o[t][4 * i], r.o[t][4 * i + 1], r.o[t][4 * i + 2], r.o[t][4 * i + 3]});
+      lds_put<f32x2>(stat, f32x2{r.m, r.l});
+    }
+    wait_lds();
+    barrier();
+    if (part > 0) return;
+    const f32x2 s = lds_at<f32x2>(stat);
+    // above 0, as an infinite value times 0 would be NaN
+    const float m = fmaxf(r.m, s[0]), f0 = fmaxf(fast_exp2(r.m - m), FLT_MIN), f1 = fast_exp2(s[0] - m);
+    r.l = r.l * f0 + s[1] * f1;
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 o = lds_at<f32x4>(to + (4 * t + i) * 1024);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.o[t][4 * i + j] = r.o[t][4 * i + j] * f0 + o[j] * f1;
+        __builtin_amdgcn_sched_barrier(0);  // few of the other's sums in registers at once
+      }
+  }
   r.l += half_swap(r.l);
   const float inv = 1.0f / r.l;
   if (w0 + col < rows) {
