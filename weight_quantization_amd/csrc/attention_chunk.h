@@ -370,10 +370,12 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
   const auto cost = [&](const Extent& e) { return Work<M, KT>(a, e).head_cost() * a.kv_heads; };
   Finder<decltype(cost), Nothing> finder(a, cost, Nothing{});
   const Share share(finder.total, a.workers, kChunkLeast);
-  if (finder.total == 0 || static_cast<int32_t>(blockIdx.x) >= share.workers) return;
+  if (finder.total == 0) return;
   // Workgroups of one XCD (every eighth) take neighbouring stretches, which
   // share a KV head's keys in its L2.
-  const int32_t worker = share.workers % 8 == 0 ? (blockIdx.x % 8) * (share.workers / 8) + blockIdx.x / 8 : blockIdx.x;
+  const int32_t of_xcd = (share.workers + 7) / 8;
+  const int32_t worker = (blockIdx.x % 8) * of_xcd + blockIdx.x / 8;
+  if (static_cast<int32_t>(blockIdx.x / 8) >= of_xcd || worker >= share.workers) return;
   const Found first = finder.find(share.bound(worker));
 
   for_segments<M, KT>(a, share, first, worker, [&](const Work<M, KT>& w, const Segment& g) {

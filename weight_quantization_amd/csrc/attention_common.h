@@ -293,22 +293,21 @@ struct Work {
   }
 };
 
-// The stretches: worker w of `workers` takes cost [bound(w), bound(w + 1)),
-// the first `more` one unit more than the others.  Fewer workgroups than there
-// are share a small total, at least the cost `least` to each.
+// The stretches: worker w of `workers` takes cost [bound(w), bound(w + 1)), all
+// but the last the same, at least `least`.  Where that is a few blocks, fewer
+// workers than there could be take as long as all of them and leave fewer
+// partial sums to join.
 struct Share {
-  int32_t workers, each, more;
-  __device__ __forceinline__ Share(int32_t total, int32_t most, int32_t least) {
-    workers = max(min(most, total / least), 1);
-    each = quotient(total, workers);
-    more = total - each * workers;
+  int32_t total, each, workers;
+  __device__ __forceinline__ Share(int32_t cost, int32_t most, int32_t least) : total(cost) {
+    each = max(quotient(cost - 1, most) + 1, least);
+    workers = quotient(cost - 1, each) + 1;
   }
-  __device__ __forceinline__ int32_t bound(int32_t w) const { return w * each + min(w, more); }
+  __device__ __forceinline__ int32_t bound(int32_t w) const {
+    return static_cast<int32_t>(min(static_cast<uint32_t>(w) * static_cast<uint32_t>(each), static_cast<uint32_t>(total)));
+  }
   // the worker whose stretch holds x
-  __device__ __forceinline__ int32_t worker_at(int32_t x) const {
-    const int32_t cut = more * (each + 1);
-    return x < cut ? quotient(x, each + 1) : more + quotient(x - cut, each);
-  }
+  __device__ __forceinline__ int32_t worker_at(int32_t x) const { return quotient(x, each); }
 };
 
 // Partial sums lie in slots of M rows of 256 floats, followed for all slots by
