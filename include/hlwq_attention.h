@@ -150,7 +150,7 @@ int hlwq_kv_paged_append(const hlwq_kv_cache* cache, const void* k_new_bf16, int
  * and infinities, which reach only rows that attend to them.
  *
  * HLWQ_ERR_LIMIT where max_pages * page_size / 128 times the number of tiles (16
- * or 32 query rows of a request and KV head) reaches 2^31 for requests of few
+ * query rows of a request and KV head) reaches 2^31 for requests of few
  * rows, or the rows make more than 2^24 tiles.
  *
  * `workspace` holds partial sums: hlwq_kv_paged_attention_workspace bytes,

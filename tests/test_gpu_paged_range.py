@@ -21,6 +21,9 @@ pytestmark = pytest.mark.gpu
     ([2000, 700, 0], [101, 257, 64], 6, 2, 3, 256, 0, 0),
     ([900], [33], 1, 1, 3, 32, 200, 201),
     ([1000, 1000], [65, 64], 8, 8, 2, 128, 37, 37),
+    ([333], [256], 1, 1, 3, 64, 128, 128),
+    ([333], [257], 1, 1, 2, 64, 128, 128),
+    ([0], [300], 6, 1, 3, 64, 128, 128),
 ])
 def test_long_chunks(wq, ctx, new, q_heads, kv_heads, bits, page, residual, ring):
     attention_case(wq, sum(new), ctx, new, q_heads, kv_heads, bits, page, residual, ring, extra=8, pad=3)
@@ -90,6 +93,25 @@ def test_wide_prompt_tiles_nan_and_infinities(wq):
             assert (torch.isnan(got[hit]) if what == 0x7FC0 else torch.isneginf(got[hit])).all()
 
 
+def test_chunks_nan_and_infinities(wq):
+    rng = np.random.default_rng(5)
+    ctx, new = [300, 20], [190, 100]
+    n = sum(new)
+    c = Cache(rng, ctx, 2, 3, 64, 128, 128)
+    q, kv = bf16_bits(rng, n, 4, D), [bf16_bits(rng, n, 2, D) for _ in range(2)]
+    cu, lens = i32([0, 190, 290]), i32([490, 120])
+    clean = wq.hlwq_kv_paged_attention(dev16(q), dev16(kv[0]), dev16(kv[1]), cu, lens, i32(c.table), *c.tensors())
+    for row, end in ((0, 190), (63, 190), (64, 190), (189, 190), (200, 290)):
+        for i, what in ((0, 0x7FC0), (1, 0x7FC0), (1, 0x7F80)):
+            dirty = [x.copy() for x in kv]
+            dirty[i][row, 1, 77] = what
+            got = wq.hlwq_kv_paged_attention(dev16(q), dev16(dirty[0]), dev16(dirty[1]), cu, lens, i32(c.table), *c.tensors())
+            hit = torch.zeros(n, 4, D, dtype=torch.bool, device="cuda")
+            hit[row:end, 2:, slice(None) if i == 0 else 77] = True
+            assert torch.equal(got[~hit], clean[~hit]), (row, i, hex(what))
+            assert (torch.isnan(got[hit]) if what == 0x7FC0 else torch.isposinf(got[hit])).all()
+
+
 @pytest.mark.parametrize("new", [[3, 2], [60, 40]])
 def test_nan_in_a_query_stays_in_its_row(wq, new):
     rng = np.random.default_rng(3)
@@ -112,7 +134,7 @@ def test_nan_in_a_query_stays_in_its_row(wq, new):
         pr.check_attention(mine, clean[r], k, v, pr.encoded(ctx[b], 128), ctx[b], 1)
 
 
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 40, 300])
 def test_norms_far_apart(wq, new):
     """The token that a row attends to most has a value 2^19 times smaller than the largest."""
     rng = np.random.default_rng(new)

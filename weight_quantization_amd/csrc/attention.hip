@@ -49,18 +49,24 @@ int launch_prompt(const AttnArgs& a, hipStream_t stream) {
   return launch(hlwq_prompt_attention_kernel<4, 32, 1>, grid, dim3(256), stream, a);
 }
 
-// How a paged call is shared among the kernels: requests with at most kFewRows
-// query rows to a KV head go to the split kernel (in tiles of sixteen or 32),
-// the others to the chunk kernel.  The lengths are on the device, so the host
-// goes by the mean: where it is few rows the split kernel takes every request,
-// and a single request goes to one of the two.
-constexpr int64_t kFewRows = 32;
-// Workgroups that the device holds at once: two to a CU of the split kernel with
-// sixteen rows (256 registers a work-item), else one.
+// How a paged call is shared among the kernels: requests of few query rows to a
+// KV head go to the split kernel, the others to the chunk kernel, which unpacks
+// each code once for 256 rows but takes a hundred microseconds however little
+// it has to do.  The lengths are on the device, so the host goes by the mean:
+// where it is few rows the split kernel takes every request; else both are
+// called, except for a single request.  Measured, split and chunk kernel (24
+// query heads on 4, 3 bits, us):
+//   one request over 16000 tokens, 36 rows     33  115;  120 rows   47  124;
+//                                  240 rows    68  140;  480 rows  112  133
+//   8 requests over 4000 tokens, 36 rows each  42   65;   60 rows   49   67;
+//                                  120 rows    79   71;  240 rows  126   93
+//   32 requests over 1000 tokens, 60 rows      66   70;  240 rows  224  105
+constexpr int64_t few_rows(int64_t requests) { return requests == 1 ? 256 : 64; }
+// Workgroups that the device holds at once: two to a CU of the split kernel
+// (256 registers a work-item), one of the chunk kernel.
 constexpr int64_t kSplitResident = 512, kChunkWorkers = 256;
 struct PagedPlan {
-  int split_rows;         // rows to a tile of the split kernel; 0: it is not called
-  bool chunk;             // whether the chunk kernel is called
+  bool split, chunk;      // which kernels are called
   int64_t split_tiles, split_workers;
   int64_t split_slots;    // of partial sums
   size_t split_bytes, chunk_bytes;  // of workspace, each its own
@@ -68,11 +74,10 @@ struct PagedPlan {
 PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
   PagedPlan p{};
   const int64_t group = q_heads / kv_heads;
-  p.chunk = rows * group > kFewRows * requests;
-  p.split_rows = p.chunk && requests == 1 ? 0 : p.chunk || rows * group > 16 * requests ? 32 : 16;
-  if (p.split_rows) {
-    const int64_t resident = p.split_rows == 32 ? kSplitResident / 2 : kSplitResident;
-    p.split_tiles = tiles_of(requests, rows, group, kv_heads, p.split_rows);
+  p.chunk = rows * group > few_rows(requests) * requests;
+  p.split = !p.chunk || requests > 1;
+  if (p.split) {
+    p.split_tiles = tiles_of(requests, rows, group, kv_heads, kSplitRows);
     // The workgroups of the tiles' windows come after the pages' and end early.
     // Where they are few all fit the device at once; where they are more, places
     // kept free for them would stand empty most of the time, and it is better
@@ -80,9 +85,9 @@ PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv
     // bits, 4000 tokens a request, us), with places kept and without: 4 requests
     // 19.8 and 22.5, 8 26.4 and 25.3, 16 35.8 and 33.6, 64 87 and 74, 128 183
     // and 154.
-    p.split_workers = resident - (p.split_tiles < resident / 16 ? p.split_tiles : 0);
+    p.split_workers = kSplitResident - (p.split_tiles < kSplitResident / 16 ? p.split_tiles : 0);
     p.split_slots = 2 * (p.split_workers + p.split_tiles);
-    p.split_bytes = partial_floats(p.split_slots, p.split_rows) * sizeof(float);
+    p.split_bytes = partial_floats(p.split_slots, kSplitRows) * sizeof(float);
   }
   p.chunk_bytes = p.chunk ? partial_floats(2 * kChunkWorkers, kChunkRows) * sizeof(float) : 0;
   return p;
@@ -95,11 +100,11 @@ size_t workspace_bytes_of(int64_t requests, int64_t rows, int64_t q_heads, int64
   return p.split_bytes + p.chunk_bytes;
 }
 
-template <int BITS, int NR>
+template <int BITS>
 int launch_split(const AttnArgs& a, int64_t tiles, hipStream_t stream) {
-  const int st = launch(hlwq_split_attention_kernel<BITS, NR>, dim3(static_cast<uint32_t>(a.workers + tiles)), dim3(kSplitThreads), stream, a);
+  const int st = launch(hlwq_split_attention_kernel<BITS>, dim3(static_cast<uint32_t>(a.workers + tiles)), dim3(kSplitThreads), stream, a);
   if (st != HLWQ_OK) return st;
-  return launch(hlwq_split_join_kernel<16 * NR>, dim3(static_cast<uint32_t>(tiles * 16 * NR)), dim3(kSplitThreads), stream, a);
+  return launch(hlwq_split_join_kernel, dim3(static_cast<uint32_t>(tiles * kSplitRows)), dim3(kSplitThreads), stream, a);
 }
 
 // The shift that keeps the sum of the costs of tiles of m rows and blocks of kt
@@ -120,18 +125,17 @@ int launch_paged(int bits, AttnArgs a, void* ws, hipStream_t stream) {
   const int64_t chunk_groups = tiles_of(a.requests, a.rows, a.group, a.kv_heads, kChunkRows) * (kChunkRows / kChunkJoinRows);
   // the launches' sizes, and the split kernel's count of blocks
   const int64_t table_blocks = ceil_div(static_cast<int64_t>(a.width) << a.page_shift, kSplitBlock);
-  if (p.split_tiles * p.split_rows > 0xffffff || p.split_tiles * table_blocks > 0x7fffffff || (p.chunk && chunk_groups > 0xffffff))
+  if (p.split_tiles * kSplitRows > 0xffffff || p.split_tiles * table_blocks > 0x7fffffff || (p.chunk && chunk_groups > 0xffffff))
     return HLWQ_ERR_LIMIT;
   a.most = 0x7fffffff;
-  if (p.split_rows) {
+  const int32_t few = static_cast<int32_t>(few_rows(a.requests));
+  if (p.split) {
     a.partial = static_cast<float*>(ws);
     a.workers = static_cast<int32_t>(p.split_workers);
     a.slots = static_cast<int32_t>(p.split_slots);
     a.least = 1;
-    if (p.chunk) a.most = kFewRows;
-    const int st = p.split_rows == 16
-                       ? (bits == 3 ? launch_split<3, 1>(a, p.split_tiles, stream) : launch_split<2, 1>(a, p.split_tiles, stream))
-                       : (bits == 3 ? launch_split<3, 2>(a, p.split_tiles, stream) : launch_split<2, 2>(a, p.split_tiles, stream));
+    if (p.chunk) a.most = few;
+    const int st = bits == 3 ? launch_split<3>(a, p.split_tiles, stream) : launch_split<2>(a, p.split_tiles, stream);
     if (st != HLWQ_OK || !p.chunk) return st;
     a.most = 0x7fffffff;
   }
@@ -139,7 +143,7 @@ int launch_paged(int bits, AttnArgs a, void* ws, hipStream_t stream) {
   a.workers = kChunkWorkers;
   a.slots = 2 * kChunkWorkers;
   a.cost_shift = cost_shift_of(a, kChunkRows, kChunkBlock);
-  a.least = p.split_rows ? kFewRows + 1 : 1;
+  a.least = p.split ? few + 1 : 1;
   const int st = launch(bits == 3 ? hlwq_chunk_attention_kernel<3> : hlwq_chunk_attention_kernel<2>,
                         dim3(static_cast<uint32_t>(a.workers)), dim3(512), stream, a);
   if (st != HLWQ_OK) return st;

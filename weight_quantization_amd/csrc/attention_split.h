@@ -31,6 +31,7 @@ typedef uint32_t u32x2_4 __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t u32x3_4 __attribute__((ext_vector_type(3), aligned(4)));
 
 constexpr int kSplitThreads = 256;
+constexpr int kSplitRows = 16;
 constexpr int kSplitBlock = 128;  // tokens to a block
 constexpr int kSplitPitch = kDim + 4;  // floats to a row of sums in LDS: rows 4 banks apart
 
@@ -186,31 +187,26 @@ __device__ __forceinline__ float group_sum(float v) {
   return v + half_swap(v);
 }
 
-// One wave's sums over its tokens: o[n][s][i] is value 16 (4 (lane / 16) + i) +
-// s of row 16 n + lane % 16.
-template <int NR>
+// One wave's sums over its tokens: o[s][i] is value 16 (4 (lane / 16) + i) + s
+// of row lane % 16.
 struct SplitRows {
-  f32x4 o[NR][16];
-  float m[NR], l[NR];
+  f32x4 o[16];
+  float m, l;
   int exponent;  // of the pages' values: sums are over p n 2^-exponent
 };
 
-template <int NR>
-__device__ __forceinline__ void clear(SplitRows<NR>& r) {
+__device__ __forceinline__ void clear(SplitRows& r) {
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-#pragma unroll
-    for (int s = 0; s < 16; ++s) r.o[n][s] = f32x4{0, 0, 0, 0};
-    r.m[n] = -FLT_MAX;
-    r.l[n] = 0;
-  }
+  for (int s = 0; s < 16; ++s) r.o[s] = f32x4{0, 0, 0, 0};
+  r.m = -FLT_MAX;
+  r.l = 0;
   r.exponent = -64;
 }
 
-// Softmax weights of eight scores a lane and row set, s[..] times factor[n];
+// Softmax weights of a lane's eight scores, s[..] times factor;
 // gone[i]: the token is not seen by the row.
-template <int NR, class G>
-__device__ __forceinline__ void weigh(SplitRows<NR>& r, int n, float (&s)[8], float factor, bool masked, G gone, float (&p)[8]) {
+template <class G>
+__device__ __forceinline__ void weigh(SplitRows& r, float (&s)[8], float factor, bool masked, G gone, float (&p)[8]) {
   if (masked) {
     keep_branch();
 #pragma unroll
@@ -220,38 +216,35 @@ __device__ __forceinline__ void weigh(SplitRows<NR>& r, int n, float (&s)[8], fl
 #pragma unroll
   for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
   mx = group_max(mx) * factor;
-  if (__any(mx - r.m[n] > kLazy)) {
-    const float mn = fmaxf(r.m[n], mx);
-    const float f = fast_exp2(r.m[n] - mn);
-    r.m[n] = mn;
-    r.l[n] *= f;
+  if (__any(mx - r.m > kLazy)) {
+    const float mn = fmaxf(r.m, mx);
+    const float f = fast_exp2(r.m - mn);
+    r.m = mn;
+    r.l *= f;
 #pragma unroll
-    for (int x = 0; x < 16; ++x) r.o[n][x] *= f;
+    for (int x = 0; x < 16; ++x) r.o[x] *= f;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    p[i] = fast_exp2(__builtin_fmaf(s[i], factor, -r.m[n]));
-    r.l[n] += p[i];
+    p[i] = fast_exp2(__builtin_fmaf(s[i], factor, -r.m));
+    r.l += p[i];
   }
 }
 
 // 32 encoded tokens; there: how many of each sixteen exist.
-template <int BITS, int NR>
-__device__ __forceinline__ void code_step(SplitRows<NR>& r, const u32x4 (&q)[NR][8], const float (&factor)[NR],
-                                          const Codes<BITS>& c, int there_a, int there_b, int lane) {
+template <int BITS>
+__device__ __forceinline__ void code_step(SplitRows& r, const u32x4 (&q)[8], float factor, const Codes<BITS>& c, int there_a,
+                                          int there_b, int lane) {
   const int h4 = lane >> 4;
   const bool odd = lane & 1, masked = there_a < 16 || there_b < 16;
-  f32x4 s[NR][2];
+  f32x4 s[2];
 #pragma unroll
   for (int sub = 0; sub < 2; ++sub) {
     u32x4 f[8];
     k_fragments<BITS>(c, sub, f);
+    s[sub] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      s[n][sub] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int x = 0; x < 8; ++x) s[n][sub] = mfma16<true>(f[x], q[n][x], s[n][sub]);
-    }
+    for (int x = 0; x < 8; ++x) s[sub] = mfma16<true>(f[x], q[x], s[sub]);
   }
   float kn[8], vn[8];
   const auto gone = [&](int i) { return 4 * h4 + (i & 3) >= (i < 4 ? there_a : there_b); };
@@ -280,21 +273,16 @@ __device__ __forceinline__ void code_step(SplitRows<NR>& r, const u32x4 (&q)[NR]
     const float f = __builtin_ldexpf(1.0f, max(r.exponent - e, -126));
     r.exponent = e;
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) r.o[n][x] *= f;
+    for (int x = 0; x < 16; ++x) r.o[x] *= f;
   }
   const float over = __builtin_ldexpf(kTopWeight, -r.exponent);
-  u32x4 pf[NR];
+  u32x4 pf;
+  float t[8], p[8];
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    float t[8], p[8];
+  for (int i = 0; i < 8; ++i) t[i] = s[i >> 2][i & 3] * kn[i];
+  weigh(r, t, factor, masked, gone, p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = s[n][i >> 2][i & 3] * kn[i];
-    weigh<NR>(r, n, t, factor[n], masked, gone, p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pf[n][i] = pack_f16x2(p[2 * i] * (vn[2 * i] * over), p[2 * i + 1] * (vn[2 * i + 1] * over));
-  }
+  for (int i = 0; i < 4; ++i) pf[i] = pack_f16x2(p[2 * i] * (vn[2 * i] * over), p[2 * i + 1] * (vn[2 * i + 1] * over));
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t ca[8], cb[8];
@@ -304,8 +292,7 @@ __device__ __forceinline__ void code_step(SplitRows<NR>& r, const u32x4 (&q)[NR]
     for (int x = 0; x < 8; ++x) {
       const u32x2 a = look_up<BITS>(ca[x]), b = look_up<BITS>(cb[x]);
       const u32x4 f{a[0], a[1], b[0], b[1]};
-#pragma unroll
-      for (int n = 0; n < NR; ++n) r.o[n][8 * half + x] = mfma16<true>(f, pf[n], r.o[n][8 * half + x]);
+      r.o[8 * half + x] = mfma16<true>(f, pf, r.o[8 * half + x]);
     }
   }
 }
@@ -341,13 +328,11 @@ struct Tokens {
   }
 };
 
-// 32 bf16 tokens from k0 on; lim[n]: last token that the lane's row of set n
-// sees; last: the last one there is.  masked: some row does not see some token;
-// mixed: nor do all that are there see the same.
-template <int NR>
-__device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR][8], float factor, int64_t k0, int64_t last,
-                                           const int64_t (&lim)[NR], bool masked, bool mixed, const Tokens& tokens,
-                                           int lane) {
+// 32 bf16 tokens from k0 on; lim: last token that the lane's row sees; last:
+// the last one there is.  masked: some row does not see some token; mixed: nor
+// do all that are there see the same.
+__device__ __forceinline__ void token_step(SplitRows& r, const u32x4 (&q)[8], float factor, int64_t k0, int64_t last,
+                                           int64_t lim, bool masked, bool mixed, const Tokens& tokens, int lane) {
   const int c = lane & 15, h4 = lane >> 4;
   const auto token = [&](int i) { return k0 + 16 * (i >> 2) + 4 * h4 + (i & 3); };
   // every load before the first use
@@ -368,25 +353,20 @@ __device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR
   for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
     for (int x = 0; x < 8; ++x) asm volatile("" : "+v"(f[sub][x]));
-  f32x4 s[NR][2];
+  f32x4 s[2];
 #pragma unroll
-  for (int sub = 0; sub < 2; ++sub)
+  for (int sub = 0; sub < 2; ++sub) {
+    s[sub] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      s[n][sub] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int x = 0; x < 8; ++x) s[n][sub] = mfma16<false>(f[sub][x], q[n][x], s[n][sub]);
-    }
-  u32x4 pf[NR];
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    float t[8], p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = s[n][i >> 2][i & 3];
-    weigh<NR>(r, n, t, factor, masked, [&](int i) { return token(i) > lim[n]; }, p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pf[n][i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+    for (int x = 0; x < 8; ++x) s[sub] = mfma16<false>(f[sub][x], q[x], s[sub]);
   }
+  u32x4 pf;
+  float t[8], p[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = s[i >> 2][i & 3];
+  weigh(r, t, factor, masked, [&](int i) { return token(i) > lim; }, p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pf[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
   // as in key_step: where some rows see a token and others do not, 0 times its
   // value must stay 0
   uint32_t left = 0;
@@ -408,8 +388,7 @@ __device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR
       for (int i = 0; i < 4; ++i) {
         f[i] = __builtin_amdgcn_perm(v[half][2 * i + 1][x >> 1], v[half][2 * i][x >> 1], sel);
       }
-#pragma unroll
-      for (int n = 0; n < NR; ++n) r.o[n][8 * half + x] = mfma16<false>(f, pf[n], r.o[n][8 * half + x]);
+      r.o[8 * half + x] = mfma16<false>(f, pf, r.o[8 * half + x]);
     }
   }
   if (mixed && __any(left != 0)) {
@@ -420,8 +399,7 @@ __device__ __forceinline__ void token_step(SplitRows<NR>& r, const u32x4 (&q)[NR
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const float v = bf16_lo(p[16 * i + x]);
-#pragma unroll
-          for (int n = 0; n < NR; ++n) r.o[n][x][i] += k0 + k <= lim[n] && !__builtin_isfinite(v) ? v : 0.0f;
+          r.o[x][i] += k0 + k <= lim && !__builtin_isfinite(v) ? v : 0.0f;
         }
     }
   }
@@ -440,63 +418,58 @@ constexpr int kSplitStats = 4 * 16 * 2;  // floats
 // The four waves' sums of a tile's `there` rows joined, rotated if they are
 // over centroids, and given to write(row, sums of lane's four values, maximum,
 // sum of weights).
-template <int NR, class F>
-__device__ __forceinline__ void join_waves(SplitRows<NR>& r, bool enc, int there, float* lds, int lane, int wave, F write) {
+template <class F>
+__device__ __forceinline__ void join_waves(SplitRows& r, bool enc, int there, float* lds, int lane, int wave, F write) {
   const int c = lane & 15, h4 = lane >> 4;
   const float f = enc ? __builtin_ldexpf(1.0f / kTopWeight, r.exponent - 8) : 1.0f;  // H c n / 256
   float* stat = lds + 4 * 16 * kSplitPitch;
+  const float l = group_sum(r.l);
+  __syncthreads();
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    if (16 * n >= there) continue;
-    const float l = group_sum(r.l[n]);
-    __syncthreads();
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int x = 0; x < 4; ++x) {
+      f32x4 v;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        f32x4 v;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = r.o[n][4 * x + k][i] * f;
-        *reinterpret_cast<f32x4*>(lds + (wave * 16 + c) * kSplitPitch + 16 * (4 * h4 + i) + 4 * x) = v;
-      }
-    if (h4 == 0) {
-      stat[(wave * 16 + c) * 2] = r.m[n];
-      stat[(wave * 16 + c) * 2 + 1] = l;
+      for (int k = 0; k < 4; ++k) v[k] = r.o[4 * x + k][i] * f;
+      *reinterpret_cast<f32x4*>(lds + (wave * 16 + c) * kSplitPitch + 16 * (4 * h4 + i) + 4 * x) = v;
     }
-    __syncthreads();
+  if (h4 == 0) {
+    stat[(wave * 16 + c) * 2] = r.m;
+    stat[(wave * 16 + c) * 2 + 1] = l;
+  }
+  __syncthreads();
 #pragma clang loop unroll(disable)
-    for (int row = wave; row < min(there - 16 * n, 16); row += 4) {
-      float2 s[4];
-      float m = -FLT_MAX;
+  for (int row = wave; row < min(there, kSplitRows); row += 4) {
+    float2 s[4];
+    float m = -FLT_MAX;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        s[w] = *reinterpret_cast<const float2*>(stat + (w * 16 + row) * 2);
-        m = fmaxf(m, s[w].x);
-      }
-      float o[4] = {0, 0, 0, 0}, sum = 0;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float g = fast_exp2(s[w].x - m);
-        sum += s[w].y * g;
-        const f32x4 v = *reinterpret_cast<const f32x4*>(lds + (w * 16 + row) * kSplitPitch + 4 * lane);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] += v[e] * g;
-      }
-      if (enc) wave_fwht(o, lane);
-      write(16 * n + row, f32x4{o[0], o[1], o[2], o[3]}, m, sum);
+    for (int w = 0; w < 4; ++w) {
+      s[w] = *reinterpret_cast<const float2*>(stat + (w * 16 + row) * 2);
+      m = fmaxf(m, s[w].x);
     }
+    float o[4] = {0, 0, 0, 0}, sum = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float g = fast_exp2(s[w].x - m);
+      sum += s[w].y * g;
+      const f32x4 v = *reinterpret_cast<const f32x4*>(lds + (w * 16 + row) * kSplitPitch + 4 * lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += v[e] * g;
+    }
+    if (enc) wave_fwht(o, lane);
+    write(row, f32x4{o[0], o[1], o[2], o[3]}, m, sum);
   }
 }
 
 // What a request asks of the split kernel.
-template <int M>
 struct SplitWork {
   Extent e;
   int32_t tiles, blocks;  // tiles of a KV head, page blocks of each
   __device__ __forceinline__ SplitWork(const AttnArgs& a, const Extent& x) {
     e = x;
     const int32_t r = e.n * a.group;
-    tiles = r >= a.least && r <= a.most ? static_cast<int32_t>(ceil_div(r, M)) : 0;
+    tiles = r >= a.least && r <= a.most ? static_cast<int32_t>(ceil_div(r, kSplitRows)) : 0;
     blocks = static_cast<int32_t>(ceil_div(e.paged, kSplitBlock));
   }
 };
@@ -505,10 +478,10 @@ struct SplitWork {
 __device__ __forceinline__ int32_t tile_slot(const AttnArgs& a, int32_t tile, int which) { return 2 * (a.workers + tile) + which; }
 
 // Pages [u0, u1) of a tile.
-template <int BITS, int NR, class F>
+template <int BITS, class F>
 __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e, int32_t b, int32_t head, int32_t r0, int32_t u0,
                                              int32_t u1, float* lds, int lane, int wave, F write) {
-  constexpr int M = 16 * NR;
+  constexpr int M = kSplitRows;
   constexpr int kQPitch = kDim + 8;  // fp16 to a row of rotated q in LDS
   const int c = lane & 15, h4 = lane >> 4;
   const int32_t rows = e.n * a.group;
@@ -568,22 +541,18 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
     if (lane == 0) qf[row] = fmaxf(__builtin_ldexpf(a.factor, ex - 8), __FLT_DENORM_MIN__);
   }
   __syncthreads();
-  u32x4 q[NR][8];
-  float factor[NR];
+  u32x4 q[8];
+  const float factor = qf[c];
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    factor[n] = qf[16 * n + c];
+  for (int x = 0; x < 8; ++x) {
+    uint32_t d[4];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      uint32_t d[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        d[k] = *reinterpret_cast<const uint32_t*>(ql + (16 * n + c) * kQPitch + 64 * h4 + dim_of<BITS>(x, k));
-      q[n][x] = u32x4{__builtin_amdgcn_perm(d[1], d[0], 0x05040100u), __builtin_amdgcn_perm(d[3], d[2], 0x05040100u),
-                      __builtin_amdgcn_perm(d[1], d[0], 0x07060302u), __builtin_amdgcn_perm(d[3], d[2], 0x07060302u)};
-    }
+    for (int k = 0; k < 4; ++k)
+      d[k] = *reinterpret_cast<const uint32_t*>(ql + c * kQPitch + 64 * h4 + dim_of<BITS>(x, k));
+    q[x] = u32x4{__builtin_amdgcn_perm(d[1], d[0], 0x05040100u), __builtin_amdgcn_perm(d[3], d[2], 0x05040100u),
+                 __builtin_amdgcn_perm(d[1], d[0], 0x07060302u), __builtin_amdgcn_perm(d[3], d[2], 0x07060302u)};
   }
-  SplitRows<NR> r;
+  SplitRows r;
   clear(r);
   // block u while the codes of u + 1 are on their way; by twos, as moving them
   // from one set of registers to the other took a tenth of the step
@@ -592,49 +561,45 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
     for (int k = 0; k < 2; ++k) {
       if (u + k >= u1) break;
       if (u + k + 1 < u1) fetch(u + k + 1, codes[k ^ 1], there[k ^ 1]);
-      if (there[k][0] + there[k][1] > 0) code_step<BITS, NR>(r, q, factor, codes[k], there[k][0], there[k][1], lane);
+      if (there[k][0] + there[k][1] > 0) code_step<BITS>(r, q, factor, codes[k], there[k][0], there[k][1], lane);
     }
-  join_waves<NR>(r, true, rows - r0, lds, lane, wave, write);
+  join_waves(r, true, rows - r0, lds, lane, wave, write);
 }
 
 // The window's and the step's own tokens of a tile.
-template <int NR, class F>
+template <class F>
 __device__ __forceinline__ void attend_tokens(const AttnArgs& a, const Extent& e, int32_t b, int32_t head, int32_t r0, float* lds,
                                               int lane, int wave, F write) {
-  constexpr int M = 16 * NR;
+  constexpr int M = kSplitRows;
   const int c = lane & 15, h4 = lane >> 4;
   const int32_t rows = e.n * a.group;
   const Tokens tokens(a, e, b, head);
   const int64_t first = tokens.near + token_of(r0, a.group), last = tokens.near + token_of(min(r0 + M, rows) - 1, a.group);
-  u32x4 q[NR][8];
-  int64_t lim[NR];
+  u32x4 q[8];
+  const int32_t row = min(r0 + c, rows - 1), token = token_of(row, a.group);
+  const uint16_t* p = a.q + (e.begin + static_cast<int64_t>(token)) * a.q_stride + (head * a.group + (row - token * a.group)) * kDim + 8 * h4;
+  const int64_t lim = tokens.near + token;
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const int32_t row = min(r0 + 16 * n + c, rows - 1), token = token_of(row, a.group);
-    const uint16_t* p = a.q + (e.begin + static_cast<int64_t>(token)) * a.q_stride + (head * a.group + (row - token * a.group)) * kDim + 8 * h4;
-    lim[n] = tokens.near + token;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      q[n][x] = *reinterpret_cast<const u32x4*>(p + 32 * x);
-      if (a.scale < 0) q[n][x] ^= 0x80008000u;
-    }
+  for (int x = 0; x < 8; ++x) {
+    q[x] = *reinterpret_cast<const u32x4*>(p + 32 * x);
+    if (a.scale < 0) q[x] ^= 0x80008000u;
   }
-  SplitRows<NR> r;
+  SplitRows r;
   clear(r);
   for (int64_t k0 = 32 * wave; k0 <= last; k0 += kSplitBlock)
-    token_step<NR>(r, q, a.factor, k0, last, lim, k0 + 31 > first, k0 + 31 > first && first < last, tokens, lane);
-  join_waves<NR>(r, false, rows - r0, lds, lane, wave, write);
+    token_step(r, q, a.factor, k0, last, lim, k0 + 31 > first, k0 + 31 > first && first < last, tokens, lane);
+  join_waves(r, false, rows - r0, lds, lane, wave, write);
 }
 
-template <int BITS, int NR>
-__global__ void __launch_bounds__(kSplitThreads) __attribute__((amdgpu_waves_per_eu(NR == 1 ? 2 : 1, NR == 1 ? 2 : 1)))
+template <int BITS>
+__global__ void __launch_bounds__(kSplitThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 hlwq_split_attention_kernel(const AttnArgs a) {
-  constexpr int M = 16 * NR;
+  constexpr int M = kSplitRows;
   __shared__ __attribute__((aligned(16))) float lds[4 * 16 * kSplitPitch + kSplitStats];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const auto tiles = [&](const Extent& e) { return SplitWork<M>(a, e).tiles * a.kv_heads; };
+  const auto tiles = [&](const Extent& e) { return SplitWork(a, e).tiles * a.kv_heads; };
   const auto cost = [&](const Extent& e) {
-    const SplitWork<M> w(a, e);
+    const SplitWork w(a, e);
     return w.tiles * w.blocks * a.kv_heads;
   };
   const auto to_slot = [&](int32_t slot) {
@@ -650,10 +615,10 @@ hlwq_split_attention_kernel(const AttnArgs a) {
     Finder<decltype(tiles), Nothing> finder(a, tiles, Nothing{});
     if (x >= finder.total) return;
     const Found f = finder.find(x);
-    const SplitWork<M> w(a, f.e);
+    const SplitWork w(a, f.e);
     const int32_t head = quotient(f.rest, w.tiles), r0 = (f.rest - head * w.tiles) * M;
     const int32_t slot = tile_slot(a, x, 1);
-    attend_tokens<NR>(a, w.e, f.b, head, r0, lds, lane, wave, [&](int row, f32x4 o, float m, float l) {
+    attend_tokens(a, w.e, f.b, head, r0, lds, lane, wave, [&](int row, f32x4 o, float m, float l) {
       if (w.blocks == 0)
         write_row(a, w.e.begin, head, r0 + row, o, l, lane);
       else
@@ -670,7 +635,7 @@ hlwq_split_attention_kernel(const AttnArgs a) {
   int32_t left = share.bound(worker + 1) - share.bound(worker), b = first.b, rest = first.rest, before = first.before;
 #pragma clang loop unroll(disable)
   while (left > 0 && b < a.requests) {
-    const SplitWork<M> w(a, b == first.b ? first.e : extent_of(a, b));
+    const SplitWork w(a, b == first.b ? first.e : extent_of(a, b));
     const int32_t tile = w.blocks ? quotient(rest, w.blocks) : 0;  // of all KV heads'
     if (w.blocks == 0 || tile >= w.tiles * a.kv_heads) {            // past the request's last
       before += w.tiles * a.kv_heads;
@@ -681,7 +646,7 @@ hlwq_split_attention_kernel(const AttnArgs a) {
     const int32_t u0 = rest - tile * w.blocks, u1 = min(u0 + left, w.blocks);
     const int32_t head = quotient(tile, w.tiles);
     const int32_t slot = u0 == 0 && u1 == w.blocks ? tile_slot(a, before + tile, 0) : 2 * worker + (u0 > 0 ? 0 : 1);
-    attend_pages<BITS, NR>(a, w.e, b, head, (tile - head * w.tiles) * M, u0, u1, lds, lane, wave, to_slot(slot));
+    attend_pages<BITS>(a, w.e, b, head, (tile - head * w.tiles) * M, u0, u1, lds, lane, wave, to_slot(slot));
     __syncthreads();
     left -= u1 - u0;
     rest += u1 - u0;
@@ -690,20 +655,20 @@ hlwq_split_attention_kernel(const AttnArgs a) {
 
 // Joins a row of a tile from the partial sums of its pages and its other
 // tokens, each wave every fourth.
-template <int M>
 __global__ void __launch_bounds__(kSplitThreads) hlwq_split_join_kernel(const AttnArgs a) {
+  constexpr int M = kSplitRows;
   __shared__ __attribute__((aligned(16))) float lds[4 * kSplitPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const auto tiles = [&](const Extent& e) { return SplitWork<M>(a, e).tiles * a.kv_heads; };
+  const auto tiles = [&](const Extent& e) { return SplitWork(a, e).tiles * a.kv_heads; };
   const auto cost = [&](const Extent& e) {
-    const SplitWork<M> w(a, e);
+    const SplitWork w(a, e);
     return w.tiles * w.blocks * a.kv_heads;
   };
   Finder<decltype(tiles), decltype(cost)> finder(a, tiles, cost);
   const int32_t x = blockIdx.x / M, row = blockIdx.x % M;
   if (x >= finder.total) return;
   const Found f = finder.find(x);
-  const SplitWork<M> w(a, f.e);
+  const SplitWork w(a, f.e);
   const int32_t head = quotient(f.rest, w.tiles), r0 = (f.rest - head * w.tiles) * M;
   if (w.blocks == 0 || r0 + row >= w.e.n * a.group) return;
   const Share share(Finder<decltype(cost), Nothing>(a, cost, Nothing{}).total, a.workers, 1);
