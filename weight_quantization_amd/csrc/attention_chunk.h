@@ -181,12 +181,14 @@ __device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Ex
   const auto exponent_of = [&](int32_t u) {
     return __builtin_amdgcn_readfirstlane(lds_at<int32_t>(base + L::side + (u & 1) * L::kSide + 2 * L::kLine + 4));
   };
-  // lane = token of the block, wave = which 32 of its 256 codes
+  // lane = token of the block; which 32 of its 256 codes is turned by lane / 8,
+  // so that the reads (24 or 16 words apart) fall on all banks, and with them
+  // the writes
   const auto unpack = [&](int32_t u) {
     if (u >= u1) return;
-    const int lane = lane_now();
-    const uint32_t raw = base + L::raw + (u & 1) * 2 * L::kCodes + lane * 32 * BITS + wave * 4 * BITS;
-    const uint32_t to = base + (u & 1) * L::kStage + lane * 512 + ((4 * wave) ^ swizzle(lane)) * 16;
+    const int lane = lane_now(), run = (wave + (lane >> 3)) & 7;
+    const uint32_t raw = base + L::raw + (u & 1) * 2 * L::kCodes + lane * 32 * BITS + run * 4 * BITS;
+    const uint32_t to = base + (u & 1) * L::kStage + lane * 512 + ((4 * run) ^ swizzle(lane)) * 16;
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       Run<BITS> codes;
