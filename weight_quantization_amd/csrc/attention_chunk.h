@@ -6,6 +6,13 @@
 // centroids while the 64 before are multiplied, so that 256 query rows share
 // one unpacking; then the sums are rotated in registers and the window's and
 // the step's own tokens follow in bf16.
+//
+// Measured: 1024 tokens over 16000 (24 query heads on 4, 3 bits, 415 GFLOP)
+// take 525 to 560 us (the card slows its clock within ten calls) and the join
+// 20.  About 90 us of that are there however few the pages: two rotations of
+// 256 x 256 sums a stretch, 92 MB of partial sums, and 80 KB of instructions
+// that run once.  A block of 64 tokens takes about 4.1 us, of which the products
+// are 1.8; matrix cores 36% busy, VALU issue 42%.
 #pragma once
 
 #include "attention_split.h"

@@ -16,11 +16,22 @@
 //     rotated once at the end.
 // A workgroup is four waves with 32 tokens each to a block of 128.  Some
 // workgroups share the pages' blocks of all requests in equal stretches, one
-// more per tile (sixteen or 32 rows of a KV head) takes the window's and the
-// step's own tokens; each joins its waves' sums in LDS and leaves them in the
+// more per tile (sixteen rows of a KV head) takes the window's and the step's
+// own tokens; each joins its waves' sums in LDS and leaves them in the
 // workspace, and a second kernel joins a tile's.  A workgroup runs through its
 // code once or twice, so what bounds a short call is the fetching of
 // instructions: what is not in the loop over blocks is kept small, not unrolled.
+//
+// Sixteen rows take 256 registers, so that two workgroups share a CU; 32 rows
+// read each code half as often but take all 512 and leave one, which took 28.5
+// us for 24 rows over 16000 tokens (24.7) and 47 for 8 requests over 4000 (34).
+//
+// Measured (24 query heads on 4, kernel and join): one token over 500, 9.7 + 4.0
+// us; over 32767, 18.7 + 5.2 us for 26 MB, of which 5.5 us are memory's and the
+// rest a chain of latencies (lengths, pages, codes, partial sums).  48 ragged
+// requests, 2 bits, 115 MB: 48.6 + 7.4 us, VALU issue 46% busy and the matrix
+// cores 9%; a step of 32 tokens takes about 600 VALU instructions a wave, four
+// tenths of them look-ups.
 #pragma once
 
 #include "attention_common.h"

@@ -8,11 +8,19 @@
 // sums O^T stay in 128 registers, Q in 64.
 //
 // What bounds it: per 32 keys a wave's products take 1024 cycles of its SIMD's
-// matrix core and it reads 32 KB from LDS, two waves a SIMD share both.  With
-// eight waves to a workgroup the CU reads 256 KB in 2048 matrix cycles, half
-// of what LDS gives (K as b128, V transposed on the way by ds_read_tr16);
-// softmax and address arithmetic (about 500 cycles a wave) run beside the
-// other wave's products.
+// matrix core, its softmax and addresses about 200 VALU instructions (1000
+// cycles with the exponentials), and it reads 32 KB from LDS.  With two waves a
+// SIMD the CU reads 256 KB in 2048 matrix cycles, half of what LDS gives (K as
+// b128, V transposed on the way by ds_read_tr16).  The two waves stand at the
+// same barrier once a block, so their softmaxes meet more often than they pass
+// each other: over 16384 tokens (24 heads on 4) the matrix cores are 60% busy
+// and VALU issue 33%, 2.78 ms, 1.19 PFLOP/s (1.36 to 1.56 in a large library
+// product).  517 tokens take 26 us, nine packed prompts of 1 to 2500 tokens
+// (16 heads on 2) 196 us.
+//
+// The loop over blocks may hold no load from scratch memory: one waits for all
+// loads under way, those of the next block among them (a single spilled
+// register took 6%).
 #pragma once
 
 #include "attention_common.h"
@@ -282,10 +290,14 @@ __device__ __forceinline__ void add_nonfinite(Rows& r, uint32_t flag, int64_t fr
 }
 
 // ---------------------------------------------------------------------------
-// Whole prompts.  A workgroup takes one tile of one KV head's rows, the tiles
-// of a sequence from its end on (a causal tile costs as many keys as its last
-// token has before it, so the long ones start first), consecutive workgroups
-// on different KV heads, so that an XCD's L2 serves as few heads as there are.
+// Whole prompts.  A workgroup takes one tile of one KV head's rows, of NW waves
+// with 32 each and blocks of KT keys; PARTS 2: half the waves take the first 32
+// keys of each block and half the others, for the same rows, and their sums are
+// joined at the end.  A causal tile costs as many keys as its last token has
+// before it, so the longest start first: of up to 64 sequences the longest of
+// all (212 us to 206 for nine packed prompts), else each sequence's.
+// Consecutive workgroups take different KV heads, so that an XCD's L2 serves as
+// few heads as there are.
 // ---------------------------------------------------------------------------
 
 template <int NW, int KT, int PARTS>

@@ -11,7 +11,9 @@ namespace {
 // ---------------------------------------------------------------------------
 // Page plan.  One workgroup plans the tables (the prefix sums over the
 // requests, the stack and the block table are one dependent chain), then a
-// grid over the rows fills the maps.
+// grid over the rows fills the maps.  Latency bounds both: 4.3 + 2.2 us for 64
+// requests of a token, 17.4 + 4.4 us for 1000 requests of which some are reset
+// and some begin.
 // ---------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 1024;
@@ -230,9 +232,11 @@ __global__ void __launch_bounds__(kRowThreads) hlwq_kv_plan_rows_kernel(const Pl
 // in the same call has the same lanes do both, in that order, so nobody waits
 // for anybody.
 //
-// What bounds a long append is the VALU (about 125 instructions a vector; a
-// whole wave to a vector, four values a lane, takes 320), what bounds a decode
-// step the chain of three loads behind one another.
+// What bounds a long append is the VALU (about 125 instructions a vector, 69%
+// busy; a whole wave to a vector, four values a lane, takes 320), what bounds a
+// decode step the chain of three loads behind one another.  Measured: a prompt
+// of 16383 tokens on 4 KV heads, 80 MB, 29 us (2.7 TB/s); a token of each of 32
+// requests 5.8 us.
 // ---------------------------------------------------------------------------
 
 struct AppendArgs {
