@@ -154,7 +154,7 @@ int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q
               const void* v, int64_t v_stride, const int32_t* cu, const int32_t* lens, const int32_t* table,
               int64_t max_pages, int64_t rows, float scale, void* out, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!c) return HLWQ_ERR_NULL;
-  std::vector<Span> spans;
+  Spans spans;
   int st = check_cache(*c, false, spans);
   if (st != HLWQ_OK) return st;
   bool nothing;
@@ -230,7 +230,7 @@ int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
     return st;
   if (!cu || !out) return HLWQ_ERR_NULL;
   if (misaligned(cu, 4) || misaligned(out, 16)) return HLWQ_ERR_ALIGN;
-  std::vector<Span> spans;
+  Spans spans;
   add_span(spans, q, qe, 2, false);
   add_span(spans, k, ke, 2, false);
   add_span(spans, v, ve, 2, false);

@@ -8,7 +8,6 @@
 #include <algorithm>
 #include <cfloat>
 #include <cstdint>
-#include <vector>
 
 #include "hlwq_attention.h"
 #include "hlwq_tables.inc"
@@ -146,21 +145,28 @@ struct Span {
   uintptr_t lo, hi;
   bool written;
 };
-inline void add_span(std::vector<Span>& v, const void* p, int64_t count, int64_t unit, bool written) {
+// Of one call: at most fourteen (an entry point allocates nothing, so that
+// nothing is thrown through it).
+struct Spans {
+  Span at[16];
+  int count = 0;
+};
+inline void add_span(Spans& v, const void* p, int64_t count, int64_t unit, bool written) {
   int64_t bytes;
   if (!p || count <= 0) return;
   if (!mul_ok(count, unit, &bytes)) bytes = INT64_MAX;
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   uintptr_t hi;
   if (__builtin_add_overflow(lo, static_cast<uintptr_t>(bytes), &hi)) hi = UINTPTR_MAX;
-  v.push_back(Span{lo, hi, written});
+  v.at[v.count++] = Span{lo, hi, written};
 }
 
 // HLWQ_ERR_OVERLAP if a written buffer shares a byte with any other buffer.
-inline int check_disjoint(std::vector<Span>& v) {
-  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+inline int check_disjoint(Spans& v) {
+  std::sort(v.at, v.at + v.count, [](const Span& a, const Span& b) { return a.lo < b.lo; });
   uintptr_t end_any = 0, end_written = 0;
-  for (const Span& x : v) {
+  for (int i = 0; i < v.count; ++i) {
+    const Span& x = v.at[i];
     if (x.lo < end_written || (x.written && x.lo < end_any)) return HLWQ_ERR_OVERLAP;
     end_any = std::max(end_any, x.hi);
     if (x.written) end_written = std::max(end_written, x.hi);
@@ -202,7 +208,7 @@ inline int check_rows(const void* p, int64_t stride, int64_t rows, int64_t heads
 }
 
 // Validate a cache and add its buffers to `spans` (written or read by the call).
-inline int check_cache(const hlwq_kv_cache& c, bool written, std::vector<Span>& spans) {
+inline int check_cache(const hlwq_kv_cache& c, bool written, Spans& spans) {
   if (c.head_dim != kDim) return HLWQ_ERR_BLOCK;
   if (c.bits != 3 && c.bits != 2) return HLWQ_ERR_BITS;
   if (c.n_pages < 0 || c.requests < 0 || c.kv_heads < 0 || c.n_residual < 0 || c.ring < c.n_residual)

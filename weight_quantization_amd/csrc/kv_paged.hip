@@ -423,7 +423,7 @@ int run_plan(const hlwq_kv_plan* p, hipStream_t stream) {
       (p->rows > 0 && (!p->row_request || !p->positions || !p->slots)) || (p->n_pages > 0 && !p->free_pages) ||
       (table > 0 && !p->block_table))
     return HLWQ_ERR_NULL;
-  std::vector<Span> spans;
+  Spans spans;
   const struct {
     const void* p;
     int64_t count;
@@ -468,7 +468,7 @@ int run_append(const hlwq_kv_cache* c, const void* k, int64_t k_stride, const vo
                const int32_t* cu, const int32_t* lens, const int32_t* row_request, const int32_t* slots, int64_t rows,
                hipStream_t stream) {
   if (!c) return HLWQ_ERR_NULL;
-  std::vector<Span> spans;
+  Spans spans;
   int st = check_cache(*c, true, spans);
   if (st != HLWQ_OK) return st;
   if (rows < 0) return HLWQ_ERR_SHAPE;
