@@ -43,13 +43,13 @@ def test_many_rows_of_few_tokens(wq):
         attention_case(wq, q_heads, [1300, 5, 260], [n, n, n], q_heads, 1, 3, 64, 128, 128)
 
 
-@pytest.mark.parametrize("count", [64, 65, 130])
-def test_wide_prompt_tiles(wq, count):
+@pytest.mark.parametrize("count,q_heads,kv_heads", [(64, 16, 8), (65, 16, 8), (130, 16, 8), (64, 32, 16), (65, 16, 16)])
+def test_wide_prompt_tiles(wq, count, q_heads, kv_heads):
     # enough tiles for those of 256 rows, the tiles of up to 64 sequences taken longest first
     rng = np.random.default_rng(count)
     lens = [int(n) for n in rng.integers(0, 100, count)]
     lens[3], lens[5], lens[count - 1] = 330, 257, 128
-    prompt_case(wq, count, lens, 16, 8, extra=8, pad=5)
+    prompt_case(wq, count, lens, q_heads, kv_heads, extra=8, pad=5)
 
 
 @pytest.mark.parametrize("lens,q_heads,kv_heads", [([700], 6, 1), ([384], 4, 4), ([513, 300, 400], 5, 1), ([1100, 1], 2, 1)])
@@ -75,11 +75,12 @@ def test_halved_prompt_tiles_nan_and_infinities(wq):
             assert (torch.isnan(got[hit]) if what == 0x7FC0 else torch.isposinf(got[hit])).all()
 
 
-def test_wide_prompt_tiles_nan_and_infinities(wq):
+@pytest.mark.parametrize("q_heads,kv_heads", [(16, 8), (32, 16)])
+def test_wide_prompt_tiles_nan_and_infinities(wq, q_heads, kv_heads):
     rng = np.random.default_rng(11)
     lens = [200] + [60] * 63
     n = sum(lens)
-    q, kv = bf16_bits(rng, n, 16, D), [bf16_bits(rng, n, 8, D) for _ in range(2)]
+    q, kv = bf16_bits(rng, n, q_heads, D), [bf16_bits(rng, n, kv_heads, D) for _ in range(2)]
     cu = i32(np.concatenate([[0], np.cumsum(lens)]))
     clean = wq.hlwq_prompt_attention(dev16(q), dev16(kv[0]), dev16(kv[1]), cu)
     for row, end in ((0, 200), (64, 200), (127, 200), (199, 200), (230, 260)):
@@ -87,7 +88,7 @@ def test_wide_prompt_tiles_nan_and_infinities(wq):
             dirty = [x.copy() for x in kv]
             dirty[i][row, 3, 40] = what
             got = wq.hlwq_prompt_attention(dev16(q), dev16(dirty[0]), dev16(dirty[1]), cu)
-            hit = torch.zeros(n, 16, D, dtype=torch.bool, device="cuda")
+            hit = torch.zeros(n, q_heads, D, dtype=torch.bool, device="cuda")
             hit[row:end, 6:8, slice(None) if i == 0 else 40] = True
             assert torch.equal(got[~hit], clean[~hit]), (row, i, hex(what))
             assert (torch.isnan(got[hit]) if what == 0x7FC0 else torch.isneginf(got[hit])).all()

@@ -37,14 +37,16 @@ int64_t prompt_groups(const AttnArgs& a, int64_t tile) {
 //   256 rows               19     36     52     79    124    214    731   2930
 //   128 rows               13     29     43     71    117    210    727   3023
 //   128 rows, keys halved  16     26     37     55    106    235    767
-// The lengths are on the device, so the host goes by their mean.
+// Four sequences of 1500 (568 tiles of 256 rows): 140, 130 and 165; nine of 1 to
+// 2500 on 2 KV heads (720 tiles): 196 and 207.  The lengths are on the device,
+// so the host goes by their mean.
 int launch_prompt(const AttnArgs& a, hipStream_t stream) {
   const int64_t wide = prompt_groups(a, 256), narrow = prompt_groups(a, 128);
   const bool halved = narrow <= 512 && a.rows >= int64_t{384} * a.requests;
-  const int64_t groups = wide >= 512 ? wide : narrow;
+  const int64_t groups = wide >= 640 ? wide : narrow;
   if (groups > 0x7fffff) return HLWQ_ERR_LIMIT;
   const dim3 grid(static_cast<uint32_t>(groups));
-  if (wide >= 512) return launch(hlwq_prompt_attention_kernel<8, 64, 1>, grid, dim3(512), stream, a);
+  if (wide >= 640) return launch(hlwq_prompt_attention_kernel<8, 64, 1>, grid, dim3(512), stream, a);
   if (halved) return launch(hlwq_prompt_attention_kernel<8, 64, 2>, grid, dim3(512), stream, a);
   return launch(hlwq_prompt_attention_kernel<4, 32, 1>, grid, dim3(256), stream, a);
 }
