@@ -22,7 +22,11 @@ namespace hlwq_kv {
 
 constexpr int kChunkRows = 256;
 constexpr int kChunkBlock = 64;   // tokens to a block
-constexpr int kChunkLeast = 4 * kBlockCost;  // cost that is worth a workgroup of its own
+// Cost that is worth a workgroup of its own.  One block against four (24 query
+// heads on 4, us): 8 requests of 40 over 500 tokens 60 and 75, of 20 over 4000
+// 71 and 72, one of 100 over 200 48 and 66, but one of 80 over 4000 94 and 84,
+// as there are more partial sums to join.
+constexpr int kChunkLeast = kBlockCost;
 
 // Butterflies over the 256 values of a row whose lanes hold 128 each, v[x] of
 // the lower half and of the upper half differing in one bit of their index,
