@@ -53,16 +53,16 @@ int launch_prompt(const AttnArgs& a, hipStream_t stream) {
 
 // How a paged call is shared among the kernels: requests of few query rows to a
 // KV head go to the split kernel, the others to the chunk kernel, which unpacks
-// each code once for 256 rows but takes a hundred microseconds however little
-// it has to do.  The lengths are on the device, so the host goes by the mean:
-// where it is few rows the split kernel takes every request; else both are
-// called, except for a single request.  Measured, split and chunk kernel (24
-// query heads on 4, 3 bits, us):
-//   one request over 16000 tokens, 36 rows     33  115;  120 rows   47  124;
-//                                  240 rows    68  140;  480 rows  112  133
-//   8 requests over 4000 tokens, 36 rows each  42   65;   60 rows   49   67;
-//                                  120 rows    79   71;  240 rows  126   93
-//   32 requests over 1000 tokens, 60 rows      66   70;  240 rows  224  105
+// each code once for 256 rows but takes 40 us however little it has to do.  The
+// lengths are on the device, so the host goes by the mean: where it is few rows
+// the split kernel takes every request; else both are called, except for a
+// single request.  Measured, split and chunk kernel (24 query heads on 4, 3
+// bits, us):
+//   one request over 16000 tokens, 36 rows     33   76;  120 rows   48   84;
+//                                  240 rows    70  100;  480 rows  112  112
+//   8 requests over 4000 tokens, 36 rows each  44   59;   60 rows   50   61;
+//                                  120 rows    79   67;  240 rows  128   91
+//   32 requests over 1000 tokens, 60 rows      67   70;  240 rows  224  106
 constexpr int64_t few_rows(int64_t requests) { return requests == 1 ? 256 : 64; }
 // Workgroups that the device holds at once: two to a CU of the split kernel
 // (256 registers a work-item), one of the chunk kernel.

@@ -8,8 +8,8 @@
 // the step's own tokens follow in bf16.
 //
 // Measured: 1024 tokens over 16000 (24 query heads on 4, 3 bits, 415 GFLOP)
-// take 525 to 560 us (the card slows its clock within ten calls) and the join
-// 20.  About 90 us of that are there however few the pages: two rotations of
+// take 535 to 580 us (the card slows its clock within ten calls) and the join
+// 21.  About 90 us of that are there however few the pages: two rotations of
 // 256 x 256 sums a stretch, 92 MB of partial sums, and 80 KB of instructions
 // that run once.  A block of 64 tokens takes about 4.1 us, of which the products
 // are 1.8; matrix cores 36% busy, VALU issue 42%.
@@ -24,8 +24,7 @@ constexpr int kChunkRows = 256;
 constexpr int kChunkBlock = 64;   // tokens to a block
 // Cost that is worth a workgroup of its own.  One block against four (24 query
 // heads on 4, us): 8 requests of 40 over 500 tokens 60 and 75, of 20 over 4000
-// 71 and 72, one of 100 over 200 48 and 66, but one of 80 over 4000 94 and 84,
-// as there are more partial sums to join.
+// 68 and 68, one of 100 over 200 42 and 64, one of 80 over 4000 75 and 73.
 constexpr int kChunkLeast = kBlockCost;
 
 // Butterflies over the 256 values of a row whose lanes hold 128 each, v[x] of
@@ -463,19 +462,33 @@ __global__ void __launch_bounds__(256) hlwq_chunk_join_kernel(const AttnArgs a) 
     l[i] = 0;
     o[i] = f32x4{0, 0, 0, 0};
   }
-  for (int32_t k = w0; k <= w1; ++k)
+  // four parts of four rows in flight: a part at a time, 480 rows over 16000
+  // tokens, four KV heads' two tiles of 32 parts each, took 133 us instead of 112
+  for (int32_t k0 = w0; k0 <= w1; k0 += 4) {
+    float2 s[4][4];
+    f32x4 v[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (row0 + i >= rows) continue;
-      const int32_t slot = 2 * k + (k == w0 ? 1 : 0);
-      const float2 s = *partial_stat<M>(a, slot, row0 + i);
-      const f32x4 v = *reinterpret_cast<const f32x4*>(partial_row<M>(a, slot, row0 + i) + 4 * lane);
-      const float mn = fmaxf(m[i], s.x);
-      const float f0 = fast_exp2(m[i] - mn), f1 = fast_exp2(s.x - mn);
-      m[i] = mn;
-      l[i] = l[i] * f0 + s.y * f1;
-      o[i] = o[i] * f0 + v * f1;
+    for (int j = 0; j < 4; ++j) {
+      const int32_t k = min(k0 + j, w1), slot = 2 * k + (k == w0 ? 1 : 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = min(row0 + i, rows - 1);
+        s[j][i] = *partial_stat<M>(a, slot, row);
+        v[j][i] = *reinterpret_cast<const f32x4*>(partial_row<M>(a, slot, row) + 4 * lane);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k0 + j <= w1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float mn = fmaxf(m[i], s[j][i].x);
+          const float f0 = fast_exp2(m[i] - mn), f1 = fast_exp2(s[j][i].x - mn);
+          m[i] = mn;
+          l[i] = l[i] * f0 + s[j][i].y * f1;
+          o[i] = o[i] * f0 + v[j][i] * f1;
+        }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (row0 + i < rows) write_row(a, w.e.begin, head, tile * M + row0 + i, o[i], l[i], lane);
