@@ -130,7 +130,7 @@ def test_nan_in_a_query_stays_in_its_row(wq, new):
         r = slice(cu[b], cu[b + 1])
         k, v = c.tokens_of(b, ctx[b], [x[r] for x in kv])
         mine = got[r].copy()
-        if b == 0:  # the row itself is judged above
+        if b == 0:  # the row itself was looked at above
             mine[1, 2] = pr.attend(clean[1, 2:3], k[0], v[0], ctx[0] + 2, 1 / 16, np.zeros(k.shape[1]), np.zeros(k.shape[1]))[0]
         pr.check_attention(mine, clean[r], k, v, pr.encoded(ctx[b], 128), ctx[b], 1)
 

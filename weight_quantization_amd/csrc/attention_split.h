@@ -588,7 +588,8 @@ __device__ __forceinline__ void attend_tokens(const AttnArgs& a, const Extent& e
   const int64_t first = tokens.near + token_of(r0, a.group), last = tokens.near + token_of(min(r0 + M, rows) - 1, a.group);
   u32x4 q[8];
   const int32_t row = min(r0 + c, rows - 1), token = token_of(row, a.group);
-  const uint16_t* p = a.q + (e.begin + static_cast<int64_t>(token)) * a.q_stride + (head * a.group + (row - token * a.group)) * kDim + 8 * h4;
+  const int32_t q_head = head * a.group + (row - token * a.group);
+  const uint16_t* p = a.q + (e.begin + static_cast<int64_t>(token)) * a.q_stride + q_head * kDim + 8 * h4;
   const int64_t lim = tokens.near + token;
 #pragma unroll
   for (int x = 0; x < 8; ++x) {
