@@ -303,3 +303,56 @@ def test_every_call_on_another_stream(wq):
 
     for x, y in zip(step(here, None), step(there, torch.cuda.Stream())):
         assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("new", [[1, 1], [3, 0], [200, 150]])
+def test_no_pages_at_all(wq, new):
+    """A pool of no pages and tables of no entries: encoded tokens are left out, window and own tokens are not."""
+    rng = np.random.default_rng(41)
+    c = Cache(rng, [300, 50], 2, 3, 64, 128, 128)
+    n = sum(new)
+    q, kv = bf16_bits(rng, n, 4, D), [bf16_bits(rng, n, 2, D) for _ in range(2)]
+    none = [torch.zeros(0, 2, 64, 96, dtype=torch.uint8, device="cuda"), torch.zeros(0, 2, 64, dtype=torch.float16, device="cuda")]
+    table = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    cu, lens = [0, new[0], n], i32([300 + new[0], 50 + new[1]])
+    out = wq.hlwq_kv_paged_attention(dev16(q), dev16(kv[0]), dev16(kv[1]), i32(cu), lens, table, *none, *none, *c.d[4:])
+    got = out.cpu().double().numpy()
+    for b, held in enumerate((300, 50)):
+        r, enc = slice(cu[b], cu[b + 1]), pr.encoded(held, 128)
+        if new[b]:
+            k, v = (x[:, enc:] for x in c.tokens_of(b, held, [x[r] for x in kv]))
+            pr.check_attention(got[r], f64(q[r]), k, v, 0, held - enc, 2)
+
+
+def test_nothing_to_do(wq):
+    c = Cache(np.random.default_rng(42), [300, 50], 2, 3, 64, 128, 128)
+    before = [x.clone() for x in c.d]
+    no = [torch.zeros(0, h, D, dtype=torch.bfloat16, device="cuda") for h in (4, 2, 2)]
+    cu, lens, table = i32([0, 0, 0]), i32([300, 50]), i32(c.table)
+    assert wq.hlwq_kv_paged_attention(*no, cu, lens, table, *c.tensors()).shape == (0, 4, D)
+    assert wq.hlwq_prompt_attention(*no, cu).shape == (0, 4, D)
+    wq.hlwq_kv_paged_append(*no[1:], cu, lens, cu[:0], cu[:0], *c.tensors())
+    # rows that nobody owns are left as they were
+    rows = [torch.ones(3, h, D, dtype=torch.bfloat16, device="cuda") for h in (4, 2, 2)]
+    out = torch.full((3, 4, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    wq.hlwq_kv_paged_attention(*rows, cu, lens, table, *c.tensors(), out=out)
+    wq.hlwq_prompt_attention(*rows, cu, out=out)
+    wq.hlwq_prompt_attention(*rows, i32([0]), out=out)
+    wq.hlwq_kv_paged_append(*rows[1:], cu, lens, i32([-1] * 3), i32([-1] * 3), *c.tensors())
+    torch.cuda.synchronize()
+    assert bool((out == 5).all())
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(before, c.d))
+
+
+def test_same_call_twice_gives_the_same_bits(wq):
+    rng = np.random.default_rng(43)
+    c = Cache(rng, [900, 2000, 64], 2, 2, 32, 128, 128)
+    for new in ([1, 1, 1], [90, 1, 200]):
+        n = sum(new)
+        q, k, v = (dev16(bf16_bits(rng, n, h, D)) for h in (12, 2, 2))
+        cu, lens = i32(np.concatenate([[0], np.cumsum(new)])), i32([900 + new[0], 2000 + new[1], 64 + new[2]])
+        first = wq.hlwq_kv_paged_attention(q, k, v, cu, lens, i32(c.table), *c.tensors(), bits=2)
+        prompt = wq.hlwq_prompt_attention(q, k, v, cu)
+        for _ in range(5):
+            assert torch.equal(first, wq.hlwq_kv_paged_attention(q, k, v, cu, lens, i32(c.table), *c.tensors(), bits=2))
+            assert torch.equal(prompt, wq.hlwq_prompt_attention(q, k, v, cu))
