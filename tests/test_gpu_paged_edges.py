@@ -1,0 +1,27 @@
+"""GPU tests of the serving operators at values that lengths and queries may take but hardly ever do."""
+import numpy as np
+import pytest
+
+from test_gpu_paged import Cache, D, bf16_bits, dev16, i32, wq  # noqa: F401
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+# few rows of one request, many of one, and both at once
+STEPS = [[5], [300], [2, 200]]
+
+
+@pytest.mark.parametrize("new", STEPS)
+def test_lengths_far_below_the_new_tokens(wq, new):
+    """Any length below a request's new tokens counts as equal to them, those whose difference passes 32 bits too."""
+    rng = np.random.default_rng(len(new))
+    n = len(new)
+    c = Cache(rng, [700] * n, 2, 3, 64, 128, 128)  # pages and a window that the step must not see
+    q, k, v = (dev16(bf16_bits(rng, sum(new), h, D)) for h in (4, 2, 2))
+    cu = i32(np.concatenate([[0], np.cumsum(new)]))
+    want = wq.hlwq_kv_paged_attention(q, k, v, cu, i32(new), i32(c.table), *c.tensors())
+    assert bool(torch.isfinite(want).all())
+    for low in (0, -1, -2 ** 30, 1 - 2 ** 31, -2 ** 31):
+        got = wq.hlwq_kv_paged_attention(q, k, v, cu, i32([low] * n), i32(c.table), *c.tensors())
+        assert torch.equal(got, want), low

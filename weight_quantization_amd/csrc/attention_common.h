@@ -63,7 +63,7 @@ __device__ __forceinline__ Extent extent_of(const AttnArgs& a, int32_t begin, in
   Extent e;
   e.begin = begin;
   e.n = n;
-  e.held = max(len - n, 0);
+  e.held = len > n ? len - n : 0;  // a length may be anything: len - n alone could pass 32 bits
   e.enc = a.lens ? max(e.held - a.n_res, int64_t{0}) : 0;
   e.paged = a.n_pages > 0 ? min(e.enc, static_cast<int64_t>(a.width) << a.page_shift) : 0;
   return e;
