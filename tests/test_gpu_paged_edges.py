@@ -25,3 +25,22 @@ def test_lengths_far_below_the_new_tokens(wq, new):
     for low in (0, -1, -2 ** 30, 1 - 2 ** 31, -2 ** 31):
         got = wq.hlwq_kv_paged_attention(q, k, v, cu, i32([low] * n), i32(c.table), *c.tensors())
         assert torch.equal(got, want), low
+
+
+@pytest.mark.parametrize("new", STEPS)
+def test_queries_near_the_smallest(wq, new):
+    """Queries below 2^-118, subnormal ones among them: no score of theirs differs from 0 by what a weight could hold, so
+    that the rows are those of queries of zero."""
+    rng = np.random.default_rng(10 + len(new))
+    n, rows = len(new), sum(new)
+    c = Cache(rng, [700] * n, 2, 3, 64, 128, 128)
+    k, v = (dev16(bf16_bits(rng, rows, 2, D)) for _ in range(2))
+    cu, lens = i32(np.concatenate([[0], np.cumsum(new)])), i32([700 + m for m in new])
+    zero = torch.zeros(rows, 4, D, dtype=torch.bfloat16, device="cuda")
+    want = wq.hlwq_kv_paged_attention(zero, k, v, cu, lens, i32(c.table), *c.tensors())
+    for top in (0x0001, 0x0002, 0x0010, 0x007F, 0x0080, 0x0400):
+        bits = rng.integers(0, top + 1, (rows, 4, D)) | (rng.integers(0, 2, (rows, 4, D)) << 15)
+        bits[0] = 0
+        bits[0, 1, 7] = top  # one value alone
+        got = wq.hlwq_kv_paged_attention(dev16(bits.astype(np.uint16)), k, v, cu, lens, i32(c.table), *c.tensors())
+        assert torch.equal(got, want), hex(top)

@@ -236,7 +236,7 @@ __device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Ex
 #pragma unroll
     for (int i = 0; i < 128; ++i) mx = fmaxf(mx, fabsf(x[i]));
     mx = fmaxf(mx, half_swap(mx));
-    const int ex = mx > 0 ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
+    const int ex = row_exponent(mx);
     const float f = __builtin_ldexpf(a.scale < 0 ? -1.0f : 1.0f, -ex);
 #pragma unroll
     for (int s = 0; s < 16; ++s)

@@ -488,6 +488,12 @@ struct SplitWork {
 // tile, for pages that one workgroup took whole and for the other tokens.
 __device__ __forceinline__ int32_t tile_slot(const AttnArgs& a, int32_t tile, int which) { return 2 * (a.workers + tile) + which; }
 
+// The exponent of a rotated query row's largest value: the row over 2^that lies in
+// [1, 2), or below 1 where 1 / 2^that would pass fp32 (rows under 2^-126).
+__device__ __forceinline__ int row_exponent(float top) {
+  return top > 0 ? max(__builtin_amdgcn_frexp_expf(top) - 1, -126) : 0;
+}
+
 // Pages [u0, u1) of a tile.
 template <int BITS, class F>
 __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e, int32_t b, int32_t head, int32_t r0, int32_t u0,
@@ -546,7 +552,7 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
     }
     wave_fwht(x, lane);
     const float mx = wave_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-    const int ex = mx > 0 ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
+    const int ex = row_exponent(mx);
     const float f = __builtin_ldexpf(a.scale < 0 ? -1.0f : 1.0f, -ex);
     *reinterpret_cast<uint2*>(ql + row * kQPitch + 4 * lane) = uint2{pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f)};
     if (lane == 0) qf[row] = fmaxf(__builtin_ldexpf(a.factor, ex - 8), __FLT_DENORM_MIN__);
