@@ -44,3 +44,23 @@ def test_queries_near_the_smallest(wq, new):
         bits[0, 1, 7] = top  # one value alone
         got = wq.hlwq_kv_paged_attention(dev16(bits.astype(np.uint16)), k, v, cu, lens, i32(c.table), *c.tensors())
         assert torch.equal(got, want), hex(top)
+
+
+@pytest.mark.parametrize("new", STEPS)
+def test_queries_of_any_size(wq, new):
+    """q times 2^s under a scale over 2^s: powers of two pass through every product, sum and rounding, so the outputs are
+    the same bits, also where a sum of 256 of the queries' values passes fp32 (s = 118: 256 times 4 times 2^118)."""
+    rng = np.random.default_rng(20 + len(new))
+    n, rows = len(new), sum(new)
+    c = Cache(rng, [700] * n, 2, 3, 64, 128, 128)
+    k, v = (dev16(bf16_bits(rng, rows, 2, D)) for _ in range(2))
+    cu, lens = i32(np.concatenate([[0], np.cumsum(new)])), i32([700 + m for m in new])
+    q = rng.integers(-16, 17, (rows, 4, D)) / 4.0
+    q[0], q[-1, 2] = 4.0, -4.0
+    q = torch.from_numpy(q).cuda()
+    want = wq.hlwq_kv_paged_attention(q.to(torch.bfloat16), k, v, cu, lens, i32(c.table), *c.tensors())
+    assert bool(torch.isfinite(want).all())
+    for s in (-90, -20, 60, 118):
+        got = wq.hlwq_kv_paged_attention((q * 2.0 ** s).to(torch.bfloat16), k, v, cu, lens, i32(c.table), *c.tensors(),
+                                         scale=2.0 ** (-4 - s))
+        assert torch.equal(got, want), s

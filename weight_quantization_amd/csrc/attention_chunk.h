@@ -227,8 +227,8 @@ __device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Ex
       const u32x4 v = *reinterpret_cast<const u32x4*>(qp + 16 * s);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[8 * s + 2 * j] = bf16_lo(v[j]);
-        x[8 * s + 2 * j + 1] = bf16_hi(v[j]);
+        x[8 * s + 2 * j] = bf16_lo(v[j]) * kQueryScale;
+        x[8 * s + 2 * j + 1] = bf16_hi(v[j]) * kQueryScale;
       }
     }
     fwht_halves(x);
@@ -242,7 +242,7 @@ __device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Ex
     for (int s = 0; s < 16; ++s)
 #pragma unroll
       for (int j = 0; j < 4; ++j) q[s][j] = pack_f16x2(x[8 * s + 2 * j] * f, x[8 * s + 2 * j + 1] * f);
-    factor = fmaxf(__builtin_ldexpf(a.factor, ex - 8), __FLT_DENORM_MIN__);
+    factor = fmaxf(__builtin_ldexpf(a.factor, ex), __FLT_DENORM_MIN__);
   }
   clear_apart(r);
   wait_staged();

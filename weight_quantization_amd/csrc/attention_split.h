@@ -488,6 +488,10 @@ struct SplitWork {
 // tile, for pages that one workgroup took whole and for the other tokens.
 __device__ __forceinline__ int32_t tile_slot(const AttnArgs& a, int32_t tile, int which) { return 2 * (a.workers + tile) + which; }
 
+// A query row is rotated as q / 256: exact for every bf16, subnormals too, and a
+// sum of 256 values then never passes fp32.
+constexpr float kQueryScale = 1.0f / 256;
+
 // The exponent of a rotated query row's largest value: the row over 2^that lies in
 // [1, 2), or below 1 where 1 / 2^that would pass fp32 (rows under 2^-126).
 __device__ __forceinline__ int row_exponent(float top) {
@@ -543,7 +547,7 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
   float* qf = lds + M * kQPitch / 2;
 #pragma clang loop unroll(disable)
   for (int row = wave; row < M; row += 4) {
-    float x[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+    float x[4] = {bf16_lo(v.x) * kQueryScale, bf16_hi(v.x) * kQueryScale, bf16_lo(v.y) * kQueryScale, bf16_hi(v.y) * kQueryScale};
     if (r0 + row + 4 < rows && row + 4 < M) v = q_load(row + 4);
     if (r0 + row >= rows) {  // rows that are not there: zeros, and no more to load
       *reinterpret_cast<uint2*>(ql + row * kQPitch + 4 * lane) = uint2{0, 0};
@@ -555,7 +559,7 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
     const int ex = row_exponent(mx);
     const float f = __builtin_ldexpf(a.scale < 0 ? -1.0f : 1.0f, -ex);
     *reinterpret_cast<uint2*>(ql + row * kQPitch + 4 * lane) = uint2{pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f)};
-    if (lane == 0) qf[row] = fmaxf(__builtin_ldexpf(a.factor, ex - 8), __FLT_DENORM_MIN__);
+    if (lane == 0) qf[row] = fmaxf(__builtin_ldexpf(a.factor, ex), __FLT_DENORM_MIN__);
   }
   __syncthreads();
   u32x4 q[8];
