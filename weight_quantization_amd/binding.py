@@ -99,6 +99,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(
             f"{path} is missing: build it with `python -m weight_quantization_amd.build` "
             "(or __graft_entry__.build()); there is no fallback path")
+    # torch brings a HIP runtime of its own: loaded first, the library takes that
+    # one; the other way round the process holds two, and its GPU calls crash.
+    # Host-only helpers do without torch where there is none.
+    try:
+        _torch()
+    except ImportError:
+        pass
     lib = ctypes.CDLL(path)
     for name, (res, args) in _SIGNATURES.items():
         f = getattr(lib, name)
