@@ -76,10 +76,15 @@ struct PagedPlan {
 PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
   PagedPlan p{};
   const int64_t group = q_heads / kv_heads;
-  p.chunk = rows * group > few_rows(requests) * requests;
-  p.split = !p.chunk || requests > 1;
+  const int64_t few = few_rows(requests);
+  p.chunk = rows * group > few * requests;
+  p.split_tiles = tiles_of(requests, rows, group, kv_heads, kSplitRows);
+  // Beside the chunk kernel the split kernel takes requests of whole tokens, at
+  // most `few` rows, whatever the call's rows are.
+  if (p.chunk)
+    p.split_tiles = requests > 1 ? std::min(p.split_tiles, std::min(requests, rows) * ceil_div(few / group * group, kSplitRows) * kv_heads) : 0;
+  p.split = p.split_tiles > 0;
   if (p.split) {
-    p.split_tiles = tiles_of(requests, rows, group, kv_heads, kSplitRows);
     // The workgroups of the tiles' windows come after the pages' and end early.
     // Where they are few all fit the device at once; where they are more, places
     // kept free for them would stand empty most of the time, and it is better
