@@ -149,20 +149,29 @@ int hlwq_kv_paged_append(const hlwq_kv_cache* cache, const void* k_new_bf16, int
  * Norms of encoded tokens must be finite and not negative; k_new, v_new and window may hold NaN
  * and infinities, which reach only rows that attend to them.
  *
- * HLWQ_ERR_LIMIT where max_pages * page_size / 128 times the number of tiles (16
- * query rows of a request and KV head) reaches 2^31 for requests of few
- * rows, or the rows make more than 2^24 tiles.
+ * Requests of few rows (rows times query heads of a KV head: up to 64, of a
+ * single request 256) are worked on in tiles of 16 such rows of one KV head.
+ * What the sizes say of their number T, whatever the lengths on the device: with
+ * g = q_heads / kv_heads at most kv_heads * min(rows * g / 16 + requests, rows * g)
+ * and, where rows * g passes 64 * requests (256 for a single one), at most
+ * kv_heads * ceil(64 / 16) for each request (none for a single one or where g
+ * passes 64).  HLWQ_ERR_LIMIT where T reaches 2^20, or T * max_pages * page_size
+ * / 128 reaches 2^31.
  *
  * `workspace` holds partial sums: hlwq_kv_paged_attention_workspace bytes,
- * 16-byte aligned, contents immaterial before and after. */
+ * 16-byte aligned, contents immaterial before and after.  That is 17 MB and 33 KB
+ * for each of the T tiles (if there are any), and 135 MB more where rows * g
+ * passes 64 * requests (256 for a single one).  Calls in turn on one stream may
+ * share it. */
 int hlwq_kv_paged_attention(const hlwq_kv_cache* cache, const void* q_bf16, int64_t q_stride, int64_t q_heads,
                             const void* k_new_bf16, int64_t k_stride, const void* v_new_bf16, int64_t v_stride,
                             const int32_t* cu_new, const int32_t* lens, const int32_t* block_table,
                             int64_t max_pages, int64_t rows, float scale, void* out_bf16, void* workspace,
                             size_t workspace_bytes, void* hip_stream);
 
-/* Workspace of hlwq_kv_paged_attention for these sizes; 0 if they are invalid
- * or there is nothing to do. */
+/* Workspace of hlwq_kv_paged_attention for these sizes; 0 if they are invalid or
+ * past its limits (2^20 requests, 2^12 query heads, rows * q_heads below 2^31, T
+ * below 2^20), or there is nothing to do. */
 size_t hlwq_kv_paged_attention_workspace(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads);
 
 /* Causal attention over whole prompts packed one after the other: sequence b

@@ -51,3 +51,25 @@ def test_few_rows_and_chunks_in_one_call(wq, requests, q_heads, kv_heads, bits, 
         r = slice(cu[b], cu[b + 1])
         k, v = c.tokens_of(b, t, [x[r] for x in kv])
         pr.check_attention(got[r], f64(q[r]), k, v, pr.encoded(t, 128), t, kv_heads)
+
+
+def test_more_tiles_than_one_dimension_of_a_grid(wq):
+    """70,400 tiles of 256 rows, joined by 16 workgroups each: more than 2^20."""
+    requests, each, q_heads = 640, 110, 256
+    n = requests * each
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn(n, h, D, device="cuda", generator=g, dtype=torch.bfloat16) for h in (q_heads, 1, 1))
+    cache = Cache(np.random.default_rng(1), [0], 1, 3, 64, 128, 128)
+    window = [torch.zeros(requests, 1, 128, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cu = i32(np.arange(requests + 1) * each)
+    table = torch.full((requests, 1), -1, dtype=torch.int32, device="cuda")
+    out = wq.hlwq_kv_paged_attention(q, k, v, cu, i32([each] * requests), table, *cache.d[:4], *window)
+    for b in (0, 300, *range(596, 640)):  # tiles from 65,536 on are those of requests 595 and later
+        r = slice(b * each, (b + 1) * each)
+        score = (q[r].float().flatten(0, 1) @ k[r, 0].float().T).view(each, q_heads, each) / 16
+        score.masked_fill_(torch.ones(each, each, dtype=torch.bool, device="cuda").triu(1)[:, None], -float("inf"))
+        p = score.double().softmax(-1)
+        o = (p.flatten(0, 1) @ v[r, 0].double()).view(each, q_heads, D)
+        # p to bf16 and the output to bf16, 2^-8 each, and the sums in 32 bits (2^-14, as in paged_ref)
+        size = (p.flatten(0, 1) @ v[r, 0].double().abs()).view(each, q_heads, D)
+        assert bool(((out[r].double() - o).abs() <= (2.0 ** -8 + 2.0 ** -14) * size + 2.0 ** -8 * o.abs()).all()), b

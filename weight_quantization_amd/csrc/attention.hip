@@ -100,11 +100,15 @@ PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv
   return p;
 }
 
+// Tiles of the split kernel's launches: sixteen workgroups of 256 to a tile in
+// its join, 2^32 - 1 work-items to a launch.
+constexpr int64_t kMaxSplitTiles = 0xffffff / kSplitRows;
+
 size_t workspace_bytes_of(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
   bool nothing;
   if (requests <= 0 || requests > kMaxRequests || check_heads(rows, q_heads, kv_heads, &nothing) != HLWQ_OK || nothing) return 0;
   const PagedPlan p = paged_plan(requests, rows, q_heads, kv_heads);
-  return p.split_bytes + p.chunk_bytes;
+  return p.split_tiles > kMaxSplitTiles ? 0 : p.split_bytes + p.chunk_bytes;
 }
 
 template <int BITS>
@@ -127,13 +131,8 @@ int32_t cost_shift_of(const AttnArgs& a, int64_t m, int64_t kt) {
   return shift;
 }
 
-int launch_paged(int bits, AttnArgs a, void* ws, hipStream_t stream) {
-  const PagedPlan p = paged_plan(a.requests, a.rows, a.q_heads, a.kv_heads);
-  const int64_t chunk_groups = tiles_of(a.requests, a.rows, a.group, a.kv_heads, kChunkRows) * (kChunkRows / kChunkJoinRows);
-  // the launches' sizes, and the split kernel's count of blocks
-  const int64_t table_blocks = ceil_div(static_cast<int64_t>(a.width) << a.page_shift, kSplitBlock);
-  if (p.split_tiles * kSplitRows > 0xffffff || p.split_tiles * table_blocks > 0x7fffffff || (p.chunk && chunk_groups > 0xffffff))
-    return HLWQ_ERR_LIMIT;
+// (run_paged has refused what passes the launches' sizes)
+int launch_paged(int bits, AttnArgs a, const PagedPlan& p, void* ws, hipStream_t stream) {
   a.most = 0x7fffffff;
   const int32_t few = static_cast<int32_t>(few_rows(a.requests));
   if (p.split) {
@@ -154,7 +153,10 @@ int launch_paged(int bits, AttnArgs a, void* ws, hipStream_t stream) {
   const int st = launch(bits == 3 ? hlwq_chunk_attention_kernel<3> : hlwq_chunk_attention_kernel<2>,
                         dim3(static_cast<uint32_t>(a.workers)), dim3(512), stream, a);
   if (st != HLWQ_OK) return st;
-  return launch(hlwq_chunk_join_kernel, dim3(static_cast<uint32_t>(chunk_groups)), dim3(256), stream, a);
+  // up to 2^29 workgroups: rows * q_heads below 2^31, more than 64 rows a request
+  const int64_t groups = tiles_of(a.requests, a.rows, a.group, a.kv_heads, kChunkRows) * (kChunkRows / kChunkJoinRows);
+  const dim3 grid(static_cast<uint32_t>(std::min(groups, kChunkJoinWide)), static_cast<uint32_t>(ceil_div(groups, kChunkJoinWide)));
+  return launch(hlwq_chunk_join_kernel, grid, dim3(256), stream, a);
 }
 
 int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q_heads, const void* k, int64_t k_stride,
@@ -174,7 +176,11 @@ int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q
       (st = check_rows(k, k_stride, rows, c->kv_heads, &ke)) != HLWQ_OK ||
       (st = check_rows(v, v_stride, rows, c->kv_heads, &ve)) != HLWQ_OK)
     return st;
-  const size_t need = workspace_bytes_of(c->requests, rows, q_heads, c->kv_heads);
+  const PagedPlan plan = paged_plan(c->requests, rows, q_heads, c->kv_heads);
+  // (the split kernel counts its tiles' blocks in 32 bits)
+  if (plan.split_tiles > kMaxSplitTiles || plan.split_tiles * ceil_div(max_pages * c->page_size, kSplitBlock) > 0x7fffffff)
+    return HLWQ_ERR_LIMIT;
+  const size_t need = plan.split_bytes + plan.chunk_bytes;
   if (!cu || !lens || !out || !ws || (max_pages > 0 && !table)) return HLWQ_ERR_NULL;
   if (ws_bytes < need) return HLWQ_ERR_SHAPE;
   if (misaligned(cu, 4) || misaligned(lens, 4) || misaligned(table, 4) || misaligned(out, 16) || misaligned(ws, 16))
@@ -217,7 +223,7 @@ int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q
   a.page_shift = __builtin_ctzll(static_cast<uint64_t>(c->page_size));
   a.scale = scale;
   a.factor = std::fmax(std::fabs(scale) * kLog2e, __FLT_DENORM_MIN__);
-  return launch_paged(c->bits, a, ws, stream);
+  return launch_paged(c->bits, a, plan, ws, stream);
 }
 
 int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,

@@ -437,18 +437,20 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
 
 // Joins the tiles that several workgroups shared, four rows to a wave.
 constexpr int kChunkJoinRows = 16;  // of a workgroup
+constexpr int64_t kChunkJoinWide = 1 << 20;  // workgroups along the grid's first dimension; the rest along its second
 __global__ void __launch_bounds__(256) hlwq_chunk_join_kernel(const AttnArgs a) {
   constexpr int M = kChunkRows, KT = kChunkBlock;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const auto cost = [&](const Extent& e) { return Work<M, KT>(a, e).head_cost() * a.kv_heads; };
   const auto tiles = [&](const Extent& e) { return Work<M, KT>(a, e).tiles * a.kv_heads; };
   Finder<decltype(tiles), decltype(cost)> finder(a, tiles, cost);
-  const int32_t x = blockIdx.x / (M / kChunkJoinRows);
+  const uint32_t at = blockIdx.y * static_cast<uint32_t>(kChunkJoinWide) + blockIdx.x;
+  const int32_t x = at / (M / kChunkJoinRows);
   if (x >= finder.total) return;
   const Found f = finder.find(x);
   const Work<M, KT> w(a, f.e);
   const int32_t head = quotient(f.rest, w.tiles), tile = f.rest - head * w.tiles;
-  const int32_t row0 = (blockIdx.x % (M / kChunkJoinRows)) * kChunkJoinRows + 4 * wave, rows = w.rows(a) - tile * M;
+  const int32_t row0 = (at % (M / kChunkJoinRows)) * kChunkJoinRows + 4 * wave, rows = w.rows(a) - tile * M;
   if (row0 >= rows) return;
   const int32_t x0 = f.before + head * w.head_cost() + w.cost_before(tile), x1 = x0 + w.cost(tile);
   const Share share(Finder<decltype(cost), Nothing>(a, cost, Nothing{}).total, a.workers, kChunkLeast);

@@ -255,7 +255,11 @@ struct Work {
     }
   }
   // of one KV head
-  __device__ __forceinline__ int32_t cost_before(int32_t j) const { return j * base + step * (j * (j - 1) / 2); }
+  // (unsigned: j (j - 1) may pass 2^31, but only where step is 0)
+  __device__ __forceinline__ int32_t cost_before(int32_t j) const {
+    const uint32_t u = static_cast<uint32_t>(j);
+    return static_cast<int32_t>(u * static_cast<uint32_t>(base) + static_cast<uint32_t>(step) * (u * (u - 1) / 2));
+  }
   __device__ __forceinline__ int32_t cost(int32_t j) const { return base + step * j; }
   __device__ __forceinline__ int32_t head_cost() const { return cost_before(tiles); }
   // the tile that holds place x of a KV head's cost: from an estimate of the
