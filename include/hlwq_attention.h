@@ -29,6 +29,11 @@
  * was given: row ranges are cut to [0, rows), a prefix sum that falls makes the
  * attention do nothing, and what the others cause is stated at each call.
  *
+ * Limits, past which a call gives HLWQ_ERR_LIMIT, beside those stated at each: 2^20
+ * requests, sequences and table entries a request, 2^12 heads, a row stride of
+ * 2^22 elements, and below 2^31 rows, rows * q_heads, ring slots a request and
+ * n_pages * page_size.
+ *
  * Layouts (row-major, contiguous unless a stride is given):
  *   packed u8   [n_pages][kv_heads][page_size][32 * bits]
  *   norms  fp16 [n_pages][kv_heads][page_size]
@@ -124,7 +129,7 @@ int hlwq_kv_page_plan(const hlwq_kv_plan* plan, void* hip_stream);
  * tokens that stay among the newest n_residual go to their ring slots.
  * cu_new, lens, row_request and slots as hlwq_kv_page_plan wrote them.  Rows
  * whose request is out of range are passed over; a slot out of range stores
- * nothing. */
+ * nothing.  HLWQ_ERR_LIMIT where rows * kv_heads passes 2^29 - 32. */
 int hlwq_kv_paged_append(const hlwq_kv_cache* cache, const void* k_new_bf16, int64_t k_stride,
                          const void* v_new_bf16, int64_t v_stride, const int32_t* cu_new, const int32_t* lens,
                          const int32_t* row_request, const int32_t* slots, int64_t rows, void* hip_stream);
@@ -180,7 +185,8 @@ size_t hlwq_kv_paged_attention_workspace(int64_t requests, int64_t rows, int64_t
  * [rows][q_heads][256], k, v bf16 [rows][kv_heads][256], strides, heads, scale
  * and arithmetic as above (no token is encoded).  Rows from
  * cu_seqlens[sequences] on are neither read nor written.  NaN and infinities reach
- * only rows that attend to them. */
+ * only rows that attend to them.  HLWQ_ERR_LIMIT where kv_heads * min(rows * g /
+ * 256 + sequences, rows * g), with g = q_heads / kv_heads, reaches 2^23. */
 int hlwq_prompt_attention(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride,
                           const void* v_bf16, int64_t v_stride, const int32_t* cu_seqlens, int64_t sequences,
                           int64_t rows, int64_t q_heads, int64_t kv_heads, int head_dim, float scale,

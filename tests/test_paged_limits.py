@@ -6,7 +6,7 @@ nothing.
 import pytest
 
 import weight_quantization_amd as wq
-from test_paged_host import ELIMIT, ESHAPE, attention, cache, lib  # noqa: F401
+from test_paged_host import EALIGN, ELIMIT, ESHAPE, append, at, attention, cache, lib, prompt  # noqa: F401
 
 SPLIT_TILE = 2 * 16 * (256 + 2) * 4   # bytes of workspace of a tile of 16 rows
 SPLIT = 512 * SPLIT_TILE
@@ -56,3 +56,18 @@ def test_tables_too_wide_for_the_tiles_are_refused(lib):
     assert sized(lib, 1, 10 ** 6, 4, 4, width=2 ** 20, page=256) == ESHAPE  # none of the split kernel's
     assert sized(lib, 63, 10 ** 6, 4, 4, width=2 ** 20, page=256) == ESHAPE   # 63 * 4 * 4 = 1008 tiles
     assert sized(lib, 64, 10 ** 6, 4, 4, width=2 ** 20, page=256) == ELIMIT   # 1024
+
+
+@pytest.mark.parametrize("kv_heads,rows,status", [(1, 2 ** 29 - 32, EALIGN), (1, 2 ** 29 - 31, ELIMIT), (8, 2 ** 26 - 4, EALIGN),
+                                                  (8, 2 ** 26 - 3, ELIMIT), (4096, 2 ** 31 - 1, ELIMIT)])
+def test_an_append_past_one_launch_is_refused(lib, kv_heads, rows, status):
+    # (keys 8 bytes off their place end the calls whose sizes are taken)
+    stride = 256 * kv_heads
+    assert append(lib, cache(kv_heads=kv_heads), k=at(6) + 8, ks=stride, vs=stride, rows=rows) == status
+
+
+@pytest.mark.parametrize("rows,n,kv_heads,status", [(2 ** 20, 2 ** 20, 8, ELIMIT), (2 ** 20, 2 ** 20, 7, EALIGN),
+                                                    (2 ** 22, 2, 24, EALIGN), (2 ** 18, 2 ** 18, 33, ELIMIT)])
+def test_a_prompt_call_past_one_launch_is_refused(lib, rows, n, kv_heads, status):
+    w = 256 * kv_heads
+    assert prompt(lib, qs=w, ks=w, vs=w, n=n, rows=rows, hq=kv_heads, hk=kv_heads, q=at(0) + 8 * (status == EALIGN)) == status

@@ -474,7 +474,9 @@ int run_append(const hlwq_kv_cache* c, const void* k, int64_t k_stride, const vo
   if (rows < 0) return HLWQ_ERR_SHAPE;
   if (rows == 0 || c->requests == 0 || c->kv_heads == 0) return HLWQ_OK;
   int64_t units;
-  if (rows > 0x7fffffff || !mul_ok(rows, c->kv_heads, &units) || units > 0x7fffffff)
+  // (a launch has at most 2^32 - 1 work-items)
+  if (rows > 0x7fffffff || !mul_ok(rows, c->kv_heads, &units) ||
+      ceil_div(units, kAppendThreads / kAppendLanes) > 0xffffffff / kAppendThreads)
     return HLWQ_ERR_LIMIT;
   int64_t ke, ve;
   if ((st = check_rows(k, k_stride, rows, c->kv_heads, &ke)) != HLWQ_OK ||
