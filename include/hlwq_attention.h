@@ -108,8 +108,9 @@ typedef struct hlwq_kv_plan {
  * (request, page).  tokens, n_new and n_free are left as they are (lens and
  * n_free_after are the next step's), so the same step can be planned again
  * unless a reset slot takes pages in it.  A page may stand in several tables (a
- * common beginning read by several requests); the plan keeps no count of that, so
- * only one of them may be reset.
+ * common beginning read by several requests) once all its tokens are encoded: a
+ * request's next tokens go on in its last page.  The plan keeps no count of that,
+ * so only one of them may be reset.
  *
  * *status afterwards: 0; or the number of pages missing from the stack; or -1
  * where a device value is out of range (a negative length, more new tokens than
@@ -164,8 +165,8 @@ int hlwq_kv_paged_append(const hlwq_kv_cache* cache, const void* k_new_bf16, int
  * / 128 reaches 2^31.
  *
  * `workspace` holds partial sums: hlwq_kv_paged_attention_workspace bytes,
- * 16-byte aligned, contents immaterial before and after.  That is 17 MB and 33 KB
- * for each of the T tiles (if there are any), and 135 MB more where rows * g
+ * 16-byte aligned, contents immaterial before and after.  That is about 17 MB and
+ * 33 KB for each of the T tiles (if there are any), and 135 MB more where rows * g
  * passes 64 * requests (256 for a single one).  Calls in turn on one stream may
  * share it. */
 int hlwq_kv_paged_attention(const hlwq_kv_cache* cache, const void* q_bf16, int64_t q_stride, int64_t q_heads,

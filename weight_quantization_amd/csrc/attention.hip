@@ -63,6 +63,10 @@ int launch_prompt(const AttnArgs& a, hipStream_t stream) {
 //   8 requests over 4000 tokens, 36 rows each  44   59;   60 rows   50   61;
 //                                  120 rows    79   67;  240 rows  128   91
 //   32 requests over 1000 tokens, 60 rows      67   70;  240 rows  224  106
+// The mean misses one chunk among many slots, which then is the split kernel's
+// alone: 512 tokens over 16000 beside 63 single tokens over 4000 take 673 us (312
+// and 80 by themselves; 1024 tokens, where both kernels are called, 587), 300
+// over 4000 in one of 32 slots 121 (105 alone).
 constexpr int64_t few_rows(int64_t requests) { return requests == 1 ? 256 : 64; }
 // Workgroups that the device holds at once: two to a CU of the split kernel
 // (256 registers a work-item), one of the chunk kernel.

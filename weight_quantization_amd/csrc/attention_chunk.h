@@ -296,7 +296,8 @@ __device__ __forceinline__ void chunk_pages(Rows& r, const AttnArgs& a, const Ex
     for (int i = 0; i < 16; ++i) r.o[t][i] = x[16 * t + i] * f;
 }
 
-// The window's and the step's own tokens, blocks [from, to) of 64 of them.
+// The window's and the step's own tokens, blocks [from, to) of 64 of them.  (Blocks
+// that are staged or masked reload a register from scratch memory each.)
 template <int BITS>
 __device__ __forceinline__ void chunk_tokens(Rows& r, const AttnArgs& a, const Extent& e, int32_t b, int32_t head, int32_t w0,
                                              int64_t end_key, int32_t from, int32_t to, uint32_t base, int wave) {

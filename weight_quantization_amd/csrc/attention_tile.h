@@ -18,9 +18,10 @@
 // product).  517 tokens take 26 us, nine packed prompts of 1 to 2500 tokens
 // (16 heads on 2) 196 us.
 //
-// The loop over blocks may hold no load from scratch memory: one waits for all
-// loads under way, those of the next block among them (a single spilled
-// register took 6%).
+// A load from scratch memory in the loop over blocks waits for all loads under
+// way, those of the next block among them (a single spilled register took 6%).
+// The two kernels with blocks of 64 keys have none there; the one of four waves
+// and 32 keys still reloads one register a block.
 #pragma once
 
 #include "attention_common.h"

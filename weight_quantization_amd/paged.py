@@ -216,7 +216,8 @@ def hlwq_kv_paged_attention(q, k_new, v_new, cu_new, lens, block_table, k_packed
     [rows, q_heads, 256], k_new and v_new bf16 [rows, kv_heads, 256], cu_new and lens from the plan, block_table int32
     [requests, max_pages], the cache as in hlwq_kv_paged_append; scale 1 / 16 by default.  Returns bf16
     [rows, q_heads, 256]; rows past cu_new[requests] are left as they were (undefined in a new `out`).  workspace:
-    uint8, hlwq_kv_paged_attention_workspace bytes; allocated for the call by default."""
+    uint8, hlwq_kv_paged_attention_workspace bytes (20 MB for a few single tokens, 135 MB more once there are chunks);
+    allocated for the call by default."""
     torch = _torch()
     i32, bf16 = torch.int32, torch.bfloat16
     n, = _shape(lens, 1, "lens")
