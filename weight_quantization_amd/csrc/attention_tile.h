@@ -40,10 +40,12 @@ __device__ __forceinline__ u32x4 buffer_of(const void* p, int64_t bytes) {
 // 16 bytes a lane from memory straight to LDS: lane l's land at lds + 16 l.
 // The compiler does not see these loads; a wait on the vector-memory counter
 // stands before the barrier that publishes them (wait_staged).  M0, which
-// holds the LDS address, is used by nothing else in these kernels.
+// holds the LDS address, is used by nothing else in these kernels.  (Nor does it
+// see what the load reads: five wait states after a VALU write of the buffer's
+// scalar registers, one after M0's, are the block's own.)
 __device__ __forceinline__ void stage16(u32x4 buffer, uint32_t offset, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer)
                : "memory");
 }
 __device__ __forceinline__ void stage16(const void* p, uint32_t lds) {
