@@ -148,7 +148,8 @@ int hlwq_kv_paged_append(const hlwq_kv_cache* cache, const void* k_new_bf16, int
  * rotated back: q is rotated once, the sum over encoded tokens runs over
  * centroids in fp16 (2^-11 relative) and its fp32 result is rotated once.
  * Scores, softmax and sums are fp32; probabilities enter the products rounded
- * to 16 bits; the output is rounded once.
+ * to 16 bits; the output is rounded once.  A row whose q . k, before the scale,
+ * or score passes fp32's range is NaN.
  *
  * A token whose page id lies outside [0, n_pages), or past max_pages, is left
  * out of the sum.  lens[b] below the number of new tokens counts as equal to it.
