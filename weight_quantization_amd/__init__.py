@@ -41,3 +41,15 @@ from .paged import (  # noqa: F401
     hlwq_kv_paged_attention_workspace,
     hlwq_prompt_attention,
 )
+from .drafts import (  # noqa: F401
+    VerifiedDrafts,
+    hlwq_kv_tree_attention,
+    hlwq_kv_tree_attention_workspace,
+    hlwq_verify_drafts,
+)
+from .moe import (  # noqa: F401
+    MoeOutput,
+    hlwq_moe_experts,
+    hlwq_moe_layer,
+    hlwq_moe_workspace,
+)

@@ -31,7 +31,7 @@ ARCH = "gfx950"
 
 # the paged KV cache and attention (include/hlwq_attention.h), linked into
 # libhlwq.so with hlwq.hip
-SERVING_SOURCES = ("kv_paged.hip", "attention.hip")
+SERVING_SOURCES = ("kv_paged.hip", "attention.hip", "moe.hip", "verify.hip")
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -77,6 +77,19 @@ struct PagedPlan {
   int64_t split_slots;    // of partial sums
   size_t split_bytes, chunk_bytes;  // of workspace, each its own
 };
+// Sizes of the split kernel's part for its tiles.
+void size_split(PagedPlan& p) {
+  // The workgroups of the tiles' windows come after the pages' and end early.
+  // Where they are few all fit the device at once; where they are more, places
+  // kept free for them would stand empty most of the time, and it is better
+  // that they follow the first pages' workgroups.  Measured (4 KV heads, 3
+  // bits, 4000 tokens a request, us), with places kept and without: 4 requests
+  // 19.8 and 22.5, 8 26.4 and 25.3, 16 35.8 and 33.6, 64 87 and 74, 128 183
+  // and 154.
+  p.split_workers = kSplitResident - (p.split_tiles < kSplitResident / 16 ? p.split_tiles : 0);
+  p.split_slots = 2 * (p.split_workers + p.split_tiles);
+  p.split_bytes = partial_floats(p.split_slots, kSplitRows) * sizeof(float);
+}
 PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
   PagedPlan p{};
   const int64_t group = q_heads / kv_heads;
@@ -88,19 +101,19 @@ PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv
   if (p.chunk)
     p.split_tiles = requests > 1 ? std::min(p.split_tiles, std::min(requests, rows) * ceil_div(few / group * group, kSplitRows) * kv_heads) : 0;
   p.split = p.split_tiles > 0;
-  if (p.split) {
-    // The workgroups of the tiles' windows come after the pages' and end early.
-    // Where they are few all fit the device at once; where they are more, places
-    // kept free for them would stand empty most of the time, and it is better
-    // that they follow the first pages' workgroups.  Measured (4 KV heads, 3
-    // bits, 4000 tokens a request, us), with places kept and without: 4 requests
-    // 19.8 and 22.5, 8 26.4 and 25.3, 16 35.8 and 33.6, 64 87 and 74, 128 183
-    // and 154.
-    p.split_workers = kSplitResident - (p.split_tiles < kSplitResident / 16 ? p.split_tiles : 0);
-    p.split_slots = 2 * (p.split_workers + p.split_tiles);
-    p.split_bytes = partial_floats(p.split_slots, kSplitRows) * sizeof(float);
-  }
+  if (p.split) size_split(p);
   p.chunk_bytes = p.chunk ? partial_floats(2 * kChunkWorkers, kChunkRows) * sizeof(float) : 0;
+  return p;
+}
+
+// A call whose rows are trees: all the split kernel's.  (The chunk kernel would
+// unpack each code once for 256 rows instead of sixteen, but trees of so many
+// rows are not drafted.)
+PagedPlan tree_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
+  PagedPlan p{};
+  p.split = true;
+  p.split_tiles = tiles_of(requests, rows, q_heads / kv_heads, kv_heads, kSplitRows);
+  size_split(p);
   return p;
 }
 
@@ -108,16 +121,16 @@ PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv
 // its join, 2^32 - 1 work-items to a launch.
 constexpr int64_t kMaxSplitTiles = 0xffffff / kSplitRows;
 
-size_t workspace_bytes_of(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
+size_t workspace_bytes_of(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads, bool tree) {
   bool nothing;
   if (requests <= 0 || requests > kMaxRequests || check_heads(rows, q_heads, kv_heads, &nothing) != HLWQ_OK || nothing) return 0;
-  const PagedPlan p = paged_plan(requests, rows, q_heads, kv_heads);
+  const PagedPlan p = (tree ? tree_plan : paged_plan)(requests, rows, q_heads, kv_heads);
   return p.split_tiles > kMaxSplitTiles ? 0 : p.split_bytes + p.chunk_bytes;
 }
 
-template <int BITS>
+template <int BITS, bool TREE>
 int launch_split(const AttnArgs& a, int64_t tiles, hipStream_t stream) {
-  const int st = launch(hlwq_split_attention_kernel<BITS>, dim3(static_cast<uint32_t>(a.workers + tiles)), dim3(kSplitThreads), stream, a);
+  const int st = launch(hlwq_split_attention_kernel<BITS, TREE>, dim3(static_cast<uint32_t>(a.workers + tiles)), dim3(kSplitThreads), stream, a);
   if (st != HLWQ_OK) return st;
   return launch(hlwq_split_join_kernel, dim3(static_cast<uint32_t>(tiles * kSplitRows)), dim3(kSplitThreads), stream, a);
 }
@@ -145,7 +158,11 @@ int launch_paged(int bits, AttnArgs a, const PagedPlan& p, void* ws, hipStream_t
     a.slots = static_cast<int32_t>(p.split_slots);
     a.least = 1;
     if (p.chunk) a.most = few;
-    const int st = bits == 3 ? launch_split<3>(a, p.split_tiles, stream) : launch_split<2>(a, p.split_tiles, stream);
+    if (a.parents) {
+      a.most = static_cast<int32_t>(std::min<int64_t>(int64_t{HLWQ_TREE_NODES} * a.group, 0x7fffffff));
+      return bits == 3 ? launch_split<3, true>(a, p.split_tiles, stream) : launch_split<2, true>(a, p.split_tiles, stream);
+    }
+    const int st = bits == 3 ? launch_split<3, false>(a, p.split_tiles, stream) : launch_split<2, false>(a, p.split_tiles, stream);
     if (st != HLWQ_OK || !p.chunk) return st;
     a.most = 0x7fffffff;
   }
@@ -164,8 +181,9 @@ int launch_paged(int bits, AttnArgs a, const PagedPlan& p, void* ws, hipStream_t
 }
 
 int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q_heads, const void* k, int64_t k_stride,
-              const void* v, int64_t v_stride, const int32_t* cu, const int32_t* lens, const int32_t* table,
-              int64_t max_pages, int64_t rows, float scale, void* out, void* ws, size_t ws_bytes, hipStream_t stream) {
+              const void* v, int64_t v_stride, bool tree, const int32_t* parents, const int32_t* cu, const int32_t* lens,
+              const int32_t* table, int64_t max_pages, int64_t rows, float scale, void* out, void* ws, size_t ws_bytes,
+              hipStream_t stream) {
   if (!c) return HLWQ_ERR_NULL;
   Spans spans;
   int st = check_cache(*c, false, spans);
@@ -180,14 +198,14 @@ int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q
       (st = check_rows(k, k_stride, rows, c->kv_heads, &ke)) != HLWQ_OK ||
       (st = check_rows(v, v_stride, rows, c->kv_heads, &ve)) != HLWQ_OK)
     return st;
-  const PagedPlan plan = paged_plan(c->requests, rows, q_heads, c->kv_heads);
+  const PagedPlan plan = (tree ? tree_plan : paged_plan)(c->requests, rows, q_heads, c->kv_heads);
   // (the split kernel counts its tiles' blocks in 32 bits)
   if (plan.split_tiles > kMaxSplitTiles || plan.split_tiles * ceil_div(max_pages * c->page_size, kSplitBlock) > 0x7fffffff)
     return HLWQ_ERR_LIMIT;
   const size_t need = plan.split_bytes + plan.chunk_bytes;
-  if (!cu || !lens || !out || !ws || (max_pages > 0 && !table)) return HLWQ_ERR_NULL;
+  if (!cu || !lens || !out || !ws || (max_pages > 0 && !table) || (tree && !parents)) return HLWQ_ERR_NULL;
   if (ws_bytes < need) return HLWQ_ERR_SHAPE;
-  if (misaligned(cu, 4) || misaligned(lens, 4) || misaligned(table, 4) || misaligned(out, 16) || misaligned(ws, 16))
+  if (misaligned(parents, 4) || misaligned(cu, 4) || misaligned(lens, 4) || misaligned(table, 4) || misaligned(out, 16) || misaligned(ws, 16))
     return HLWQ_ERR_ALIGN;
   add_span(spans, q, qe, 2, false);
   add_span(spans, k, ke, 2, false);
@@ -195,6 +213,7 @@ int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q
   add_span(spans, cu, c->requests + 1, 4, false);
   add_span(spans, lens, c->requests, 4, false);
   add_span(spans, table, c->requests * max_pages, 4, false);
+  add_span(spans, parents, rows, 4, false);
   add_span(spans, out, rows * q_heads, 2 * kDim, true);
   add_span(spans, ws, static_cast<int64_t>(need), 1, true);
   if (check_disjoint(spans) != HLWQ_OK) return HLWQ_ERR_OVERLAP;
@@ -214,6 +233,7 @@ int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q
   a.cu = cu;
   a.lens = lens;
   a.table = table;
+  a.parents = parents;
   a.out = static_cast<uint16_t*>(out);
   a.n_res = c->n_residual;
   a.ring = c->ring;
@@ -283,13 +303,27 @@ int hlwq_kv_paged_attention(const hlwq_kv_cache* cache, const void* q_bf16, int6
                             const int32_t* cu_new, const int32_t* lens, const int32_t* block_table,
                             int64_t max_pages, int64_t rows, float scale, void* out_bf16, void* workspace,
                             size_t workspace_bytes, void* hip_stream) {
-  return hlwq_kv::run_paged(cache, q_bf16, q_stride, q_heads, k_new_bf16, k_stride, v_new_bf16, v_stride, cu_new, lens,
-                            block_table, max_pages, rows, scale, out_bf16, workspace, workspace_bytes,
+  return hlwq_kv::run_paged(cache, q_bf16, q_stride, q_heads, k_new_bf16, k_stride, v_new_bf16, v_stride, false, nullptr, cu_new,
+                            lens, block_table, max_pages, rows, scale, out_bf16, workspace, workspace_bytes,
                             static_cast<hipStream_t>(hip_stream));
 }
 
 size_t hlwq_kv_paged_attention_workspace(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
-  return hlwq_kv::workspace_bytes_of(requests, rows, q_heads, kv_heads);
+  return hlwq_kv::workspace_bytes_of(requests, rows, q_heads, kv_heads, false);
+}
+
+int hlwq_kv_tree_attention(const hlwq_kv_cache* cache, const void* q_bf16, int64_t q_stride, int64_t q_heads,
+                           const void* k_new_bf16, int64_t k_stride, const void* v_new_bf16, int64_t v_stride,
+                           const int32_t* parents, const int32_t* cu_rows, const int32_t* lens,
+                           const int32_t* block_table, int64_t max_pages, int64_t rows, float scale, void* out_bf16,
+                           void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return hlwq_kv::run_paged(cache, q_bf16, q_stride, q_heads, k_new_bf16, k_stride, v_new_bf16, v_stride, true, parents, cu_rows,
+                            lens, block_table, max_pages, rows, scale, out_bf16, workspace, workspace_bytes,
+                            static_cast<hipStream_t>(hip_stream));
+}
+
+size_t hlwq_kv_tree_attention_workspace(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
+  return hlwq_kv::workspace_bytes_of(requests, rows, q_heads, kv_heads, true);
 }
 
 int hlwq_prompt_attention(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride,

@@ -41,6 +41,7 @@ struct AttnArgs {
   const int32_t* cu;
   const int32_t* lens;  // null: nothing is cached
   const int32_t* table;
+  const int32_t* parents;  // of the rows, where they are trees
   uint16_t* out;
   float* partial;  // workspace: partial sums, then their statistics
   int64_t n_res, ring;

@@ -36,6 +36,8 @@
 
 #include "attention_common.h"
 
+#include "hlwq_drafts.h"
+
 namespace hlwq_kv {
 
 typedef uint32_t u32x2_4 __attribute__((ext_vector_type(2), aligned(4)));
@@ -339,11 +341,12 @@ struct Tokens {
   }
 };
 
-// 32 bf16 tokens from k0 on; lim: last token that the lane's row sees; last:
+// 32 bf16 tokens from k0 on; sees(k): whether the lane's row sees token k; last:
 // the last one there is.  masked: some row does not see some token; mixed: nor
 // do all that are there see the same.
-__device__ __forceinline__ void token_step(SplitRows& r, const u32x4 (&q)[8], float factor, int64_t k0, int64_t last,
-                                           int64_t lim, bool masked, bool mixed, const Tokens& tokens, int lane) {
+template <class F>
+__device__ __forceinline__ void token_step(SplitRows& r, const u32x4 (&q)[8], float factor, int64_t k0, int64_t last, F sees,
+                                           bool masked, bool mixed, const Tokens& tokens, int lane) {
   const int c = lane & 15, h4 = lane >> 4;
   const auto token = [&](int i) { return k0 + 16 * (i >> 2) + 4 * h4 + (i & 3); };
   // every load before the first use
@@ -375,7 +378,7 @@ __device__ __forceinline__ void token_step(SplitRows& r, const u32x4 (&q)[8], fl
   float t[8], p[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) t[i] = s[i >> 2][i & 3];
-  weigh(r, t, factor, masked, [&](int i) { return token(i) > lim; }, p);
+  weigh(r, t, factor, masked, [&](int i) { return !sees(token(i)); }, p);
 #pragma unroll
   for (int i = 0; i < 4; ++i) pf[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
   // as in key_step: where some rows see a token and others do not, 0 times its
@@ -410,7 +413,7 @@ __device__ __forceinline__ void token_step(SplitRows& r, const u32x4 (&q)[8], fl
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const float v = bf16_lo(p[16 * i + x]);
-          r.o[x][i] += k0 + k <= lim && !__builtin_isfinite(v) ? v : 0.0f;
+          r.o[x][i] += sees(k0 + k) && !__builtin_isfinite(v) ? v : 0.0f;
         }
     }
   }
@@ -587,8 +590,46 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
   join_waves(r, true, rows - r0, lds, lane, wave, write);
 }
 
+// Which of the step's own tokens the sixteen rows of a tile see, where these are
+// trees: a bit for each token that is the row's own or an ancestor of it.  Parents
+// come before their children, so the ways up end; sixteen lanes go them in LDS,
+// where the sums of join_waves lie later.
+struct Kin {
+  static constexpr int kWords = HLWQ_TREE_NODES / 32 + 1;  // of a row; the last stays 0
+  const uint32_t* bits;
+  int64_t near;
+  // bit j: whether the lane's row sees token k0 + j
+  __device__ __forceinline__ uint32_t word(int64_t k0) const {
+    const int64_t at = k0 - near;
+    if (at <= -32) return ~0u;
+    if (at < 0) return (1u << -at) - 1 | bits[0] << -at;
+    const int w = static_cast<int>(at >> 5);
+    return __builtin_amdgcn_alignbit(bits[w + 1], bits[w], static_cast<uint32_t>(at & 31));
+  }
+};
+static_assert((HLWQ_TREE_NODES + 16 * Kin::kWords) * 4 <= 4 * 16 * kSplitPitch * 4, "a tile's tree lies where its sums do");
+
+// (`count` tokens: up to the tile's last)
+__device__ __forceinline__ Kin find_kin(const AttnArgs& a, const Extent& e, int64_t near, int32_t r0, int32_t rows, int32_t count,
+                                        float* lds, int lane) {
+  int32_t* parent = reinterpret_cast<int32_t*>(lds);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(lds) + HLWQ_TREE_NODES;
+  for (int32_t i = threadIdx.x; i < count; i += kSplitThreads) {
+    const int32_t p = a.parents[e.begin + static_cast<int64_t>(i)];
+    parent[i] = p < i ? p : -1;
+  }
+  const int32_t words = (count + 31) / 32 + 1;
+  for (int32_t i = threadIdx.x; i < 16 * words; i += kSplitThreads) bits[i / words * Kin::kWords + i % words] = 0;
+  __syncthreads();
+  if (threadIdx.x < 16)
+    for (int32_t t = token_of(min(r0 + static_cast<int32_t>(threadIdx.x), rows - 1), a.group); t >= 0; t = parent[t])
+      bits[threadIdx.x * Kin::kWords + (t >> 5)] |= 1u << (t & 31);
+  __syncthreads();
+  return Kin{bits + (lane & 15) * Kin::kWords, near};
+}
+
 // The window's and the step's own tokens of a tile.
-template <class F>
+template <bool TREE, class F>
 __device__ __forceinline__ void attend_tokens(const AttnArgs& a, const Extent& e, int32_t b, int32_t head, int32_t r0, float* lds,
                                               int lane, int wave, F write) {
   constexpr int M = kSplitRows;
@@ -607,13 +648,26 @@ __device__ __forceinline__ void attend_tokens(const AttnArgs& a, const Extent& e
     if (a.scale < 0) q[x] ^= 0x80008000u;
   }
   SplitRows r;
-  clear(r);
-  for (int64_t k0 = 32 * wave; k0 <= last; k0 += kSplitBlock)
-    token_step(r, q, a.factor, k0, last, lim, k0 + 31 > first, k0 + 31 > first && first < last, tokens, lane);
+  if constexpr (TREE) {
+    const Kin kin = find_kin(a, e, tokens.near, r0, rows, static_cast<int32_t>(last - tokens.near) + 1, lds, lane);
+    clear(r);
+    for (int64_t k0 = 32 * wave; k0 <= last; k0 += kSplitBlock) {
+      const uint32_t seen = kin.word(k0);
+      if (!__any(seen != 0)) continue;
+      const bool masked = k0 + 31 >= tokens.near;
+      token_step(r, q, a.factor, k0, last, [&](int64_t k) { return seen >> (k - k0) & 1; }, masked, masked, tokens, lane);
+    }
+  } else {
+    clear(r);
+    for (int64_t k0 = 32 * wave; k0 <= last; k0 += kSplitBlock)
+      token_step(r, q, a.factor, k0, last, [&](int64_t k) { return k <= lim; }, k0 + 31 > first, k0 + 31 > first && first < last,
+                 tokens, lane);
+  }
   join_waves(r, false, rows - r0, lds, lane, wave, write);
 }
 
-template <int BITS>
+// TREE: the step's rows are trees (AttnArgs::parents), not sequences.
+template <int BITS, bool TREE>
 __global__ void __launch_bounds__(kSplitThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 hlwq_split_attention_kernel(const AttnArgs a) {
   constexpr int M = kSplitRows;
@@ -640,7 +694,7 @@ hlwq_split_attention_kernel(const AttnArgs a) {
     const SplitWork w(a, f.e);
     const int32_t head = quotient(f.rest, w.tiles), r0 = (f.rest - head * w.tiles) * M;
     const int32_t slot = tile_slot(a, x, 1);
-    attend_tokens(a, w.e, f.b, head, r0, lds, lane, wave, [&](int row, f32x4 o, float m, float l) {
+    attend_tokens<TREE>(a, w.e, f.b, head, r0, lds, lane, wave, [&](int row, f32x4 o, float m, float l) {
       if (w.blocks == 0)
         write_row(a, w.e.begin, head, r0 + row, o, l, lane);
       else

@@ -65,6 +65,12 @@ __device__ __forceinline__ uint32_t lane_xor(uint32_t v, int d) {
 }
 __device__ __forceinline__ float lane_xor(float v, int d) { return __uint_as_float(lane_xor(__float_as_uint(v), d)); }
 
+__device__ __forceinline__ double lane_xor(double v, int d) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = lane_xor(static_cast<uint32_t>(u), d), hi = lane_xor(static_cast<uint32_t>(u >> 32), d);
+  return __builtin_bit_cast(double, lo | static_cast<uint64_t>(hi) << 32);
+}
+
 // Inclusive prefix sum over the wave: within rows of sixteen, then the rows'
 // last values on.
 template <int CTRL, int ROWS>
@@ -96,6 +102,12 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 __device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += lane_xor(v, d);
+  return v;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) v += lane_xor(v, d);
   return v;
@@ -145,7 +157,7 @@ struct Span {
   uintptr_t lo, hi;
   bool written;
 };
-// Of one call: at most fourteen (an entry point allocates nothing, so that
+// Of one call: at most fifteen (an entry point allocates nothing, so that
 // nothing is thrown through it).
 struct Spans {
   Span at[16];

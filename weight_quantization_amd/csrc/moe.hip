@@ -1,0 +1,668 @@
+// moe.hip — a mixture-of-experts layer of a few tokens, from the codes of its
+// banks (include/hlwq_moe.h).
+
+#include "kv_common.h"
+
+#include "hlwq_moe.h"
+
+namespace hlwq_kv {
+namespace {
+
+typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x3_4 __attribute__((ext_vector_type(3), aligned(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kBlock = 128;
+constexpr int64_t kMaxExperts = 1024, kMaxTopK = 32, kMaxSize = 1 << 20, kMaxTokens = 1 << 24;
+constexpr int kMaxPairs = 4096;  // (token, expert) pairs of one pass over the banks
+constexpr int kTile = 16;        // rows of a matrix, and pairs, to a product
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const f16x2 v = {static_cast<_Float16>(lo), static_cast<_Float16>(hi)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// ---------------------------------------------------------------------------
+// Activations: rotated by blocks of 128 and rounded to fp16, a row over a power
+// of two that brings its largest value to [1, 2) before the rotation; a rotated
+// value is at most 128 times that, so it is held times 2^7 and stays below 2^15.
+// ---------------------------------------------------------------------------
+
+constexpr int kRotateThreads = 256;
+
+// Largest magnitude of a row, NaN and infinities left out, in every thread.
+template <class F>
+__device__ __forceinline__ float row_top(F at, int32_t n, float* lds) {
+  float top = 0;
+  for (int32_t i = threadIdx.x; i < n; i += kRotateThreads) {
+    const float v = fabsf(at(i));
+    top = v <= FLT_MAX ? fmaxf(top, v) : top;
+  }
+  top = wave_max(top);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = top;
+  __syncthreads();
+  return fmaxf(fmaxf(lds[0], lds[1]), fmaxf(lds[2], lds[3]));
+}
+
+// A block of 128 held two values to a lane (2 l and 2 l + 1), unnormalised.
+__device__ __forceinline__ void block_fwht(float (&x)[2], int lane) {
+  const float a = x[0] + x[1], b = x[0] - x[1];
+  x[0] = a;
+  x[1] = b;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const bool upper = (lane & d) != 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float q = lane_xor(x[j], d);
+      x[j] = upper ? q - x[j] : x[j] + q;
+    }
+  }
+}
+
+// (at least -110: the factors 2^(7 - e) and 2^(e - 14) are normal numbers, and exact)
+__device__ __forceinline__ int scale_exponent(float top) { return top > 0 ? max(__builtin_amdgcn_frexp_expf(top) - 1, -110) : 0; }
+
+template <class F>
+__device__ __forceinline__ void rotate_row(F at, int32_t n, uint16_t* __restrict__ to, float* __restrict__ scale) {
+  __shared__ float lds[kRotateThreads / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = scale_exponent(row_top(at, n, lds));
+  const float f = __builtin_ldexpf(1.0f, 7 - e);
+  if (threadIdx.x == 0) *scale = __builtin_ldexpf(1.0f, e - 7 - 7);  // and the blocks' 1 / 128
+  const int32_t nb = static_cast<int32_t>(ceil_div(n, kBlock));
+  for (int32_t b = wave; b < nb; b += kRotateThreads / 64) {
+    const int32_t i = b * kBlock + 2 * lane;
+    float x[2] = {i < n ? at(i) * f : 0.0f, i + 1 < n ? at(i + 1) * f : 0.0f};
+    block_fwht(x, lane);
+    *reinterpret_cast<uint32_t*>(to + i) = pack_f16x2(x[0], x[1]);
+  }
+}
+
+struct PrepareArgs {
+  const uint16_t* x;
+  int64_t x_stride;
+  const uint16_t* router;  // null: the routing is known
+  double* logits;          // [tokens][experts]
+  uint16_t* rotated;       // [tokens][nb * 128]
+  float* scale;            // [tokens]
+  int32_t tokens, hidden, experts, expert_groups;
+};
+
+// Router logits of four experts and up to four tokens a wave, lanes along the
+// row.  Products of bf16 are exact in 64 bits, where they are summed: experts
+// whose logits differ by less than fp32 resolves are told apart.
+constexpr int kRouterExperts = 4, kRouterTokens = 4, kRouterWaves = kRotateThreads / 64;
+
+template <int TOKENS>
+__device__ __forceinline__ void router_logits(const PrepareArgs& a, int32_t e0, int32_t t0) {
+  const int lane = threadIdx.x & 63;
+  double sum[kRouterExperts][TOKENS] = {};
+  for (int32_t i = lane; i < a.hidden; i += 64) {
+    double r[kRouterExperts], x[TOKENS];
+#pragma unroll
+    for (int k = 0; k < kRouterExperts; ++k)
+      r[k] = bf16_lo(a.router[static_cast<int64_t>(min(e0 + k, a.experts - 1)) * a.hidden + i]);
+#pragma unroll
+    for (int k = 0; k < TOKENS; ++k) x[k] = bf16_lo(a.x[min(t0 + k, a.tokens - 1) * a.x_stride + i]);
+#pragma unroll
+    for (int k = 0; k < kRouterExperts; ++k)
+#pragma unroll
+      for (int j = 0; j < TOKENS; ++j) sum[k][j] = __builtin_fma(r[k], x[j], sum[k][j]);
+  }
+#pragma unroll
+  for (int k = 0; k < kRouterExperts; ++k)
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j) {
+      const double s = wave_sum(sum[k][j]);
+      if (lane == 0 && e0 + k < a.experts && t0 + j < a.tokens) a.logits[static_cast<int64_t>(t0 + j) * a.experts + e0 + k] = s;
+    }
+}
+
+// The first workgroups rotate a token each, the others take the router's.
+__global__ void __launch_bounds__(kRotateThreads) hlwq_moe_prepare_kernel(const PrepareArgs a) {
+  if (static_cast<int32_t>(blockIdx.x) < a.tokens) {
+    const int32_t t = blockIdx.x;
+    const uint16_t* row = a.x + t * a.x_stride;
+    const int64_t pitch = ceil_div(a.hidden, kBlock) * kBlock;
+    rotate_row([row](int32_t i) { return bf16_lo(row[i]); }, a.hidden, a.rotated + t * pitch, a.scale + t);
+    return;
+  }
+  const int32_t w = blockIdx.x - a.tokens;
+  const int32_t e0 = (w % a.expert_groups * kRouterWaves + (threadIdx.x >> 6)) * kRouterExperts;
+  if (e0 >= a.experts) return;
+  if (a.tokens == 1)
+    router_logits<1>(a, e0, 0);
+  else
+    router_logits<kRouterTokens>(a, e0, w / a.expert_groups * kRouterTokens);
+}
+
+// ---------------------------------------------------------------------------
+// The best experts of a token, a wave each: lane l holds experts l, l + 64, ..
+// ---------------------------------------------------------------------------
+
+struct TopArgs {
+  const double* logits;
+  int32_t* ids;
+  float* weights;
+  int32_t tokens, experts, top_k, renormalize;
+};
+
+// Order of 64-bit floats as that of unsigned numbers; NaN lowest, then minus infinity; never 0.
+__device__ __forceinline__ uint64_t order_of(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 counts as 0
+  if (v != v) return 1;
+  return u >> 63 ? ~u : u | (uint64_t{1} << 63);
+}
+__device__ __forceinline__ double value_of(uint64_t key) {
+  if (key == 1) return __builtin_nan("");
+  return __builtin_bit_cast(double, key >> 63 ? key & ~(uint64_t{1} << 63) : ~key);
+}
+__device__ __forceinline__ uint32_t top_of_wave(uint32_t v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = max(v, lane_xor(v, d));
+  return v;
+}
+__device__ __forceinline__ uint64_t top_of_wave(uint64_t v) {
+  const uint32_t hi = top_of_wave(static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = top_of_wave(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+constexpr int kTopThreads = 256;
+template <int PER>
+__global__ void __launch_bounds__(kTopThreads) hlwq_moe_top_kernel(const TopArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int32_t t = blockIdx.x * (kTopThreads / 64) + (threadIdx.x >> 6);
+  if (t >= a.tokens) return;
+  const double* row = a.logits + static_cast<int64_t>(t) * a.experts;
+  uint64_t key[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) key[k] = lane + 64 * k < a.experts ? order_of(row[lane + 64 * k]) : 0;
+  double top = 0, total = 0, mine = 0;
+  int32_t chosen = 0;
+  if (!a.renormalize) {
+    uint64_t best = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) best = max(best, key[k]);
+    top = value_of(top_of_wave(best));
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (key[k]) total += exp(value_of(key[k]) - top);
+    total = wave_sum(total);
+  }
+  for (int32_t j = 0; j < a.top_k; ++j) {
+    uint64_t best = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) best = max(best, key[k]);
+    best = top_of_wave(best);
+    // of equal ones the lowest index: the lowest k, then the lowest lane
+    int32_t at = 0;
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const uint64_t has = __ballot(key[k] == best);
+      if (!found && has) {
+        at = 64 * k + __builtin_ctzll(has);
+        found = true;
+        if (lane == (at & 63)) key[k] = 0;
+      }
+    }
+    const double v = value_of(best);
+    if (j == 0 && a.renormalize) top = v;
+    const double w = exp(v - top);
+    if (a.renormalize) total += w;
+    if (lane == j) {
+      mine = w;
+      chosen = at;
+    }
+  }
+  if (lane < a.top_k) {
+    const int64_t p = static_cast<int64_t>(t) * a.top_k + lane;
+    a.ids[p] = chosen;
+    a.weights[p] = static_cast<float>(mine / total);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Products with an expert's codes.  A workgroup takes the a-th of the experts
+// that some pair names and some tiles of sixteen rows of its matrix (with GATED
+// the same tile of gate and up); its waves split the blocks of a row, KS ways,
+// or the tiles.  Per block and tile a lane holds 32 codes of one row, looks them
+// up two at a time, and they meet sixteen pairs' activations in four matrix
+// products; the norm of a row and block multiplies the result, where it is one
+// value to a lane.
+// ---------------------------------------------------------------------------
+
+constexpr int kProductThreads = 512, kProductWaves = kProductThreads / 64;
+
+struct ProductArgs {
+  const uint8_t* packed;
+  const uint16_t* norms;
+  const uint16_t* act;     // fp16 [.][nb * 128]
+  const float* act_scale;  // [.]
+  const int32_t* ids;      // [pairs]
+  const float* weights;    // [pairs] (GATED)
+  float* out;              // [pairs][n_out]
+  int32_t pairs, experts, top_k;
+  int32_t rows;   // of an expert's matrix
+  int32_t n_out;  // of them outputs: rows, or half of them
+  int32_t nb;     // blocks to a row
+  int32_t tiles;  // of outputs, a pair of row tiles each
+  int32_t activation;
+};
+
+template <int BITS>
+struct PairBook {
+  static constexpr int kCount = 1 << (2 * BITS);
+};
+
+template <int BITS>
+struct RowCodes;
+template <>
+struct RowCodes<5> {
+  u32x4_4 a;
+  uint32_t b;
+};
+template <>
+struct RowCodes<3> {
+  u32x3_4 a;
+};
+__device__ __forceinline__ void load_row(RowCodes<5>& c, const uint8_t* p) {
+  c.a = *reinterpret_cast<const u32x4_4*>(p);
+  c.b = *reinterpret_cast<const uint32_t*>(p + 16);
+}
+__device__ __forceinline__ void load_row(RowCodes<3>& c, const uint8_t* p) { c.a = *reinterpret_cast<const u32x3_4*>(p); }
+__device__ __forceinline__ uint32_t word_of(const RowCodes<5>& c, int i) { return i < 4 ? c.a[i] : c.b; }
+__device__ __forceinline__ uint32_t word_of(const RowCodes<3>& c, int i) { return c.a[i]; }
+
+constexpr int kBookShift = 2;  // 2^2 copies of the book, side by side
+
+// 32 codes to four operands of eight centroids.
+template <int BITS>
+__device__ __forceinline__ void decode(const RowCodes<BITS>& c, const uint32_t* book, uint32_t copy, u32x4 (&w)[4]) {
+#pragma unroll
+  for (int p = 0; p < 16; ++p) {
+    const int bit = 2 * BITS * p, at = bit >> 5, s = bit & 31;
+    uint32_t v = word_of(c, at);
+    if (s + 2 * BITS > 32)
+      v = __builtin_amdgcn_alignbit(word_of(c, at + 1), v, s);
+    else
+      v >>= s;
+    v &= PairBook<BITS>::kCount - 1;
+    w[p >> 2][p & 3] = book[(v << kBookShift) | copy];
+  }
+}
+
+__device__ __forceinline__ float sigmoid_times(float g, float z) { return g / (1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * z)); }
+__device__ __forceinline__ float activate(float g, int32_t kind) {
+  // gelu's g / 2 (1 + tanh(z)) is g / (1 + exp(-2 z))
+  return sigmoid_times(g, kind == HLWQ_ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g));
+}
+
+template <int BITS>
+__device__ __forceinline__ void fill_book(uint32_t* book) {
+  constexpr float c5[32] = HLWQ_CENTROIDS_5;
+  constexpr float c3[8] = HLWQ_CENTROIDS_3;
+  for (int i = threadIdx.x; i < PairBook<BITS>::kCount << kBookShift; i += kProductThreads) {
+    const int p = i >> kBookShift, lo = p & ((1 << BITS) - 1), hi = p >> BITS;
+    book[i] = BITS == 5 ? pack_f16x2(c5[lo], c5[hi]) : pack_f16x2(c3[lo & 7], c3[hi & 7]);
+  }
+}
+
+template <int BITS, int KS, int BW, bool GATED>
+__global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const ProductArgs a) {
+  constexpr int kGroups = kProductWaves / KS;  // of waves, a tile each
+  constexpr int kPitch = 20;                   // floats to a pair's sums of a tile
+  __shared__ uint32_t book[PairBook<BITS>::kCount << kBookShift];
+  __shared__ int32_t list[kMaxPairs];
+  __shared__ uint32_t named[kMaxExperts / 32];
+  __shared__ int32_t count_of;
+  __shared__ float sums[kProductWaves][2][kTile * kPitch];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // the expert, and its pairs (in any order: each is a column of its own)
+  if (threadIdx.x < kMaxExperts / 32) named[threadIdx.x] = 0;
+  if (threadIdx.x == 0) count_of = 0;
+  fill_book<BITS>(book);
+  __syncthreads();
+  int32_t id[kMaxPairs / kProductThreads];
+#pragma unroll
+  for (int k = 0; k < kMaxPairs / kProductThreads; ++k) {
+    const int32_t p = threadIdx.x + k * kProductThreads;
+    id[k] = p < a.pairs ? a.ids[p] : -1;
+    if (id[k] >= a.experts) id[k] = -1;
+    if (id[k] >= 0) atomicOr(&named[id[k] >> 5], 1u << (id[k] & 31));
+  }
+  __syncthreads();
+  int32_t expert;
+  {
+    uint32_t word = lane < kMaxExperts / 32 ? named[lane] : 0;
+    const int32_t upto = wave_scan(static_cast<int32_t>(__builtin_popcount(word)));
+    const uint64_t past = __ballot(upto > static_cast<int32_t>(blockIdx.y));
+    if (!past) return;
+    const int at = __builtin_ctzll(past);
+    word = __builtin_amdgcn_readlane(word, at);
+    int32_t skip = blockIdx.y - (__builtin_amdgcn_readlane(upto, at) - __builtin_popcount(word));
+    for (; skip > 0; --skip) word &= word - 1;
+    expert = 32 * at + __builtin_ctz(word);
+  }
+#pragma unroll
+  for (int k = 0; k < kMaxPairs / kProductThreads; ++k)
+    if (id[k] == expert) list[atomicAdd(&count_of, 1)] = threadIdx.x + k * kProductThreads;
+  __syncthreads();
+  const int32_t count = count_of;
+
+  const int r = lane & 15, h4 = lane >> 4;
+  const int ks = wave % KS, group = wave / KS;
+  const uint32_t copy = lane & ((1 << kBookShift) - 1);
+  const uint8_t* packed = a.packed + static_cast<int64_t>(expert) * a.rows * a.nb * (16 * BITS);
+  const uint16_t* norms = a.norms + static_cast<int64_t>(expert) * a.rows * a.nb;
+  const int32_t pitch = a.nb * kBlock;
+
+  for (int32_t c0 = 0; c0 < count; c0 += kTile) {
+    const int32_t pair = c0 + r < count ? list[c0 + r] : -1;
+    const uint16_t* act = a.act + static_cast<int64_t>(GATED ? max(pair, 0) / a.top_k : max(pair, 0)) * pitch + 32 * h4;
+    for (int32_t tile0 = blockIdx.x * kGroups; tile0 < a.tiles; tile0 += gridDim.x * kGroups) {
+      const int32_t tile = tile0 + group;
+      f32x4 acc[2] = {};
+      if (tile < a.tiles) {
+        const int32_t first[2] = {GATED ? tile * kTile : 2 * tile * kTile, GATED ? a.n_out + tile * kTile : (2 * tile + 1) * kTile};
+        uint32_t row[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) row[m] = min(first[m] + r, a.rows - 1) * a.nb;
+        for (int32_t b0 = ks * BW; b0 < a.nb; b0 += KS * BW) {
+          RowCodes<BITS> codes[BW][2];
+          float norm[BW][2];
+          u32x4 x[BW][4];
+#pragma unroll
+          for (int k = 0; k < BW; ++k)
+            if (b0 + k < a.nb) {
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                load_row(codes[k][m], packed + static_cast<uint64_t>(row[m] + b0 + k) * (16 * BITS) + 4 * BITS * h4);
+                norm[k][m] = f16_value(norms[row[m] + b0 + k]);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                x[k][j] = pair >= 0 ? *reinterpret_cast<const u32x4*>(act + (b0 + k) * kBlock + 8 * j) : u32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+          for (int k = 0; k < BW; ++k)
+            if (b0 + k < a.nb) {
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                u32x4 w[4];
+                decode<BITS>(codes[k][m], book, copy, w);
+                f32x4 d = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x[k][j]), __builtin_bit_cast(f16x8, w[j]), d, 0, 0, 0);
+                acc[m] += d * norm[k][m];
+              }
+            }
+        }
+      }
+      // pairs 4 h4 + i of row r: the waves that split the blocks join
+      __syncthreads();
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[wave][m][(4 * h4 + i) * kPitch + r] = acc[m][i];
+      __syncthreads();
+      for (int32_t i = threadIdx.x; i < kGroups * kTile * kTile; i += kProductThreads) {
+        const int32_t g = i / (kTile * kTile), c = i / kTile % kTile, rr = i % kTile;
+        if (tile0 + g >= a.tiles || c0 + c >= count) continue;
+        const int32_t p = list[c0 + c];
+        float s[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) s[m] += sums[g * KS + k][m][c * kPitch + rr];
+        const float scale = a.act_scale[GATED ? p / a.top_k : p];
+        float* out = a.out + static_cast<int64_t>(p) * a.n_out;
+        if constexpr (GATED) {
+          const int32_t o = (tile0 + g) * kTile + rr;
+          if (o < a.n_out) out[o] = activate(s[0] * scale, a.activation) * (s[1] * scale) * a.weights[p];
+        } else {
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const int32_t o = (2 * (tile0 + g) + m) * kTile + rr;
+            if (o < a.n_out) out[o] = s[m] * scale;
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Between the two: a pair's inner activations rotated; after them: a token's
+// pairs joined.
+// ---------------------------------------------------------------------------
+
+struct RotateArgs {
+  const float* in;  // [pairs][n]
+  const int32_t* ids;
+  uint16_t* rotated;
+  float* scale;
+  int32_t n, experts;
+};
+__global__ void __launch_bounds__(kRotateThreads) hlwq_moe_rotate_kernel(const RotateArgs a) {
+  const int32_t p = blockIdx.x;
+  if (a.ids[p] < 0 || a.ids[p] >= a.experts) return;
+  const float* row = a.in + static_cast<int64_t>(p) * a.n;
+  const int64_t pitch = ceil_div(a.n, kBlock) * kBlock;
+  rotate_row([row](int32_t i) { return row[i]; }, a.n, a.rotated + p * pitch, a.scale + p);
+}
+
+struct JoinArgs {
+  const float* in;  // [pairs][n]
+  const int32_t* ids;
+  uint16_t* out;  // [tokens][n]
+  int32_t n, experts, top_k;
+};
+__global__ void __launch_bounds__(256) hlwq_moe_join_kernel(const JoinArgs a) {
+  const int32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.n) return;
+  const int64_t t = blockIdx.y;
+  float s = 0;
+  for (int32_t k = 0; k < a.top_k; ++k) {
+    const int64_t p = t * a.top_k + k;
+    if (a.ids[p] >= 0 && a.ids[p] < a.experts) s += a.in[p * a.n + i];
+  }
+  a.out[t * a.n + i] = static_cast<uint16_t>(pack_bf16x2(s, 0));
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+struct Sizes {
+  int64_t experts, hidden, inner, tokens, top_k;
+  int64_t hidden_blocks, inner_blocks;
+  int64_t pass;  // tokens to a pass
+};
+
+// *nothing: valid, with no work.
+int check_sizes(Sizes& s, bool* nothing) {
+  if (s.experts < 0 || s.hidden < 0 || s.inner < 0 || s.tokens < 0 || s.top_k < 0) return HLWQ_ERR_SHAPE;
+  if (s.experts > kMaxExperts || s.hidden > kMaxSize || s.inner > kMaxSize || s.top_k > kMaxTopK || s.tokens > kMaxTokens)
+    return HLWQ_ERR_LIMIT;
+  *nothing = s.tokens == 0 || s.hidden == 0;
+  s.hidden_blocks = ceil_div(s.hidden, kBlock);
+  s.inner_blocks = ceil_div(s.inner, kBlock);
+  s.pass = std::min(s.tokens, kMaxPairs / std::max<int64_t>(s.top_k, 1));
+  return HLWQ_OK;
+}
+
+// The workspace's parts, each a multiple of 16 bytes.
+struct Parts {
+  size_t logits, x, x_scale, h, h_rotated, h_scale, y, total;
+};
+Parts parts_of(const Sizes& s) {
+  Parts p;
+  size_t at = 0;
+  const auto take = [&at](int64_t count, int64_t unit) {
+    const size_t here = at;
+    at += (static_cast<size_t>(count * unit) + 15) & ~size_t{15};
+    return here;
+  };
+  const int64_t pairs = s.pass * s.top_k;
+  p.logits = take(s.pass * s.experts, 8);
+  p.x = take(s.pass * s.hidden_blocks * kBlock, 2);
+  p.x_scale = take(s.pass, 4);
+  p.h = take(pairs * s.inner, 4);
+  p.h_rotated = take(pairs * s.inner_blocks * kBlock, 2);
+  p.h_scale = take(pairs, 4);
+  p.y = take(pairs * s.hidden, 4);
+  p.total = at;
+  return p;
+}
+
+template <int BITS, bool GATED>
+int launch_product(const ProductArgs& a, hipStream_t stream) {
+  const auto go = [&](auto kernel, int groups) {
+    const uint32_t wide = static_cast<uint32_t>(ceil_div(a.tiles, groups));
+    return launch(kernel, dim3(wide, static_cast<uint32_t>(std::min(a.experts, a.pairs))), dim3(kProductThreads), stream, a);
+  };
+  if (a.nb <= 4) return go(hlwq_moe_product_kernel<BITS, 4, 1, GATED>, 2);
+  if (a.nb <= 8) return go(hlwq_moe_product_kernel<BITS, 4, 2, GATED>, 2);
+  if (a.nb <= 16) return go(hlwq_moe_product_kernel<BITS, 8, 2, GATED>, 1);
+  return go(hlwq_moe_product_kernel<BITS, 8, 3, GATED>, 1);
+}
+
+int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t tokens, const void* router, bool route, int64_t top_k,
+            int renormalize, int32_t* ids, float* weights, void* out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!b) return HLWQ_ERR_NULL;
+  if (b->bits != 5 && b->bits != 3) return HLWQ_ERR_BITS;
+  if (b->activation != HLWQ_ACT_SILU && b->activation != HLWQ_ACT_GELU_TANH) return HLWQ_ERR_SHAPE;
+  Sizes s{b->experts, b->hidden, b->inner, tokens, top_k, 0, 0, 0};
+  bool nothing;
+  int st = check_sizes(s, &nothing);
+  if (st != HLWQ_OK) return st;
+  if (x_stride < s.hidden || (route && top_k > s.experts)) return HLWQ_ERR_SHAPE;
+  const int64_t block = 16 * b->bits;
+  if (x_stride > kMaxSize || 2 * s.inner * s.hidden_blocks > 0x7fffffff / block || s.hidden * s.inner_blocks > 0x7fffffff / block)
+    return HLWQ_ERR_LIMIT;
+  if (nothing) return HLWQ_OK;
+  const int64_t pairs = tokens * top_k, up = s.experts * 2 * s.inner * s.hidden_blocks, down = s.experts * s.hidden * s.inner_blocks;
+  const Parts parts = parts_of(s);
+  if (!x || !out || !ws || (route && s.experts > 0 && !router) || (pairs > 0 && (!ids || !weights)) ||
+      (up > 0 && (!b->gate_up_packed || !b->gate_up_norms)) || (down > 0 && (!b->down_packed || !b->down_norms)))
+    return HLWQ_ERR_NULL;
+  if (ws_bytes < parts.total) return HLWQ_ERR_SHAPE;
+  if (misaligned(x, 2) || misaligned(out, 2) || misaligned(router, 2) || misaligned(ids, 4) || misaligned(weights, 4) ||
+      misaligned(ws, 16) || misaligned(b->gate_up_packed, 4) || misaligned(b->down_packed, 4) ||
+      misaligned(b->gate_up_norms, 2) || misaligned(b->down_norms, 2))
+    return HLWQ_ERR_ALIGN;
+  Spans spans;
+  add_span(spans, x, (tokens - 1) * x_stride + s.hidden, 2, false);
+  if (route) add_span(spans, router, s.experts * s.hidden, 2, false);
+  add_span(spans, b->gate_up_packed, up, block, false);
+  add_span(spans, b->gate_up_norms, up, 2, false);
+  add_span(spans, b->down_packed, down, block, false);
+  add_span(spans, b->down_norms, down, 2, false);
+  add_span(spans, ids, pairs, 4, route);
+  add_span(spans, weights, pairs, 4, route);
+  add_span(spans, out, tokens * s.hidden, 2, true);
+  add_span(spans, ws, static_cast<int64_t>(parts.total), 1, true);
+  if (check_disjoint(spans) != HLWQ_OK) return HLWQ_ERR_OVERLAP;
+
+  char* const at = static_cast<char*>(ws);
+  const auto i32 = [](int64_t v) { return static_cast<int32_t>(v); };
+  for (int64_t t0 = 0; t0 < tokens; t0 += s.pass) {
+    const int64_t n = std::min(s.pass, tokens - t0), m = n * top_k;
+    int32_t* const my_ids = ids ? ids + t0 * top_k : nullptr;
+    float* const my_weights = weights ? weights + t0 * top_k : nullptr;
+    uint16_t* const my_out = static_cast<uint16_t*>(out) + t0 * s.hidden;
+    const bool empty = m == 0 || s.inner == 0 || s.experts == 0;
+    PrepareArgs pa{};
+    pa.x = static_cast<const uint16_t*>(x) + t0 * x_stride;
+    pa.x_stride = x_stride;
+    pa.router = route ? static_cast<const uint16_t*>(router) : nullptr;
+    pa.logits = reinterpret_cast<double*>(at + parts.logits);
+    pa.rotated = reinterpret_cast<uint16_t*>(at + parts.x);
+    pa.scale = reinterpret_cast<float*>(at + parts.x_scale);
+    pa.tokens = i32(n);
+    pa.hidden = i32(s.hidden);
+    pa.experts = i32(s.experts);
+    pa.expert_groups = i32(ceil_div(s.experts, kRouterExperts * kRouterWaves));
+    const int64_t router_groups = route ? pa.expert_groups * ceil_div(n, n == 1 ? 1 : kRouterTokens) : 0;
+    if ((st = launch(hlwq_moe_prepare_kernel, dim3(static_cast<uint32_t>(n + router_groups)), dim3(kRotateThreads), stream, pa)) != HLWQ_OK)
+      return st;
+    if (route && m > 0) {
+      TopArgs ta{pa.logits, my_ids, my_weights, i32(n), i32(s.experts), i32(top_k), renormalize != 0};
+      const dim3 grid(static_cast<uint32_t>(ceil_div(n, kTopThreads / 64)));
+      st = s.experts <= 256 ? launch(hlwq_moe_top_kernel<4>, grid, dim3(kTopThreads), stream, ta)
+                            : launch(hlwq_moe_top_kernel<16>, grid, dim3(kTopThreads), stream, ta);
+      if (st != HLWQ_OK) return st;
+    }
+    if (!empty) {
+      ProductArgs g{};
+      g.packed = static_cast<const uint8_t*>(b->gate_up_packed);
+      g.norms = static_cast<const uint16_t*>(b->gate_up_norms);
+      g.act = pa.rotated;
+      g.act_scale = pa.scale;
+      g.ids = my_ids;
+      g.weights = my_weights;
+      g.out = reinterpret_cast<float*>(at + parts.h);
+      g.pairs = i32(m);
+      g.experts = i32(s.experts);
+      g.top_k = i32(top_k);
+      g.rows = i32(2 * s.inner);
+      g.n_out = i32(s.inner);
+      g.nb = i32(s.hidden_blocks);
+      g.tiles = i32(ceil_div(s.inner, kTile));
+      g.activation = b->activation;
+      if ((st = b->bits == 5 ? launch_product<5, true>(g, stream) : launch_product<3, true>(g, stream)) != HLWQ_OK) return st;
+      RotateArgs ra{g.out, my_ids, reinterpret_cast<uint16_t*>(at + parts.h_rotated), reinterpret_cast<float*>(at + parts.h_scale),
+                    i32(s.inner), i32(s.experts)};
+      if ((st = launch(hlwq_moe_rotate_kernel, dim3(static_cast<uint32_t>(m)), dim3(kRotateThreads), stream, ra)) != HLWQ_OK) return st;
+      ProductArgs d = g;
+      d.packed = static_cast<const uint8_t*>(b->down_packed);
+      d.norms = static_cast<const uint16_t*>(b->down_norms);
+      d.act = ra.rotated;
+      d.act_scale = ra.scale;
+      d.weights = nullptr;
+      d.out = reinterpret_cast<float*>(at + parts.y);
+      d.rows = d.n_out = i32(s.hidden);
+      d.nb = i32(s.inner_blocks);
+      d.tiles = i32(ceil_div(s.hidden, 2 * kTile));
+      if ((st = b->bits == 5 ? launch_product<5, false>(d, stream) : launch_product<3, false>(d, stream)) != HLWQ_OK) return st;
+    }
+    JoinArgs ja{reinterpret_cast<const float*>(at + parts.y), my_ids, my_out, i32(s.hidden), i32(s.experts), empty ? 0 : i32(top_k)};
+    const dim3 grid(static_cast<uint32_t>(ceil_div(s.hidden, 256)), static_cast<uint32_t>(n));
+    if ((st = launch(hlwq_moe_join_kernel, grid, dim3(256), stream, ja)) != HLWQ_OK) return st;
+  }
+  return HLWQ_OK;
+}
+
+}  // namespace
+}  // namespace hlwq_kv
+
+extern "C" {
+
+int hlwq_moe_experts(const hlwq_moe_banks* banks, const void* x_bf16, int64_t x_stride, int64_t tokens, int64_t top_k,
+                     const int32_t* experts, const float* weights, void* out_bf16, void* workspace,
+                     size_t workspace_bytes, void* hip_stream) {
+  return hlwq_kv::run_moe(banks, x_bf16, x_stride, tokens, nullptr, false, top_k, 0, const_cast<int32_t*>(experts),
+                          const_cast<float*>(weights), out_bf16, workspace, workspace_bytes, static_cast<hipStream_t>(hip_stream));
+}
+
+int hlwq_moe_layer(const hlwq_moe_banks* banks, const void* x_bf16, int64_t x_stride, int64_t tokens,
+                   const void* router_bf16, int64_t top_k, int renormalize, int32_t* experts, float* weights,
+                   void* out_bf16, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return hlwq_kv::run_moe(banks, x_bf16, x_stride, tokens, router_bf16, true, top_k, renormalize, experts, weights, out_bf16,
+                          workspace, workspace_bytes, static_cast<hipStream_t>(hip_stream));
+}
+
+size_t hlwq_moe_workspace(int64_t experts, int64_t hidden, int64_t inner, int64_t tokens, int64_t top_k) {
+  hlwq_kv::Sizes s{experts, hidden, inner, tokens, top_k, 0, 0, 0};
+  bool nothing;
+  if (hlwq_kv::check_sizes(s, &nothing) != HLWQ_OK || nothing) return 0;
+  return hlwq_kv::parts_of(s).total;
+}
+
+}  // extern "C"
