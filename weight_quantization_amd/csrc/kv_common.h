@@ -71,6 +71,14 @@ __device__ __forceinline__ double lane_xor(double v, int d) {
   return __builtin_bit_cast(double, lo | static_cast<uint64_t>(hi) << 32);
 }
 
+// The value of one lane, in all.
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(u), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(u >> 32), lane);
+  return __builtin_bit_cast(double, lo | static_cast<uint64_t>(hi) << 32);
+}
+
 // Inclusive prefix sum over the wave: within rows of sixteen, then the rows'
 // last values on.
 template <int CTRL, int ROWS>

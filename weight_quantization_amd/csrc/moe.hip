@@ -1,7 +1,7 @@
 // moe.hip — a mixture-of-experts layer of a few tokens, from the codes of its
 // banks (include/hlwq_moe.h).
 
-#include "kv_common.h"
+#include "staging.h"
 
 #include "hlwq_moe.h"
 
@@ -10,6 +10,7 @@ namespace {
 
 typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x3_4 __attribute__((ext_vector_type(3), aligned(4)));
+typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -90,35 +91,57 @@ struct PrepareArgs {
   int32_t tokens, hidden, experts, expert_groups;
 };
 
-// Router logits of four experts and up to four tokens a wave, lanes along the
-// row.  Products of bf16 are exact in 64 bits, where they are summed: experts
-// whose logits differ by less than fp32 resolves are told apart.
-constexpr int kRouterExperts = 4, kRouterTokens = 4, kRouterWaves = kRotateThreads / 64;
+// Router logits of some experts and tokens a wave, lanes along the row, eight
+// values to a load.  Products of bf16 are exact in 64 bits, where they are summed:
+// experts whose logits differ by less than fp32 resolves are told apart.
+constexpr int kRouterWaves = kRotateThreads / 64;
 
-template <int TOKENS>
+template <int EXPERTS, int TOKENS>
 __device__ __forceinline__ void router_logits(const PrepareArgs& a, int32_t e0, int32_t t0) {
   const int lane = threadIdx.x & 63;
-  double sum[kRouterExperts][TOKENS] = {};
-  for (int32_t i = lane; i < a.hidden; i += 64) {
-    double r[kRouterExperts], x[TOKENS];
+  const uint16_t *r[EXPERTS], *x[TOKENS];
 #pragma unroll
-    for (int k = 0; k < kRouterExperts; ++k)
-      r[k] = bf16_lo(a.router[static_cast<int64_t>(min(e0 + k, a.experts - 1)) * a.hidden + i]);
+  for (int k = 0; k < EXPERTS; ++k) r[k] = a.router + static_cast<int64_t>(min(e0 + k, a.experts - 1)) * a.hidden;
 #pragma unroll
-    for (int k = 0; k < TOKENS; ++k) x[k] = bf16_lo(a.x[min(t0 + k, a.tokens - 1) * a.x_stride + i]);
+  for (int j = 0; j < TOKENS; ++j) x[j] = a.x + min(t0 + j, a.tokens - 1) * a.x_stride;
+  double sum[EXPERTS][TOKENS] = {};
+  const int32_t whole = a.hidden & ~7;
+#pragma unroll 2
+  for (int32_t i = 8 * lane; i < whole; i += 512) {
+    u32x4_2 rv[EXPERTS], xv[TOKENS];
 #pragma unroll
-    for (int k = 0; k < kRouterExperts; ++k)
+    for (int k = 0; k < EXPERTS; ++k) rv[k] = *reinterpret_cast<const u32x4_2*>(r[k] + i);
 #pragma unroll
-      for (int j = 0; j < TOKENS; ++j) sum[k][j] = __builtin_fma(r[k], x[j], sum[k][j]);
+    for (int j = 0; j < TOKENS; ++j) xv[j] = *reinterpret_cast<const u32x4_2*>(x[j] + i);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      double xd[TOKENS];
+#pragma unroll
+      for (int j = 0; j < TOKENS; ++j) xd[j] = w & 1 ? bf16_hi(xv[j][w >> 1]) : bf16_lo(xv[j][w >> 1]);
+#pragma unroll
+      for (int k = 0; k < EXPERTS; ++k) {
+        const double rd = w & 1 ? bf16_hi(rv[k][w >> 1]) : bf16_lo(rv[k][w >> 1]);
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j) sum[k][j] = __builtin_fma(rd, xd[j], sum[k][j]);
+      }
+    }
   }
+  if (const int32_t i = whole + lane; i < a.hidden)
 #pragma unroll
-  for (int k = 0; k < kRouterExperts; ++k)
+    for (int k = 0; k < EXPERTS; ++k)
+#pragma unroll
+      for (int j = 0; j < TOKENS; ++j) sum[k][j] = __builtin_fma(static_cast<double>(bf16_lo(r[k][i])), static_cast<double>(bf16_lo(x[j][i])), sum[k][j]);
+#pragma unroll
+  for (int k = 0; k < EXPERTS; ++k)
 #pragma unroll
     for (int j = 0; j < TOKENS; ++j) {
       const double s = wave_sum(sum[k][j]);
       if (lane == 0 && e0 + k < a.experts && t0 + j < a.tokens) a.logits[static_cast<int64_t>(t0 + j) * a.experts + e0 + k] = s;
     }
 }
+// Experts and tokens to a wave.
+__host__ __device__ inline int router_experts(int64_t tokens) { return tokens == 1 ? 1 : 4; }
+__host__ __device__ inline int router_tokens(int64_t tokens) { return tokens == 1 ? 1 : 4; }
 
 // The first workgroups rotate a token each, the others take the router's.
 __global__ void __launch_bounds__(kRotateThreads) hlwq_moe_prepare_kernel(const PrepareArgs a) {
@@ -130,12 +153,12 @@ __global__ void __launch_bounds__(kRotateThreads) hlwq_moe_prepare_kernel(const 
     return;
   }
   const int32_t w = blockIdx.x - a.tokens;
-  const int32_t e0 = (w % a.expert_groups * kRouterWaves + (threadIdx.x >> 6)) * kRouterExperts;
+  const int32_t e0 = (w % a.expert_groups * kRouterWaves + (threadIdx.x >> 6)) * router_experts(a.tokens);
   if (e0 >= a.experts) return;
   if (a.tokens == 1)
-    router_logits<1>(a, e0, 0);
+    router_logits<1, 1>(a, e0, 0);
   else
-    router_logits<kRouterTokens>(a, e0, w / a.expert_groups * kRouterTokens);
+    router_logits<4, 4>(a, e0, w / a.expert_groups * 4);
 }
 
 // ---------------------------------------------------------------------------
@@ -180,48 +203,47 @@ __global__ void __launch_bounds__(kTopThreads) hlwq_moe_top_kernel(const TopArgs
   uint64_t key[PER];
 #pragma unroll
   for (int k = 0; k < PER; ++k) key[k] = lane + 64 * k < a.experts ? order_of(row[lane + 64 * k]) : 0;
-  double top = 0, total = 0, mine = 0;
+  uint64_t all = 0;  // lane j: the j-th best's key
   int32_t chosen = 0;
-  if (!a.renormalize) {
-    uint64_t best = 0;
+  uint64_t left[PER];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) best = max(best, key[k]);
-    top = value_of(top_of_wave(best));
-#pragma unroll
-    for (int k = 0; k < PER; ++k)
-      if (key[k]) total += exp(value_of(key[k]) - top);
-    total = wave_sum(total);
-  }
+  for (int k = 0; k < PER; ++k) left[k] = key[k];
   for (int32_t j = 0; j < a.top_k; ++j) {
     uint64_t best = 0;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) best = max(best, key[k]);
+    for (int k = 0; k < PER; ++k) best = max(best, left[k]);
     best = top_of_wave(best);
     // of equal ones the lowest index: the lowest k, then the lowest lane
     int32_t at = 0;
     bool found = false;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const uint64_t has = __ballot(key[k] == best);
+      const uint64_t has = __ballot(left[k] == best);
       if (!found && has) {
         at = 64 * k + __builtin_ctzll(has);
         found = true;
-        if (lane == (at & 63)) key[k] = 0;
+        if (lane == (at & 63)) left[k] = 0;
       }
     }
-    const double v = value_of(best);
-    if (j == 0 && a.renormalize) top = v;
-    const double w = exp(v - top);
-    if (a.renormalize) total += w;
     if (lane == j) {
-      mine = w;
+      all = best;
       chosen = at;
     }
   }
+  const double top = lane_value(value_of(all), 0);
+  const double w = lane < a.top_k ? exp(value_of(all) - top) : 0.0;
+  double total = w;
+  if (!a.renormalize) {
+    total = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (key[k]) total += exp(value_of(key[k]) - top);
+  }
+  total = wave_sum(total);
   if (lane < a.top_k) {
     const int64_t p = static_cast<int64_t>(t) * a.top_k + lane;
     a.ids[p] = chosen;
-    a.weights[p] = static_cast<float>(mine / total);
+    a.weights[p] = static_cast<float>(w / total);
   }
 }
 
@@ -245,6 +267,8 @@ struct ProductArgs {
   const int32_t* ids;      // [pairs]
   const float* weights;    // [pairs] (GATED)
   float* out;              // [pairs][n_out]
+  uint16_t* rotated;       // [pairs][blocks of n_out * 128], where a workgroup rotates what it has
+  float* rotated_scale;    // [pairs][blocks of n_out]
   int32_t pairs, experts, top_k;
   int32_t rows;   // of an expert's matrix
   int32_t n_out;  // of them outputs: rows, or half of them
@@ -276,22 +300,32 @@ __device__ __forceinline__ void load_row(RowCodes<5>& c, const uint8_t* p) {
 __device__ __forceinline__ void load_row(RowCodes<3>& c, const uint8_t* p) { c.a = *reinterpret_cast<const u32x3_4*>(p); }
 __device__ __forceinline__ uint32_t word_of(const RowCodes<5>& c, int i) { return i < 4 ? c.a[i] : c.b; }
 __device__ __forceinline__ uint32_t word_of(const RowCodes<3>& c, int i) { return c.a[i]; }
+__device__ __forceinline__ void set_word(RowCodes<5>& c, int i, uint32_t v) {
+  if (i < 4)
+    c.a[i] = v;
+  else
+    c.b = v;
+}
+__device__ __forceinline__ void set_word(RowCodes<3>& c, int i, uint32_t v) { c.a[i] = v; }
 
-constexpr int kBookShift = 2;  // 2^2 copies of the book, side by side
+constexpr int kBookShift = 1;  // 2^1 copies of the book, side by side
 
-// 32 codes to four operands of eight centroids.
+// 32 codes to four operands of eight centroids: two codes, at a multiple of the
+// book's entry size, are where their pair of centroids lies (a shift, and one mask
+// with the lane's copy).
 template <int BITS>
-__device__ __forceinline__ void decode(const RowCodes<BITS>& c, const uint32_t* book, uint32_t copy, u32x4 (&w)[4]) {
+__device__ __forceinline__ void decode(const RowCodes<BITS>& c, const uint8_t* book, uint32_t copy, u32x4 (&w)[4]) {
+  constexpr int kTo = 2 + kBookShift;
+  constexpr uint32_t kMask = (PairBook<BITS>::kCount - 1) << kTo;
 #pragma unroll
   for (int p = 0; p < 16; ++p) {
     const int bit = 2 * BITS * p, at = bit >> 5, s = bit & 31;
     uint32_t v = word_of(c, at);
     if (s + 2 * BITS > 32)
-      v = __builtin_amdgcn_alignbit(word_of(c, at + 1), v, s);
+      v = __builtin_amdgcn_alignbit(word_of(c, at + 1), v, s - kTo);
     else
-      v >>= s;
-    v &= PairBook<BITS>::kCount - 1;
-    w[p >> 2][p & 3] = book[(v << kBookShift) | copy];
+      v = s >= kTo ? v >> (s - kTo) : v << (kTo - s);
+    w[p >> 2][p & 3] = *reinterpret_cast<const uint32_t*>(book + ((v & kMask) | copy));
   }
 }
 
@@ -311,6 +345,40 @@ __device__ __forceinline__ void fill_book(uint32_t* book) {
   }
 }
 
+// The a-th expert that some pair names, or -1; its pairs, in any order, to `list`.
+struct Expert {
+  int32_t id, count;
+};
+__device__ __forceinline__ Expert find_expert(const ProductArgs& a, int32_t slot, int32_t* list, uint32_t* named, int32_t* count_of) {
+  const int lane = threadIdx.x & 63;
+  if (threadIdx.x < kMaxExperts / 32) named[threadIdx.x] = 0;
+  if (threadIdx.x == 0) *count_of = 0;
+  __syncthreads();
+  int32_t id[kMaxPairs / kProductThreads];
+#pragma unroll
+  for (int k = 0; k < kMaxPairs / kProductThreads; ++k) {
+    const int32_t p = threadIdx.x + k * kProductThreads;
+    id[k] = p < a.pairs ? a.ids[p] : -1;
+    if (id[k] >= a.experts) id[k] = -1;
+    if (id[k] >= 0) atomicOr(&named[id[k] >> 5], 1u << (id[k] & 31));
+  }
+  __syncthreads();
+  uint32_t word = lane < kMaxExperts / 32 ? named[lane] : 0;
+  const int32_t upto = wave_scan(static_cast<int32_t>(__builtin_popcount(word)));
+  const uint64_t past = __ballot(upto > slot);
+  if (!past) return Expert{-1, 0};
+  const int at = __builtin_ctzll(past);
+  word = __builtin_amdgcn_readlane(word, at);
+  int32_t skip = slot - (__builtin_amdgcn_readlane(upto, at) - __builtin_popcount(word));
+  for (; skip > 0; --skip) word &= word - 1;
+  const int32_t expert = 32 * at + __builtin_ctz(word);
+#pragma unroll
+  for (int k = 0; k < kMaxPairs / kProductThreads; ++k)
+    if (id[k] == expert) list[atomicAdd(count_of, 1)] = threadIdx.x + k * kProductThreads;
+  __syncthreads();
+  return Expert{expert, *count_of};
+}
+
 template <int BITS, int KS, int BW, bool GATED>
 __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const ProductArgs a) {
   constexpr int kGroups = kProductWaves / KS;  // of waves, a tile each
@@ -322,41 +390,14 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
   __shared__ float sums[kProductWaves][2][kTile * kPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // the expert, and its pairs (in any order: each is a column of its own)
-  if (threadIdx.x < kMaxExperts / 32) named[threadIdx.x] = 0;
-  if (threadIdx.x == 0) count_of = 0;
   fill_book<BITS>(book);
-  __syncthreads();
-  int32_t id[kMaxPairs / kProductThreads];
-#pragma unroll
-  for (int k = 0; k < kMaxPairs / kProductThreads; ++k) {
-    const int32_t p = threadIdx.x + k * kProductThreads;
-    id[k] = p < a.pairs ? a.ids[p] : -1;
-    if (id[k] >= a.experts) id[k] = -1;
-    if (id[k] >= 0) atomicOr(&named[id[k] >> 5], 1u << (id[k] & 31));
-  }
-  __syncthreads();
-  int32_t expert;
-  {
-    uint32_t word = lane < kMaxExperts / 32 ? named[lane] : 0;
-    const int32_t upto = wave_scan(static_cast<int32_t>(__builtin_popcount(word)));
-    const uint64_t past = __ballot(upto > static_cast<int32_t>(blockIdx.y));
-    if (!past) return;
-    const int at = __builtin_ctzll(past);
-    word = __builtin_amdgcn_readlane(word, at);
-    int32_t skip = blockIdx.y - (__builtin_amdgcn_readlane(upto, at) - __builtin_popcount(word));
-    for (; skip > 0; --skip) word &= word - 1;
-    expert = 32 * at + __builtin_ctz(word);
-  }
-#pragma unroll
-  for (int k = 0; k < kMaxPairs / kProductThreads; ++k)
-    if (id[k] == expert) list[atomicAdd(&count_of, 1)] = threadIdx.x + k * kProductThreads;
-  __syncthreads();
-  const int32_t count = count_of;
+  const Expert ex = find_expert(a, blockIdx.y, list, named, &count_of);
+  if (ex.id < 0) return;
+  const int32_t expert = ex.id, count = ex.count;
 
   const int r = lane & 15, h4 = lane >> 4;
   const int ks = wave % KS, group = wave / KS;
-  const uint32_t copy = lane & ((1 << kBookShift) - 1);
+  const uint32_t copy = (lane & ((1 << kBookShift) - 1)) * 4;
   const uint8_t* packed = a.packed + static_cast<int64_t>(expert) * a.rows * a.nb * (16 * BITS);
   const uint16_t* norms = a.norms + static_cast<int64_t>(expert) * a.rows * a.nb;
   const int32_t pitch = a.nb * kBlock;
@@ -394,7 +435,7 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
                 u32x4 w[4];
-                decode<BITS>(codes[k][m], book, copy, w);
+                decode<BITS>(codes[k][m], reinterpret_cast<const uint8_t*>(book), copy, w);
                 f32x4 d = {0, 0, 0, 0};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -434,6 +475,263 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
         }
       }
     }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The same where the touched experts are many.  A workgroup a CU takes an equal
+// run of (expert, 128 rows of gate and of up, or 256 of down), a wave a pair of
+// row tiles of each, whose blocks it goes through from first to last, so that no
+// sums are joined.  The codes come straight to LDS, four blocks of both tiles at a
+// time, the next four as soon as these are in registers: four lanes fetch 64
+// bytes of a row side by side (each lane its own 20 bytes of another row, straight
+// to registers, is an address a cycle, and took twice as long), and 16-byte pieces
+// are turned by the row so that the dwords that the lanes then read lie in
+// different banks.  Inner values are rotated before they leave, over a power of
+// two for each block (act_scale [.][nb]).
+// ---------------------------------------------------------------------------
+
+constexpr int kWorkgroups = 256;
+constexpr int kMaxInnerBlocks = 64;  // whose scales a workgroup keeps
+constexpr int kActBytes = 48 << 10;  // of activations in LDS
+constexpr int kChunk = 4;            // blocks that are staged together
+
+template <int BITS>
+struct StreamLds {
+  static constexpr uint32_t codes = 1024 * BITS, norms = 2 * codes, wave = norms + 2 * 256;  // of a wave: two tiles' codes, their norms
+  static constexpr uint32_t book = 0, stage = (PairBook<BITS>::kCount << kBookShift) * 4, act = stage + kProductWaves * wave,
+                            inner = act + kActBytes, list = inner + kTile * (kBlock + 4) * 4, bytes = list + kMaxPairs * 2;
+};
+
+template <int BITS, bool GATED>
+__global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(const ProductArgs a) {
+  using L = StreamLds<BITS>;
+  constexpr int kPitch = kBlock + 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[L::bytes];
+  __shared__ uint32_t named[kMaxExperts / 2];  // pairs of two experts
+  __shared__ int32_t counts[64];
+  static_assert(kMaxPairs == 64 * 64, "a count for each wave's ballot");
+  static_assert(kMaxInnerBlocks * kTile <= kTile * kPitch, "scales lie where inner values do");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+  float* const inner = reinterpret_cast<float*>(lds + L::inner);
+  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + L::list);
+  const int r = lane & 15, h4 = lane >> 4;
+  const uint32_t copy = (lane & ((1 << kBookShift) - 1)) * 4;
+
+  const int32_t sets = a.tiles;  // of 128 or 256 rows
+  const int32_t capacity = min(kTile, kActBytes / (a.nb * 256));
+
+  // The experts' pairs, and this workgroup's run of (expert, pass over as many of
+  // its pairs as fit, set): passes cost the same whatever their pairs.
+  static_assert(kMaxExperts == 64 * 16 && kMaxPairs < 0x10000, "sixteen experts a lane, two counts a word");
+  for (int i = threadIdx.x; i < kMaxExperts / 2; i += kProductThreads) named[i] = 0;
+  __syncthreads();
+  int32_t id[kMaxPairs / kProductThreads];
+#pragma unroll
+  for (int k = 0; k < kMaxPairs / kProductThreads; ++k) {
+    const int32_t p = threadIdx.x + k * kProductThreads;
+    id[k] = p < a.pairs ? a.ids[p] : -1;
+    if (id[k] >= a.experts) id[k] = -1;
+    if (id[k] >= 0) atomicAdd(&named[id[k] >> 1], 1u << 16 * (id[k] & 1));
+  }
+  fill_book<BITS>(reinterpret_cast<uint32_t*>(lds + L::book));
+  __syncthreads();
+  const auto count_at = [&](int32_t e) { return static_cast<int32_t>(named[e >> 1] >> 16 * (e & 1) & 0xffff); };
+  const auto passes_at = [&](int32_t e) { return (count_at(e) + capacity - 1) / capacity; };
+  int32_t own = 0;
+  for (int i = 0; i < 16; ++i) own += passes_at(16 * lane + i);
+  const int32_t upto = wave_scan(own);
+  const int64_t total = static_cast<int64_t>(__builtin_amdgcn_readlane(upto, 63)) * sets;
+  int32_t q = static_cast<int32_t>(total * blockIdx.x / gridDim.x);
+  const int32_t q_end = static_cast<int32_t>(total * (blockIdx.x + 1) / gridDim.x);
+
+  const uint32_t row_bytes = a.nb * (16 * BITS);
+  const int32_t chunks = static_cast<int32_t>(ceil_div(a.nb, kChunk)), pitch = a.nb * kBlock;
+  const uint32_t my = base + L::stage + wave * L::wave;
+  // where dword d of a lane's codes of block k lies in a tile's stage
+  uint32_t place[kChunk][BITS];
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k)
+#pragma unroll
+    for (int d = 0; d < BITS; ++d) {
+      const int g = 4 * BITS * k + BITS * h4 + d;
+      place[k][d] = my + (g >> 4) * 1024 + r * 64 + (((g >> 2) & 3) ^ (r >> 2)) * 16 + (g & 3) * 4;
+    }
+  const auto row_of = [&](int32_t set, int m, int i) {
+    const int32_t o = (set * kProductWaves + wave) * (GATED ? kTile : 2 * kTile);
+    return min(o + i + (GATED ? m * a.n_out : m * kTile), a.rows - 1);
+  };
+
+  int32_t listed = -1;
+  while (q < q_end) {
+    const int32_t slot = q / sets, set0 = q - slot * sets, set1 = min(sets, set0 + q_end - q);
+    q += set1 - set0;
+    const int at = __builtin_ctzll(__ballot(upto > slot));
+    const int32_t rest = slot - __builtin_amdgcn_readlane(upto - own, at);
+    const int32_t its = lane < 16 ? passes_at(16 * at + lane) : 0, its_upto = wave_scan(its);
+    const int within = __builtin_ctzll(__ballot(its_upto > rest));
+    const int32_t expert = 16 * at + within, c0 = (rest - __builtin_amdgcn_readlane(its_upto - its, within)) * capacity;
+    const int32_t columns = min(capacity, count_at(expert) - c0);
+    const int64_t first = static_cast<int64_t>(expert) * a.rows * a.nb, blocks = static_cast<int64_t>(a.rows) * a.nb;
+    const u32x4 codes = buffer_of(a.packed + first * (16 * BITS), blocks * (16 * BITS)), norms = buffer_of(a.norms + first, 2 * blocks);
+    const auto stage = [&](int32_t set, int32_t chunk) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t row = row_of(set, m, lane >> 2);
+        const uint32_t from = row * row_bytes + chunk * (kChunk * 16 * BITS) + 16 * ((lane & 3) ^ (lane >> 4));
+#pragma unroll
+        for (int i = 0; i < BITS; ++i) stage16(codes, from + 64 * i, my + m * L::codes + i * 1024);
+        stage4(norms, ((2 * (row * a.nb + chunk * kChunk)) & ~3u) + 4 * (lane & 3), my + L::norms + m * 256);
+      }
+    };
+    const auto idle = [&](int32_t set) { return (set * kProductWaves + wave) * (GATED ? kTile : 2 * kTile) >= a.n_out; };
+    if (!idle(set0)) stage(set0, 0);
+
+    // the expert's pairs in order, as other workgroups may take other passes of them
+    barrier();
+    if (expert != listed) {
+      uint64_t mine[kMaxPairs / kProductThreads];
+#pragma unroll
+      for (int k = 0; k < kMaxPairs / kProductThreads; ++k) {
+        mine[k] = __ballot(id[k] == expert);
+        if (lane == 0) counts[k * kProductWaves + wave] = __builtin_popcountll(mine[k]);
+      }
+      wait_lds();
+      barrier();
+      const int32_t all = counts[lane], before = wave_scan(all) - all;
+#pragma unroll
+      for (int k = 0; k < kMaxPairs / kProductThreads; ++k)
+        if (id[k] == expert)
+          list[__builtin_amdgcn_readlane(before, k * kProductWaves + wave) + __builtin_popcountll(mine[k] & ((uint64_t{1} << lane) - 1))] =
+              static_cast<uint16_t>(threadIdx.x + k * kProductThreads);
+      wait_lds();
+      barrier();
+      listed = expert;
+    }
+      for (int32_t i = threadIdx.x; i < columns * a.nb * 16; i += kProductThreads) {
+        const int32_t c = i / (a.nb * 16), piece = i - c * (a.nb * 16), b = piece >> 4, h = (piece >> 2) & 3, j = piece & 3;
+        const int32_t pair = list[c0 + c];
+        const u32x4 v = *reinterpret_cast<const u32x4*>(a.act + static_cast<int64_t>(GATED ? pair / a.top_k : pair) * pitch + 8 * piece);
+        lds_put<u32x4>(base + L::act + (((b * 4 + j) * 4 + h) * columns + c) * 16, v);
+      }
+      if constexpr (!GATED)
+        for (int32_t i = threadIdx.x; i < a.nb * kTile; i += kProductThreads) {
+          const int32_t c = i & (kTile - 1);
+          inner[i] = c < columns ? a.act_scale[static_cast<int64_t>(list[c0 + c]) * a.nb + (i >> 4)] : 0.0f;
+        }
+      wait_lds();
+      barrier();
+      const uint32_t act = base + L::act + (h4 * columns + min(r, columns - 1)) * 16;
+
+      for (int32_t set = set0; set < set1; ++set) {
+        f32x4 acc[2] = {};
+        if (!idle(set)) {
+          uint32_t norm_at[2];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) norm_at[m] = my + L::norms + m * 256 + r * 16 + 2 * ((row_of(set, m, r) * a.nb) & 1);
+          for (int32_t chunk = 0; chunk < chunks; ++chunk) {
+            wait_staged();
+            RowCodes<BITS> code[2][kChunk];
+            float norm[2][kChunk];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int k = 0; k < kChunk; ++k) {
+#pragma unroll
+                for (int d = 0; d < BITS; ++d) set_word(code[m][k], d, lds_at<uint32_t>(place[k][d] + m * L::codes));
+                norm[m][k] = f16_value(lds_at<uint16_t>(norm_at[m] + 2 * k));
+              }
+            wait_lds();
+            if (chunk + 1 < chunks)
+              stage(set, chunk + 1);
+            else if (set + 1 < set1 && !idle(set + 1))
+              stage(set + 1, 0);
+            // Unit u: block u / 2, tile u % 2.  The look-ups of the next unit are under
+            // way while one is multiplied.
+            u32x4 x[2][4], w[2][4];
+            f32x4 scale[2];
+            const auto look = [&](int u) {
+              const int k = u >> 1;
+              if ((u & 1) == 0) {
+                const int32_t b = chunk * kChunk + k;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[k & 1][j] = lds_at<u32x4>(act + (b * 4 + j) * 64 * columns);
+                if constexpr (!GATED) scale[k & 1] = *reinterpret_cast<const f32x4*>(inner + b * kTile + 4 * h4);
+              }
+              decode<BITS>(code[u & 1][k], lds + L::book, copy, w[u & 1]);
+              __builtin_amdgcn_sched_barrier(0);
+            };
+            const auto multiply = [&](int u) {
+              const int k = u >> 1, m = u & 1;
+              f32x4 d = {0, 0, 0, 0};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x[k & 1][j]), __builtin_bit_cast(f16x8, w[m][j]), d, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[m][i] = __builtin_fmaf(d[i], GATED ? norm[m][k] : scale[k & 1][i] * norm[m][k], acc[m][i]);
+              __builtin_amdgcn_sched_barrier(0);
+            };
+            const int32_t there = min(a.nb - chunk * kChunk, kChunk);
+            if (there == kChunk) {
+              look(0);
+#pragma unroll
+              for (int u = 0; u < 2 * kChunk; ++u) {
+                if (u + 1 < 2 * kChunk) look(u + 1);
+                multiply(u);
+              }
+            } else {
+#pragma unroll
+              for (int u = 0; u < 2 * (kChunk - 1); ++u)
+                if (u < 2 * there) {
+                  look(u);
+                  multiply(u);
+                }
+            }
+          }
+        }
+        const int32_t out0 = (set * kProductWaves + wave) * (GATED ? kTile : 2 * kTile);
+        if constexpr (GATED) {
+          barrier();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int32_t c = 4 * h4 + i;
+            float v = 0;
+            if (c < columns && out0 + r < a.n_out) {
+              const int32_t pair = list[c0 + c];
+              const float s = a.act_scale[pair / a.top_k];
+              v = activate(acc[0][i] * s, a.activation) * (acc[1][i] * s) * a.weights[pair];
+            }
+            inner[c * kPitch + wave * kTile + r] = v;
+          }
+          wait_lds();
+          barrier();
+          for (int32_t c = wave; c < columns; c += kProductWaves) {
+            const float2 v = *reinterpret_cast<const float2*>(inner + c * kPitch + 2 * lane);
+            float y[2] = {v.x, v.y};
+            const float y0 = fabsf(y[0]) <= FLT_MAX ? fabsf(y[0]) : 0.0f, y1 = fabsf(y[1]) <= FLT_MAX ? fabsf(y[1]) : 0.0f;
+            const int e = scale_exponent(wave_max(fmaxf(y0, y1)));
+            const float f = __builtin_ldexpf(1.0f, 7 - e);
+            y[0] *= f;
+            y[1] *= f;
+            block_fwht(y, lane);
+            const int64_t to = static_cast<int64_t>(list[c0 + c]) * sets + set;
+            *reinterpret_cast<uint32_t*>(a.rotated + to * kBlock + 2 * lane) = pack_f16x2(y[0], y[1]);
+            if (lane == 0) a.rotated_scale[to] = __builtin_ldexpf(1.0f, e - 14);
+          }
+        } else {
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const int32_t o = out0 + m * kTile + r;
+            if (o >= a.n_out) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int32_t c = 4 * h4 + i;
+              if (c < columns) a.out[static_cast<int64_t>(list[c0 + c]) * a.n_out + o] = acc[m][i];
+            }
+          }
+        }
+      }
   }
 }
 
@@ -515,7 +813,7 @@ Parts parts_of(const Sizes& s) {
   p.x_scale = take(s.pass, 4);
   p.h = take(pairs * s.inner, 4);
   p.h_rotated = take(pairs * s.inner_blocks * kBlock, 2);
-  p.h_scale = take(pairs, 4);
+  p.h_scale = take(pairs * s.inner_blocks, 4);
   p.y = take(pairs * s.hidden, 4);
   p.total = at;
   return p;
@@ -531,6 +829,19 @@ int launch_product(const ProductArgs& a, hipStream_t stream) {
   if (a.nb <= 8) return go(hlwq_moe_product_kernel<BITS, 4, 2, GATED>, 2);
   if (a.nb <= 16) return go(hlwq_moe_product_kernel<BITS, 8, 2, GATED>, 1);
   return go(hlwq_moe_product_kernel<BITS, 8, 3, GATED>, 1);
+}
+
+// Whether the touched experts' sets of rows give the CUs work enough, and the
+// banks lie as the loads to LDS take them.
+bool streams(const hlwq_moe_banks& b, const Sizes& s, int64_t pairs) {
+  return s.inner_blocks <= kMaxInnerBlocks && s.hidden_blocks <= kActBytes / 256 && std::min(s.experts, pairs) * s.inner_blocks >= 128 &&
+         !misaligned(b.gate_up_packed, 16) && !misaligned(b.down_packed, 16) && !misaligned(b.gate_up_norms, 4) &&
+         !misaligned(b.down_norms, 4) && (s.hidden * s.inner_blocks) % 2 == 0;
+}
+template <int BITS, bool GATED>
+int launch_stream(ProductArgs a, hipStream_t stream) {
+  a.tiles = static_cast<int32_t>(ceil_div(a.n_out, GATED ? kBlock : 2 * kBlock));
+  return launch(hlwq_moe_stream_kernel<BITS, GATED>, dim3(kWorkgroups), dim3(kProductThreads), stream, a);
 }
 
 int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t tokens, const void* router, bool route, int64_t top_k,
@@ -588,8 +899,8 @@ int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t to
     pa.tokens = i32(n);
     pa.hidden = i32(s.hidden);
     pa.experts = i32(s.experts);
-    pa.expert_groups = i32(ceil_div(s.experts, kRouterExperts * kRouterWaves));
-    const int64_t router_groups = route ? pa.expert_groups * ceil_div(n, n == 1 ? 1 : kRouterTokens) : 0;
+    pa.expert_groups = i32(ceil_div(s.experts, router_experts(n) * kRouterWaves));
+    const int64_t router_groups = route ? pa.expert_groups * ceil_div(n, router_tokens(n)) : 0;
     if ((st = launch(hlwq_moe_prepare_kernel, dim3(static_cast<uint32_t>(n + router_groups)), dim3(kRotateThreads), stream, pa)) != HLWQ_OK)
       return st;
     if (route && m > 0) {
@@ -616,10 +927,16 @@ int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t to
       g.nb = i32(s.hidden_blocks);
       g.tiles = i32(ceil_div(s.inner, kTile));
       g.activation = b->activation;
-      if ((st = b->bits == 5 ? launch_product<5, true>(g, stream) : launch_product<3, true>(g, stream)) != HLWQ_OK) return st;
-      RotateArgs ra{g.out, my_ids, reinterpret_cast<uint16_t*>(at + parts.h_rotated), reinterpret_cast<float*>(at + parts.h_scale),
-                    i32(s.inner), i32(s.experts)};
-      if ((st = launch(hlwq_moe_rotate_kernel, dim3(static_cast<uint32_t>(m)), dim3(kRotateThreads), stream, ra)) != HLWQ_OK) return st;
+      g.rotated = reinterpret_cast<uint16_t*>(at + parts.h_rotated);
+      g.rotated_scale = reinterpret_cast<float*>(at + parts.h_scale);
+      const bool stream_banks = streams(*b, s, m);
+      if (stream_banks)
+        st = b->bits == 5 ? launch_stream<5, true>(g, stream) : launch_stream<3, true>(g, stream);
+      else
+        st = b->bits == 5 ? launch_product<5, true>(g, stream) : launch_product<3, true>(g, stream);
+      if (st != HLWQ_OK) return st;
+      RotateArgs ra{g.out, my_ids, g.rotated, g.rotated_scale, i32(s.inner), i32(s.experts)};
+      if (!stream_banks && (st = launch(hlwq_moe_rotate_kernel, dim3(static_cast<uint32_t>(m)), dim3(kRotateThreads), stream, ra)) != HLWQ_OK) return st;
       ProductArgs d = g;
       d.packed = static_cast<const uint8_t*>(b->down_packed);
       d.norms = static_cast<const uint16_t*>(b->down_norms);
@@ -630,7 +947,11 @@ int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t to
       d.rows = d.n_out = i32(s.hidden);
       d.nb = i32(s.inner_blocks);
       d.tiles = i32(ceil_div(s.hidden, 2 * kTile));
-      if ((st = b->bits == 5 ? launch_product<5, false>(d, stream) : launch_product<3, false>(d, stream)) != HLWQ_OK) return st;
+      if (stream_banks)
+        st = b->bits == 5 ? launch_stream<5, false>(d, stream) : launch_stream<3, false>(d, stream);
+      else
+        st = b->bits == 5 ? launch_product<5, false>(d, stream) : launch_product<3, false>(d, stream);
+      if (st != HLWQ_OK) return st;
     }
     JoinArgs ja{reinterpret_cast<const float*>(at + parts.y), my_ids, my_out, i32(s.hidden), i32(s.experts), empty ? 0 : i32(top_k)};
     const dim3 grid(static_cast<uint32_t>(ceil_div(s.hidden, 256)), static_cast<uint32_t>(n));

@@ -50,13 +50,6 @@ struct F16 {
   __device__ __forceinline__ static float value(uint16_t v) { return f16_value(v); }
 };
 
-__device__ __forceinline__ double lane_value(double v, int lane) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(u), lane);
-  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(u >> 32), lane);
-  return __builtin_bit_cast(double, lo | static_cast<uint64_t>(hi) << 32);
-}
-
 // A row's residual weights, (p - s q)+ or p without the refused tokens.
 template <class T>
 struct Residual {
