@@ -278,11 +278,6 @@ struct ProductArgs {
 };
 
 template <int BITS>
-struct PairBook {
-  static constexpr int kCount = 1 << (2 * BITS);
-};
-
-template <int BITS>
 struct RowCodes;
 template <>
 struct RowCodes<5> {
@@ -308,25 +303,73 @@ __device__ __forceinline__ void set_word(RowCodes<5>& c, int i, uint32_t v) {
 }
 __device__ __forceinline__ void set_word(RowCodes<3>& c, int i, uint32_t v) { c.a[i] = v; }
 
-constexpr int kBookShift = 1;  // 2^1 copies of the book, side by side
-
-// 32 codes to four operands of eight centroids: two codes, at a multiple of the
-// book's entry size, are where their pair of centroids lies (a shift, and one mask
-// with the lane's copy).
+// The book in LDS: pairs of centroids, looked up by two codes at once.  Of 3-bit
+// codes 64 of them, in 32 copies side by side, one for each bank; of 5-bit codes
+// 1024 in two copies, whose look-ups meet in the banks: 7.5 cycles of the CU each
+// (4.5 with sixteen copies, 64 KB; single codes, 32 values whose 16 words meet
+// never, under 3, but two of them and their packing take longer).
 template <int BITS>
-__device__ __forceinline__ void decode(const RowCodes<BITS>& c, const uint8_t* book, uint32_t copy, u32x4 (&w)[4]) {
-  constexpr int kTo = 2 + kBookShift;
-  constexpr uint32_t kMask = (PairBook<BITS>::kCount - 1) << kTo;
-#pragma unroll
-  for (int p = 0; p < 16; ++p) {
-    const int bit = 2 * BITS * p, at = bit >> 5, s = bit & 31;
-    uint32_t v = word_of(c, at);
-    if (s + 2 * BITS > 32)
-      v = __builtin_amdgcn_alignbit(word_of(c, at + 1), v, s - kTo);
-    else
-      v = s >= kTo ? v >> (s - kTo) : v << (kTo - s);
-    w[p >> 2][p & 3] = *reinterpret_cast<const uint32_t*>(book + ((v & kMask) | copy));
+struct Book {
+  static constexpr int kShift = BITS == 5 ? 1 : 5;  // 2^this copies
+  static constexpr uint32_t kBytes = (4u << (2 * BITS)) << kShift;
+  static constexpr int kTo = 2 + kShift;  // where a look-up's bits begin in an address
+  static constexpr uint32_t kMask = ((1u << (2 * BITS)) - 1) << kTo;
+};
+
+// The bits of a row's codes from `bit` on (at least `count` of them), from bit `to`
+// of the result on.
+template <int BITS>
+__device__ __forceinline__ uint32_t bits_at(const RowCodes<BITS>& c, int bit, int count, int to) {
+  const int at = bit >> 5, s = bit & 31;
+  if (s + count > 32) return __builtin_amdgcn_alignbit(word_of(c, at + 1), word_of(c, at), s - to);
+  return s >= to ? word_of(c, at) >> (s - to) : word_of(c, at) << (to - s);
+}
+
+// Four 5-bit codes, the low 20 bits of v, to four centroids without LDS: spread to
+// bytes, each the place k of its size among sixteen (k counted from the middle, so
+// downwards below it); the high and the low bytes of the fp16 sizes picked from two
+// eights each, and the sign put to the high ones.
+struct Sizes5 {
+  static constexpr float c[32] = HLWQ_CENTROIDS_5;
+  static constexpr uint32_t word(int first, int shift) {
+    uint32_t w = 0;
+    for (int i = 0; i < 4; ++i) w |= ((__builtin_bit_cast(uint16_t, static_cast<_Float16>(c[16 + first + i])) >> shift) & 0xffu) << (8 * i);
+    return w;
   }
+};
+__device__ __forceinline__ u32x2 four_centroids(uint32_t v) {
+  const uint32_t t = __builtin_amdgcn_bitop3_b32(v, v << 6, 0x3ffu, 0xE4);       // c ? a : b
+  const uint32_t k = __builtin_amdgcn_bitop3_b32(t, t << 3, 0x00ff00ffu, 0xE4);  // a code a byte, above it bits of others
+  const uint32_t upper = k & 0x10101010u;
+  const uint32_t size = __builtin_amdgcn_bitop3_b32(k, upper - (upper >> 4), 0x0f0f0f0fu, 0x82);  // ~(a ^ b) & c
+  const uint32_t in8 = size & 0x07070707u;
+  const uint32_t which = __builtin_amdgcn_bitop3_b32(size >> 1, 0x04040404u, 0x03020100u, 0xEA);  // (a & b) | c
+  uint32_t hi = __builtin_amdgcn_perm(__builtin_amdgcn_perm(Sizes5::word(12, 8), Sizes5::word(8, 8), in8),
+                                      __builtin_amdgcn_perm(Sizes5::word(4, 8), Sizes5::word(0, 8), in8), which);
+  const uint32_t lo = __builtin_amdgcn_perm(__builtin_amdgcn_perm(Sizes5::word(12, 0), Sizes5::word(8, 0), in8),
+                                            __builtin_amdgcn_perm(Sizes5::word(4, 0), Sizes5::word(0, 0), in8), which);
+  hi = __builtin_amdgcn_bitop3_b32(hi, upper << 3, 0x80808080u, 0xF2);  // a | (~b & c)
+  return u32x2{__builtin_amdgcn_perm(hi, lo, 0x05010400u), __builtin_amdgcn_perm(hi, lo, 0x07030602u)};
+}
+
+// 32 codes to four operands of eight centroids.
+template <int BITS, int WITHOUT = 0>
+__device__ __forceinline__ void decode(const RowCodes<BITS>& c, const uint8_t* book, uint32_t copy, u32x4 (&w)[4]) {
+  using K = Book<BITS>;
+#pragma unroll
+  for (int p = 2 * WITHOUT; p < 16; ++p)
+    w[p >> 2][p & 3] = *reinterpret_cast<const uint32_t*>(book + ((bits_at<BITS>(c, 2 * BITS * p, 2 * BITS, K::kTo) & K::kMask) | copy));
+#pragma unroll
+  for (int g = 0; g < WITHOUT; ++g) {
+    const u32x2 v = four_centroids(bits_at<BITS>(c, 4 * BITS * g, 4 * BITS, 0));
+    w[g >> 1][2 * (g & 1)] = v[0];
+    w[g >> 1][2 * (g & 1) + 1] = v[1];
+  }
+}
+
+template <int BITS>
+__device__ __forceinline__ uint32_t book_copy(int lane) {
+  return (lane & ((1 << Book<BITS>::kShift) - 1)) * 4;
 }
 
 __device__ __forceinline__ float sigmoid_times(float g, float z) { return g / (1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * z)); }
@@ -336,12 +379,13 @@ __device__ __forceinline__ float activate(float g, int32_t kind) {
 }
 
 template <int BITS>
-__device__ __forceinline__ void fill_book(uint32_t* book) {
+__device__ __forceinline__ void fill_book(uint8_t* book) {
   constexpr float c5[32] = HLWQ_CENTROIDS_5;
   constexpr float c3[8] = HLWQ_CENTROIDS_3;
-  for (int i = threadIdx.x; i < PairBook<BITS>::kCount << kBookShift; i += kProductThreads) {
-    const int p = i >> kBookShift, lo = p & ((1 << BITS) - 1), hi = p >> BITS;
-    book[i] = BITS == 5 ? pack_f16x2(c5[lo], c5[hi]) : pack_f16x2(c3[lo & 7], c3[hi & 7]);
+#pragma unroll
+  for (uint32_t i = 0; i < Book<BITS>::kBytes / 4 / kProductThreads; ++i) {
+    const uint32_t at = i * kProductThreads + threadIdx.x, p = at >> Book<BITS>::kShift;
+    reinterpret_cast<uint32_t*>(book)[at] = BITS == 5 ? pack_f16x2(c5[p & 31], c5[p >> 5]) : pack_f16x2(c3[p & 7], c3[p >> 3 & 7]);
   }
 }
 
@@ -383,7 +427,7 @@ template <int BITS, int KS, int BW, bool GATED>
 __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const ProductArgs a) {
   constexpr int kGroups = kProductWaves / KS;  // of waves, a tile each
   constexpr int kPitch = 20;                   // floats to a pair's sums of a tile
-  __shared__ uint32_t book[PairBook<BITS>::kCount << kBookShift];
+  __shared__ __attribute__((aligned(16))) uint8_t book[Book<BITS>::kBytes];
   __shared__ int32_t list[kMaxPairs];
   __shared__ uint32_t named[kMaxExperts / 32];
   __shared__ int32_t count_of;
@@ -397,7 +441,7 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
 
   const int r = lane & 15, h4 = lane >> 4;
   const int ks = wave % KS, group = wave / KS;
-  const uint32_t copy = (lane & ((1 << kBookShift) - 1)) * 4;
+  const uint32_t copy = book_copy<BITS>(lane);
   const uint8_t* packed = a.packed + static_cast<int64_t>(expert) * a.rows * a.nb * (16 * BITS);
   const uint16_t* norms = a.norms + static_cast<int64_t>(expert) * a.rows * a.nb;
   const int32_t pitch = a.nb * kBlock;
@@ -435,7 +479,7 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
                 u32x4 w[4];
-                decode<BITS>(codes[k][m], reinterpret_cast<const uint8_t*>(book), copy, w);
+                decode<BITS>(codes[k][m], book, copy, w);
                 f32x4 d = {0, 0, 0, 0};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -491,15 +535,20 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
 // two for each block (act_scale [.][nb]).
 // ---------------------------------------------------------------------------
 
+__device__ __forceinline__ int32_t quotient(int32_t a, int32_t b) {
+  return static_cast<int32_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
 constexpr int kWorkgroups = 256;
 constexpr int kMaxInnerBlocks = 64;  // whose scales a workgroup keeps
 constexpr int kActBytes = 48 << 10;  // of activations in LDS
 constexpr int kChunk = 4;            // blocks that are staged together
+constexpr int kWithoutBook = 1;      // fours of 32 5-bit codes whose centroids come from registers
 
 template <int BITS>
 struct StreamLds {
   static constexpr uint32_t codes = 1024 * BITS, norms = 2 * codes, wave = norms + 2 * 256;  // of a wave: two tiles' codes, their norms
-  static constexpr uint32_t book = 0, stage = (PairBook<BITS>::kCount << kBookShift) * 4, act = stage + kProductWaves * wave,
+  static constexpr uint32_t book = 0, stage = Book<BITS>::kBytes, act = stage + kProductWaves * wave,
                             inner = act + kActBytes, list = inner + kTile * (kBlock + 4) * 4, bytes = list + kMaxPairs * 2;
 };
 
@@ -508,7 +557,7 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
   using L = StreamLds<BITS>;
   constexpr int kPitch = kBlock + 4;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[L::bytes];
-  __shared__ uint32_t named[kMaxExperts / 2];  // pairs of two experts
+  __shared__ __attribute__((aligned(16))) uint32_t named[kMaxExperts / 2];  // pairs of two experts
   __shared__ int32_t counts[64];
   static_assert(kMaxPairs == 64 * 64, "a count for each wave's ballot");
   static_assert(kMaxInnerBlocks * kTile <= kTile * kPitch, "scales lie where inner values do");
@@ -517,7 +566,7 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
   float* const inner = reinterpret_cast<float*>(lds + L::inner);
   uint16_t* const list = reinterpret_cast<uint16_t*>(lds + L::list);
   const int r = lane & 15, h4 = lane >> 4;
-  const uint32_t copy = (lane & ((1 << kBookShift) - 1)) * 4;
+  const uint32_t copy = book_copy<BITS>(lane);
 
   const int32_t sets = a.tiles;  // of 128 or 256 rows
   const int32_t capacity = min(kTile, kActBytes / (a.nb * 256));
@@ -525,26 +574,36 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
   // The experts' pairs, and this workgroup's run of (expert, pass over as many of
   // its pairs as fit, set): passes cost the same whatever their pairs.
   static_assert(kMaxExperts == 64 * 16 && kMaxPairs < 0x10000, "sixteen experts a lane, two counts a word");
-  for (int i = threadIdx.x; i < kMaxExperts / 2; i += kProductThreads) named[i] = 0;
-  __syncthreads();
   int32_t id[kMaxPairs / kProductThreads];
 #pragma unroll
   for (int k = 0; k < kMaxPairs / kProductThreads; ++k) {
     const int32_t p = threadIdx.x + k * kProductThreads;
     id[k] = p < a.pairs ? a.ids[p] : -1;
+  }
+  for (int i = threadIdx.x; i < kMaxExperts / 2; i += kProductThreads) named[i] = 0;
+  fill_book<BITS>(lds + L::book);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kMaxPairs / kProductThreads; ++k) {
     if (id[k] >= a.experts) id[k] = -1;
     if (id[k] >= 0) atomicAdd(&named[id[k] >> 1], 1u << 16 * (id[k] & 1));
   }
-  fill_book<BITS>(reinterpret_cast<uint32_t*>(lds + L::book));
   __syncthreads();
-  const auto count_at = [&](int32_t e) { return static_cast<int32_t>(named[e >> 1] >> 16 * (e & 1) & 0xffff); };
-  const auto passes_at = [&](int32_t e) { return (count_at(e) + capacity - 1) / capacity; };
+  const float per_pass = 1.0f / capacity;
+  // (counts are small: the quotient's error stays under the half that is added)
+  const auto passes_of = [&](uint32_t count) { return static_cast<int32_t>((count + (capacity - 0.5f)) * per_pass); };
+  const auto count_at = [&](int32_t e) { return named[e >> 1] >> 16 * (e & 1) & 0xffffu; };
   int32_t own = 0;
-  for (int i = 0; i < 16; ++i) own += passes_at(16 * lane + i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t both = named[8 * lane + i];
+    own += passes_of(both & 0xffffu) + passes_of(both >> 16);
+  }
   const int32_t upto = wave_scan(own);
-  const int64_t total = static_cast<int64_t>(__builtin_amdgcn_readlane(upto, 63)) * sets;
-  int32_t q = static_cast<int32_t>(total * blockIdx.x / gridDim.x);
-  const int32_t q_end = static_cast<int32_t>(total * (blockIdx.x + 1) / gridDim.x);
+  const uint64_t total = static_cast<uint64_t>(__builtin_amdgcn_readlane(upto, 63)) * static_cast<uint32_t>(sets);
+  static_assert(kWorkgroups == 256, "");
+  int32_t q = static_cast<int32_t>(total * blockIdx.x >> 8);
+  const int32_t q_end = static_cast<int32_t>(total * (blockIdx.x + 1) >> 8);
 
   const uint32_t row_bytes = a.nb * (16 * BITS);
   const int32_t chunks = static_cast<int32_t>(ceil_div(a.nb, kChunk)), pitch = a.nb * kBlock;
@@ -569,10 +628,10 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
     q += set1 - set0;
     const int at = __builtin_ctzll(__ballot(upto > slot));
     const int32_t rest = slot - __builtin_amdgcn_readlane(upto - own, at);
-    const int32_t its = lane < 16 ? passes_at(16 * at + lane) : 0, its_upto = wave_scan(its);
+    const int32_t its = lane < 16 ? passes_of(count_at(16 * at + lane)) : 0, its_upto = wave_scan(its);
     const int within = __builtin_ctzll(__ballot(its_upto > rest));
     const int32_t expert = 16 * at + within, c0 = (rest - __builtin_amdgcn_readlane(its_upto - its, within)) * capacity;
-    const int32_t columns = min(capacity, count_at(expert) - c0);
+    const int32_t columns = min(capacity, static_cast<int32_t>(count_at(expert)) - c0);
     const int64_t first = static_cast<int64_t>(expert) * a.rows * a.nb, blocks = static_cast<int64_t>(a.rows) * a.nb;
     const u32x4 codes = buffer_of(a.packed + first * (16 * BITS), blocks * (16 * BITS)), norms = buffer_of(a.norms + first, 2 * blocks);
     const auto stage = [&](int32_t set, int32_t chunk) {
@@ -609,12 +668,22 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
       barrier();
       listed = expert;
     }
-      for (int32_t i = threadIdx.x; i < columns * a.nb * 16; i += kProductThreads) {
-        const int32_t c = i / (a.nb * 16), piece = i - c * (a.nb * 16), b = piece >> 4, h = (piece >> 2) & 3, j = piece & 3;
-        const int32_t pair = list[c0 + c];
-        const u32x4 v = *reinterpret_cast<const u32x4*>(a.act + static_cast<int64_t>(GATED ? pair / a.top_k : pair) * pitch + 8 * piece);
-        lds_put<u32x4>(base + L::act + (((b * 4 + j) * 4 + h) * columns + c) * 16, v);
+      for (int32_t c = wave; c < columns; c += kProductWaves) {
+        const int32_t pair = __builtin_amdgcn_readfirstlane(list[c0 + c]);
+        const uint16_t* from = a.act + static_cast<int64_t>(GATED ? quotient(pair, a.top_k) : pair) * pitch;
+        for (int32_t piece = lane; piece < a.nb * 16; piece += 64) {
+          const int32_t at_j = (piece & ~15) + (piece & 3) * 4 + (piece >> 2 & 3);  // pieces of 16 bytes: block, h4, j to block, j, h4
+          lds_put<u32x4>(base + L::act + (at_j * columns + c) * 16, *reinterpret_cast<const u32x4*>(from + 8 * piece));
+        }
       }
+      float pair_scale[4], pair_weight[4];  // of the lane's four
+      if constexpr (GATED)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t pair = list[c0 + min(4 * h4 + i, columns - 1)];
+          pair_scale[i] = a.act_scale[quotient(pair, a.top_k)];
+          pair_weight[i] = a.weights[pair];
+        }
       if constexpr (!GATED)
         for (int32_t i = threadIdx.x; i < a.nb * kTile; i += kProductThreads) {
           const int32_t c = i & (kTile - 1);
@@ -659,7 +728,7 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
                 for (int j = 0; j < 4; ++j) x[k & 1][j] = lds_at<u32x4>(act + (b * 4 + j) * 64 * columns);
                 if constexpr (!GATED) scale[k & 1] = *reinterpret_cast<const f32x4*>(inner + b * kTile + 4 * h4);
               }
-              decode<BITS>(code[u & 1][k], lds + L::book, copy, w[u & 1]);
+              decode<BITS, BITS == 5 ? kWithoutBook : 0>(code[u & 1][k], lds + L::book, copy, w[u & 1]);
               __builtin_amdgcn_sched_barrier(0);
             };
             const auto multiply = [&](int u) {
@@ -697,11 +766,8 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
           for (int i = 0; i < 4; ++i) {
             const int32_t c = 4 * h4 + i;
             float v = 0;
-            if (c < columns && out0 + r < a.n_out) {
-              const int32_t pair = list[c0 + c];
-              const float s = a.act_scale[pair / a.top_k];
-              v = activate(acc[0][i] * s, a.activation) * (acc[1][i] * s) * a.weights[pair];
-            }
+            if (c < columns && out0 + r < a.n_out)
+              v = activate(acc[0][i] * pair_scale[i], a.activation) * (acc[1][i] * pair_scale[i]) * pair_weight[i];
             inner[c * kPitch + wave * kTile + r] = v;
           }
           wait_lds();
