@@ -19,6 +19,10 @@ constexpr int64_t kMaxExperts = 1024, kMaxTopK = 32, kMaxSize = 1 << 20, kMaxTok
 constexpr int kMaxPairs = 4096;  // (token, expert) pairs of one pass over the banks
 constexpr int kTile = 16;        // rows of a matrix, and pairs, to a product
 
+__device__ __forceinline__ int32_t quotient(int32_t a, int32_t b) {
+  return static_cast<int32_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const f16x2 v = {static_cast<_Float16>(lo), static_cast<_Float16>(hi)};
   return __builtin_bit_cast(uint32_t, v);
@@ -89,6 +93,7 @@ struct PrepareArgs {
   uint16_t* rotated;       // [tokens][nb * 128]
   float* scale;            // [tokens]
   int32_t tokens, hidden, experts, expert_groups;
+  int32_t rotating;  // workgroups that rotate: one a token, or none
 };
 
 // Router logits of some experts and tokens a wave, lanes along the row, eight
@@ -145,14 +150,14 @@ __host__ __device__ inline int router_tokens(int64_t tokens) { return tokens == 
 
 // The first workgroups rotate a token each, the others take the router's.
 __global__ void __launch_bounds__(kRotateThreads) hlwq_moe_prepare_kernel(const PrepareArgs a) {
-  if (static_cast<int32_t>(blockIdx.x) < a.tokens) {
+  if (static_cast<int32_t>(blockIdx.x) < a.rotating) {
     const int32_t t = blockIdx.x;
     const uint16_t* row = a.x + t * a.x_stride;
     const int64_t pitch = ceil_div(a.hidden, kBlock) * kBlock;
     rotate_row([row](int32_t i) { return bf16_lo(row[i]); }, a.hidden, a.rotated + t * pitch, a.scale + t);
     return;
   }
-  const int32_t w = blockIdx.x - a.tokens;
+  const int32_t w = blockIdx.x - a.rotating;
   const int32_t e0 = (w % a.expert_groups * kRouterWaves + (threadIdx.x >> 6)) * router_experts(a.tokens);
   if (e0 >= a.experts) return;
   if (a.tokens == 1)
@@ -182,15 +187,75 @@ __device__ __forceinline__ double value_of(uint64_t key) {
   if (key == 1) return __builtin_nan("");
   return __builtin_bit_cast(double, key >> 63 ? key & ~(uint64_t{1} << 63) : ~key);
 }
+// The largest of the wave's, in every lane (running maxima towards the last lane).
 __device__ __forceinline__ uint32_t top_of_wave(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = max(v, lane_xor(v, d));
-  return v;
+  const auto step = [&](int from) { return static_cast<uint32_t>(from); };
+  v = max(v, step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x111, 0xF, 0xF, false)));
+  v = max(v, step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x112, 0xF, 0xF, false)));
+  v = max(v, step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x114, 0xF, 0xF, false)));
+  v = max(v, step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x118, 0xF, 0xF, false)));
+  v = max(v, step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x142, 0xA, 0xF, false)));
+  v = max(v, step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x143, 0xC, 0xF, false)));
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
 }
-__device__ __forceinline__ uint64_t top_of_wave(uint64_t v) {
-  const uint32_t hi = top_of_wave(static_cast<uint32_t>(v >> 32));
-  const uint32_t lo = top_of_wave(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
-  return static_cast<uint64_t>(hi) << 32 | lo;
+
+// A wave finds a token's best: lane j < top_k gets the j-th.
+struct Chosen {
+  int32_t id;
+  float weight;
+};
+template <int PER>
+__device__ __forceinline__ Chosen choose(const double* __restrict__ row, int32_t experts, int32_t top_k, bool renormalize) {
+  const int lane = threadIdx.x & 63;
+  uint64_t key[PER], left[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    key[k] = lane + 64 * k < experts ? order_of(row[lane + 64 * k]) : 0;
+    left[k] = key[k];
+  }
+  uint64_t mine = 0;
+  int32_t id = 0;
+  for (int32_t j = 0; j < top_k; ++j) {
+    uint64_t best = left[0];
+    int32_t at = 0;
+#pragma unroll
+    for (int k = 1; k < PER; ++k) {
+      at = left[k] > best ? k : at;
+      best = max(best, left[k]);
+    }
+    const uint32_t hi = static_cast<uint32_t>(best >> 32);
+    const uint32_t top = top_of_wave(hi);
+    uint64_t who = __ballot(hi == top);
+    int32_t lowest = 64 * at + lane;
+    if (who & (who - 1)) {  // several: by their lower halves, then by index
+      const uint32_t lo = hi == top ? static_cast<uint32_t>(best) : 0;
+      const uint32_t low_top = top_of_wave(lo);
+      who = __ballot(hi == top && lo == low_top);
+      lowest = static_cast<int32_t>(~top_of_wave(who >> lane & 1 ? ~static_cast<uint32_t>(lowest) : 0u));
+    } else {
+      lowest = __builtin_amdgcn_readlane(lowest, __builtin_ctzll(who));
+    }
+    const int from = lowest & 63;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) left[k] = lane == from && k == lowest >> 6 ? 0 : left[k];
+    const uint64_t b = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(hi), from))) << 32 |
+                       static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(best)), from));
+    if (lane == j) {
+      mine = b;
+      id = lowest;
+    }
+  }
+  const double top = lane_value(value_of(mine), 0);
+  const double w = lane < top_k ? exp(value_of(mine) - top) : 0.0;
+  double total = w;
+  if (!renormalize) {
+    total = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (key[k]) total += exp(value_of(key[k]) - top);
+  }
+  total = wave_sum(total);
+  return Chosen{id, static_cast<float>(w / total)};
 }
 
 constexpr int kTopThreads = 256;
@@ -199,51 +264,11 @@ __global__ void __launch_bounds__(kTopThreads) hlwq_moe_top_kernel(const TopArgs
   const int lane = threadIdx.x & 63;
   const int32_t t = blockIdx.x * (kTopThreads / 64) + (threadIdx.x >> 6);
   if (t >= a.tokens) return;
-  const double* row = a.logits + static_cast<int64_t>(t) * a.experts;
-  uint64_t key[PER];
-#pragma unroll
-  for (int k = 0; k < PER; ++k) key[k] = lane + 64 * k < a.experts ? order_of(row[lane + 64 * k]) : 0;
-  uint64_t all = 0;  // lane j: the j-th best's key
-  int32_t chosen = 0;
-  uint64_t left[PER];
-#pragma unroll
-  for (int k = 0; k < PER; ++k) left[k] = key[k];
-  for (int32_t j = 0; j < a.top_k; ++j) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) best = max(best, left[k]);
-    best = top_of_wave(best);
-    // of equal ones the lowest index: the lowest k, then the lowest lane
-    int32_t at = 0;
-    bool found = false;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const uint64_t has = __ballot(left[k] == best);
-      if (!found && has) {
-        at = 64 * k + __builtin_ctzll(has);
-        found = true;
-        if (lane == (at & 63)) left[k] = 0;
-      }
-    }
-    if (lane == j) {
-      all = best;
-      chosen = at;
-    }
-  }
-  const double top = lane_value(value_of(all), 0);
-  const double w = lane < a.top_k ? exp(value_of(all) - top) : 0.0;
-  double total = w;
-  if (!a.renormalize) {
-    total = 0;
-#pragma unroll
-    for (int k = 0; k < PER; ++k)
-      if (key[k]) total += exp(value_of(key[k]) - top);
-  }
-  total = wave_sum(total);
+  const Chosen c = choose<PER>(a.logits + static_cast<int64_t>(t) * a.experts, a.experts, a.top_k, a.renormalize);
   if (lane < a.top_k) {
     const int64_t p = static_cast<int64_t>(t) * a.top_k + lane;
-    a.ids[p] = chosen;
-    a.weights[p] = static_cast<float>(w / total);
+    a.ids[p] = c.id;
+    a.weights[p] = c.weight;
   }
 }
 
@@ -535,10 +560,6 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
 // two for each block (act_scale [.][nb]).
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ int32_t quotient(int32_t a, int32_t b) {
-  return static_cast<int32_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
-}
-
 constexpr int kWorkgroups = 256;
 constexpr int kMaxInnerBlocks = 64;  // whose scales a workgroup keeps
 constexpr int kActBytes = 48 << 10;  // of activations in LDS
@@ -802,6 +823,190 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
 }
 
 // ---------------------------------------------------------------------------
+// The same for a few pairs, where what counts is how many kernels follow each
+// other and what each waits for: the first finds its token's experts by itself
+// (every workgroup again, from the logits) and rotates its activations while it
+// does, the second rotates the inner values and joins a token's pairs.  A
+// workgroup takes sixteen rows; its waves split the blocks of one pair, or the
+// pairs.  All sixteen rows of the activations' operand are the same pair's.
+// ---------------------------------------------------------------------------
+
+constexpr int kFewPairs = 32, kFewBlocks = 64;
+
+struct FewArgs {
+  ProductArgs p;
+  const uint16_t* x;
+  int64_t x_stride;
+  const double* logits;  // null: the routing is known
+  int32_t* ids;
+  float* weights;
+  float* h;       // [pairs][inner]
+  uint16_t* out;  // [tokens][hidden]
+  int32_t hidden, inner, renormalize, tokens;
+};
+
+// A block of values v[2 l], v[2 l + 1] rotated to LDS as fp16 over a power of two,
+// which is returned (with the blocks' 1 / 128).
+__device__ __forceinline__ float rotate_block(float (&v)[2], uint16_t* to, int lane) {
+  const float a = fabsf(v[0]) <= FLT_MAX ? fabsf(v[0]) : 0.0f, b = fabsf(v[1]) <= FLT_MAX ? fabsf(v[1]) : 0.0f;
+  const int e = scale_exponent(wave_max(fmaxf(a, b)));
+  const float f = __builtin_ldexpf(1.0f, 7 - e);
+  v[0] *= f;
+  v[1] *= f;
+  block_fwht(v, lane);
+  *reinterpret_cast<uint32_t*>(to + 2 * lane) = pack_f16x2(v[0], v[1]);
+  return __builtin_ldexpf(1.0f, e - 14);
+}
+
+// A block's products of a row tile with the activations at `act`: lane r has row r's.
+template <int BITS>
+__device__ __forceinline__ float few_product(const RowCodes<BITS>& c, const uint8_t* book, uint32_t copy, const uint16_t* act) {
+  u32x4 w[4];
+  decode<BITS>(c, book, copy, w);
+  f32x4 d = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    d = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const f16x8*>(act + 8 * j), __builtin_bit_cast(f16x8, w[j]), d, 0, 0, 0);
+  return d[0];
+}
+
+template <int BITS, int PER>
+__global__ void __launch_bounds__(kProductThreads) hlwq_moe_few_up_kernel(const FewArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t book[Book<BITS>::kBytes];
+  __shared__ __attribute__((aligned(16))) uint16_t act[kFewBlocks * kBlock];
+  __shared__ float scales[kFewBlocks];
+  __shared__ Chosen chosen;
+  __shared__ float sums[kProductWaves][2][kTile];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, h4 = lane >> 4;
+  const int32_t pair = blockIdx.y, t = quotient(pair, a.p.top_k), j = pair - t * a.p.top_k;
+  if (a.logits) {
+    if (wave == kProductWaves - 1) {
+      const Chosen c = choose<PER>(a.logits + static_cast<int64_t>(t) * a.p.experts, a.p.experts, a.p.top_k, a.renormalize);
+      if (lane == j) chosen = c;
+      if (blockIdx.x == 0 && j == 0 && lane < a.p.top_k) {
+        a.ids[pair + lane] = c.id;
+        a.weights[pair + lane] = c.weight;
+      }
+    }
+  } else if (threadIdx.x == 0) {
+    chosen = Chosen{a.ids[pair], a.weights[pair]};
+  }
+  fill_book<BITS>(book);
+  const uint16_t* x = a.x + t * a.x_stride;
+  for (int32_t b = wave; b < a.p.nb; b += kProductWaves) {
+    const int32_t i = b * kBlock + 2 * lane;
+    float v[2] = {i < a.hidden ? bf16_lo(x[i]) : 0.0f, i + 1 < a.hidden ? bf16_lo(x[i + 1]) : 0.0f};
+    const float scale = rotate_block(v, act + b * kBlock, lane);
+    if (lane == 0) scales[b] = scale;
+  }
+  __syncthreads();
+  const Chosen c = chosen;
+  const int32_t expert = __builtin_amdgcn_readfirstlane(c.id);
+  if (expert < 0 || expert >= a.p.experts) return;
+  const int32_t out0 = blockIdx.x * kTile;
+  const uint32_t copy = book_copy<BITS>(lane);
+  const uint8_t* codes[2];
+  const uint16_t* norms[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const int64_t at = (static_cast<int64_t>(expert) * a.p.rows + min(out0 + r + m * a.p.n_out, a.p.rows - 1)) * a.p.nb;
+    codes[m] = a.p.packed + at * (16 * BITS) + 4 * BITS * h4;
+    norms[m] = a.p.norms + at;
+  }
+  float acc[2] = {0, 0};
+  constexpr int kAhead = 3;  // blocks whose codes are under way together
+  for (int32_t b0 = wave; b0 < a.p.nb; b0 += kAhead * kProductWaves) {
+    RowCodes<BITS> code[kAhead][2];
+    float norm[kAhead][2];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int32_t b = b0 + k * kProductWaves;
+      if (b >= a.p.nb) break;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        load_row(code[k][m], codes[m] + b * (16 * BITS));
+        norm[k][m] = f16_value(norms[m][b]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int32_t b = b0 + k * kProductWaves;
+      if (b >= a.p.nb) break;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        acc[m] = __builtin_fmaf(few_product<BITS>(code[k][m], book, copy, act + b * kBlock + 32 * h4), norm[k][m] * scales[b], acc[m]);
+    }
+  }
+  if (lane < kTile) {
+    sums[wave][0][lane] = acc[0];
+    sums[wave][1][lane] = acc[1];
+  }
+  __syncthreads();
+  if (threadIdx.x < kTile && out0 + static_cast<int32_t>(threadIdx.x) < a.p.n_out) {
+    float s[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < kProductWaves; ++k)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) s[m] += sums[k][m][threadIdx.x];
+    a.h[static_cast<int64_t>(pair) * a.inner + out0 + threadIdx.x] = activate(s[0], a.p.activation) * s[1] * c.weight;
+  }
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kProductThreads) hlwq_moe_few_down_kernel(const FewArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t book[Book<BITS>::kBytes];
+  __shared__ __attribute__((aligned(16))) uint16_t act[kProductWaves][kChunk * kBlock];
+  __shared__ float sums[kFewPairs][kTile];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, h4 = lane >> 4;
+  const int32_t out0 = blockIdx.x * kTile;
+  const uint32_t copy = book_copy<BITS>(lane);
+  fill_book<BITS>(book);
+  __syncthreads();
+  for (int32_t pair = wave; pair < a.p.pairs; pair += kProductWaves) {
+    const int32_t expert = a.ids[pair];
+    float acc = 0;
+    if (expert >= 0 && expert < a.p.experts) {
+      const int64_t at = (static_cast<int64_t>(expert) * a.p.rows + min(out0 + r, a.p.rows - 1)) * a.p.nb;
+      const uint8_t* codes = a.p.packed + at * (16 * BITS) + 4 * BITS * h4;
+      const uint16_t* norms = a.p.norms + at;
+      const float* h = a.h + static_cast<int64_t>(pair) * a.inner;
+      for (int32_t b0 = 0; b0 < a.p.nb; b0 += kChunk) {
+        RowCodes<BITS> code[kChunk];
+        float norm[kChunk], v[kChunk][2], scale[kChunk];
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) {
+          const int32_t b = b0 + k, i = b * kBlock + 2 * lane;
+          if (b >= a.p.nb) break;
+          load_row(code[k], codes + b * (16 * BITS));
+          norm[k] = f16_value(norms[b]);
+          v[k][0] = i < a.inner ? h[i] : 0.0f;
+          v[k][1] = i + 1 < a.inner ? h[i + 1] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k)
+          if (b0 + k < a.p.nb) scale[k] = rotate_block(v[k], act[wave] + k * kBlock, lane);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k)
+          if (b0 + k < a.p.nb)
+            acc = __builtin_fmaf(few_product<BITS>(code[k], book, copy, act[wave] + k * kBlock + 32 * h4), norm[k] * scale[k], acc);
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+    if (lane < kTile) sums[pair][lane] = acc;
+  }
+  __syncthreads();
+  const int32_t t = threadIdx.x / kTile, row = threadIdx.x % kTile;
+  if (t < a.tokens && out0 + row < a.hidden) {
+    float s = 0;
+    for (int32_t j = 0; j < a.p.top_k; ++j) s += sums[t * a.p.top_k + j][row];
+    a.out[static_cast<int64_t>(t) * a.hidden + out0 + row] = static_cast<uint16_t>(pack_bf16x2(s, 0));
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Between the two: a pair's inner activations rotated; after them: a token's
 // pairs joined.
 // ---------------------------------------------------------------------------
@@ -897,6 +1102,21 @@ int launch_product(const ProductArgs& a, hipStream_t stream) {
   return go(hlwq_moe_product_kernel<BITS, 8, 3, GATED>, 1);
 }
 
+// Whether the pairs are few enough for the two kernels that do the most by themselves.
+bool few(const Sizes& s, int64_t pairs) {
+  return pairs <= kFewPairs && s.hidden_blocks <= kFewBlocks && s.inner_blocks <= kFewBlocks;
+}
+template <int BITS>
+int launch_few(const FewArgs& up, const ProductArgs& down, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(ceil_div(up.inner, kTile)), static_cast<uint32_t>(up.p.pairs));
+  const int st = up.p.experts <= 256 ? launch(hlwq_moe_few_up_kernel<BITS, 4>, grid, dim3(kProductThreads), stream, up)
+                                     : launch(hlwq_moe_few_up_kernel<BITS, 16>, grid, dim3(kProductThreads), stream, up);
+  if (st != HLWQ_OK) return st;
+  FewArgs a = up;
+  a.p = down;
+  return launch(hlwq_moe_few_down_kernel<BITS>, dim3(static_cast<uint32_t>(ceil_div(up.hidden, kTile))), dim3(kProductThreads), stream, a);
+}
+
 // Whether the touched experts' sets of rows give the CUs work enough, and the
 // banks lie as the loads to LDS take them.
 bool streams(const hlwq_moe_banks& b, const Sizes& s, int64_t pairs) {
@@ -958,7 +1178,7 @@ int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t to
     PrepareArgs pa{};
     pa.x = static_cast<const uint16_t*>(x) + t0 * x_stride;
     pa.x_stride = x_stride;
-    pa.router = route ? static_cast<const uint16_t*>(router) : nullptr;
+    pa.router = static_cast<const uint16_t*>(router);
     pa.logits = reinterpret_cast<double*>(at + parts.logits);
     pa.rotated = reinterpret_cast<uint16_t*>(at + parts.x);
     pa.scale = reinterpret_cast<float*>(at + parts.x_scale);
@@ -966,10 +1186,13 @@ int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t to
     pa.hidden = i32(s.hidden);
     pa.experts = i32(s.experts);
     pa.expert_groups = i32(ceil_div(s.experts, router_experts(n) * kRouterWaves));
-    const int64_t router_groups = route ? pa.expert_groups * ceil_div(n, router_tokens(n)) : 0;
-    if ((st = launch(hlwq_moe_prepare_kernel, dim3(static_cast<uint32_t>(n + router_groups)), dim3(kRotateThreads), stream, pa)) != HLWQ_OK)
+    const bool is_few = !empty && few(s, m);
+    pa.rotating = empty || is_few ? 0 : i32(n);
+    const int64_t preparing = pa.rotating + (route && m > 0 ? pa.expert_groups * ceil_div(n, router_tokens(n)) : 0);
+    if (preparing > 0 &&
+        (st = launch(hlwq_moe_prepare_kernel, dim3(static_cast<uint32_t>(preparing)), dim3(kRotateThreads), stream, pa)) != HLWQ_OK)
       return st;
-    if (route && m > 0) {
+    if (route && m > 0 && !is_few) {
       TopArgs ta{pa.logits, my_ids, my_weights, i32(n), i32(s.experts), i32(top_k), renormalize != 0};
       const dim3 grid(static_cast<uint32_t>(ceil_div(n, kTopThreads / 64)));
       st = s.experts <= 256 ? launch(hlwq_moe_top_kernel<4>, grid, dim3(kTopThreads), stream, ta)
@@ -985,6 +1208,8 @@ int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t to
       g.ids = my_ids;
       g.weights = my_weights;
       g.out = reinterpret_cast<float*>(at + parts.h);
+      g.rotated = reinterpret_cast<uint16_t*>(at + parts.h_rotated);
+      g.rotated_scale = reinterpret_cast<float*>(at + parts.h_scale);
       g.pairs = i32(m);
       g.experts = i32(s.experts);
       g.top_k = i32(top_k);
@@ -993,26 +1218,31 @@ int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t to
       g.nb = i32(s.hidden_blocks);
       g.tiles = i32(ceil_div(s.inner, kTile));
       g.activation = b->activation;
-      g.rotated = reinterpret_cast<uint16_t*>(at + parts.h_rotated);
-      g.rotated_scale = reinterpret_cast<float*>(at + parts.h_scale);
+      ProductArgs d = g;
+      d.packed = static_cast<const uint8_t*>(b->down_packed);
+      d.norms = static_cast<const uint16_t*>(b->down_norms);
+      d.act = g.rotated;
+      d.act_scale = g.rotated_scale;
+      d.weights = nullptr;
+      d.out = reinterpret_cast<float*>(at + parts.y);
+      d.rows = d.n_out = i32(s.hidden);
+      d.nb = i32(s.inner_blocks);
+      d.tiles = i32(ceil_div(s.hidden, 2 * kTile));
+      if (is_few) {
+        const FewArgs f{g, pa.x, x_stride, route ? pa.logits : nullptr, my_ids, my_weights, g.out, my_out, i32(s.hidden), i32(s.inner),
+                        renormalize != 0, i32(n)};
+        if ((st = b->bits == 5 ? launch_few<5>(f, d, stream) : launch_few<3>(f, d, stream)) != HLWQ_OK) return st;
+        continue;
+      }
       const bool stream_banks = streams(*b, s, m);
       if (stream_banks)
         st = b->bits == 5 ? launch_stream<5, true>(g, stream) : launch_stream<3, true>(g, stream);
       else
         st = b->bits == 5 ? launch_product<5, true>(g, stream) : launch_product<3, true>(g, stream);
       if (st != HLWQ_OK) return st;
-      RotateArgs ra{g.out, my_ids, g.rotated, g.rotated_scale, i32(s.inner), i32(s.experts)};
-      if (!stream_banks && (st = launch(hlwq_moe_rotate_kernel, dim3(static_cast<uint32_t>(m)), dim3(kRotateThreads), stream, ra)) != HLWQ_OK) return st;
-      ProductArgs d = g;
-      d.packed = static_cast<const uint8_t*>(b->down_packed);
-      d.norms = static_cast<const uint16_t*>(b->down_norms);
-      d.act = ra.rotated;
-      d.act_scale = ra.scale;
-      d.weights = nullptr;
-      d.out = reinterpret_cast<float*>(at + parts.y);
-      d.rows = d.n_out = i32(s.hidden);
-      d.nb = i32(s.inner_blocks);
-      d.tiles = i32(ceil_div(s.hidden, 2 * kTile));
+      const RotateArgs ra{g.out, my_ids, g.rotated, g.rotated_scale, i32(s.inner), i32(s.experts)};
+      if (!stream_banks && (st = launch(hlwq_moe_rotate_kernel, dim3(static_cast<uint32_t>(m)), dim3(kRotateThreads), stream, ra)) != HLWQ_OK)
+        return st;
       if (stream_banks)
         st = b->bits == 5 ? launch_stream<5, false>(d, stream) : launch_stream<3, false>(d, stream);
       else
