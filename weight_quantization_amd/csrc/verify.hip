@@ -50,23 +50,15 @@ struct F16 {
   __device__ __forceinline__ static float value(uint16_t v) { return f16_value(v); }
 };
 
-// A row's residual weights, (p - s q)+ or p without the refused tokens.
-template <class T>
+// A row's residual weights: with DRAFT (p - s q)+, without p but for the refused
+// tokens.
+template <class T, bool DRAFT>
 struct Residual {
   const typename T::type* p;
-  const typename T::type* q;  // null: none, or s = 0
-  double s;
+  const typename T::type* q;
+  double s;                // 0: of p alone
   const int32_t* refused;  // in LDS
   int32_t n_refused;
-  __device__ __forceinline__ double weight(float pv, float qv) const {
-    const double v = q ? pv - s * qv : static_cast<double>(pv);
-    return v > 0 ? v : 0.0;
-  }
-  __device__ __forceinline__ double at(int32_t i) const {
-    for (int32_t k = 0; k < n_refused; ++k)
-      if (refused[k] == i) return 0;
-    return weight(T::value(p[i]), q ? T::value(q[i]) : 0.0f);
-  }
 };
 
 template <class T>
@@ -74,45 +66,73 @@ struct Wide {
   typedef typename T::type type __attribute__((ext_vector_type(T::kWide), aligned(sizeof(typename T::type))));
 };
 
-// A lane's sum of weights of [lo, hi), over the wave's share of it.
-template <class T>
-__device__ __forceinline__ double lane_sum(const Residual<T>& r, int32_t lo, int32_t hi, int lane) {
+// A lane's sum of weights of [lo, hi), over the wave's share of it, W values to a
+// load.  Sixteen waves keep enough loads on their way; several to a wave make the
+// code longer, and most of it runs once: four took 25 us for 250 rows of 100003
+// bf16 where one takes 19.
+template <class T, bool DRAFT>
+__device__ __forceinline__ double lane_sum(const Residual<T, DRAFT>& r, int32_t lo, int32_t hi, int lane) {
   typedef typename Wide<T>::type wide;
   constexpr int W = T::kWide;
   double sum = 0;
   const int32_t whole = lo + (hi - lo) / W * W;
-  for (int32_t i = lo + lane * W; i < whole; i += 64 * W) {
-    const wide p = *reinterpret_cast<const wide*>(r.p + i);
-    wide q{};
-    if (r.q) q = *reinterpret_cast<const wide*>(r.q + i);
-    uint64_t out = 0;
-    for (int32_t k = 0; k < r.n_refused; ++k) out |= static_cast<uint32_t>(r.refused[k] - i) < W ? 1ull << (r.refused[k] - i) : 0;
+  const auto over = [&](auto weight, bool both) {
+#pragma clang loop unroll(disable)
+    for (int32_t i = lo + lane * W; i < whole; i += 64 * W) {
+      const wide p = *reinterpret_cast<const wide*>(r.p + i);
+      wide q{};
+      if (both) q = *reinterpret_cast<const wide*>(r.q + i);
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      const double v = r.weight(T::value(p[j]), T::value(q[j]));
-      sum += out >> j & 1 ? 0.0 : v;
+      for (int j = 0; j < W; ++j) sum += weight(i + j, T::value(p[j]), T::value(q[j]));
     }
+    for (int32_t i = whole + lane; i < hi; i += 64) sum += weight(i, T::value(r.p[i]), both ? T::value(r.q[i]) : 0.0f);
+  };
+  const auto alone = [](int32_t, float p, float) { return static_cast<double>(fmaxf(p, 0.0f)); };
+  if constexpr (DRAFT) {
+    if (r.s == 0)
+      over(alone, false);
+    else if (r.s == 1)
+      over([](int32_t, float p, float q) { return fmax(static_cast<double>(p) - static_cast<double>(q), 0.0); }, true);
+    else
+      over([s = r.s](int32_t, float p, float q) { return fmax(p - s * q, 0.0); }, true);
+  } else {
+    // the refused tokens that lie here: none in most waves' shares
+    int32_t here[2] = {-1, -1}, some = 0;
+    for (int32_t k = 0; k < r.n_refused; ++k) {
+      const int32_t x = __builtin_amdgcn_readfirstlane(r.refused[k]);
+      if (x < lo || x >= hi) continue;
+      if (some < 2) (some ? here[1] : here[0]) = x;
+      ++some;
+    }
+    if (some == 0)
+      over(alone, false);
+    else if (some <= 2)
+      over([here](int32_t i, float p, float) { return i == here[0] || i == here[1] ? 0.0 : static_cast<double>(fmaxf(p, 0.0f)); }, false);
+    else
+      over([&](int32_t i, float p, float) {
+        for (int32_t k = 0; k < r.n_refused; ++k) p = r.refused[k] == i ? 0.0f : p;
+        return static_cast<double>(fmaxf(p, 0.0f));
+      }, false);
   }
-  for (int32_t i = whole + lane; i < hi; i += 64) sum += r.at(i);
   return sum;
 }
 
-// The range k of `parts` equal ones of [lo, hi), multiples of `unit` long.
+// The range k of sixteen equal ones of [lo, hi), multiples of `unit` long.
 struct Range {
   int32_t lo, hi;
 };
-__device__ __forceinline__ Range part_of(Range a, int32_t k, int32_t parts, int32_t unit) {
-  const int64_t size = ceil_div(ceil_div(a.hi - a.lo, parts), unit) * unit;
+__device__ __forceinline__ Range part_of(Range a, int32_t k, int32_t unit) {
+  const int32_t size = static_cast<int32_t>(ceil_div(a.hi - a.lo, kVerifyWaves * unit)) * unit;
   Range r;
-  r.lo = static_cast<int32_t>(min(a.lo + k * size, static_cast<int64_t>(a.hi)));
-  r.hi = static_cast<int32_t>(min(r.lo + size, static_cast<int64_t>(a.hi)));
+  r.lo = min(a.lo + k * size, a.hi);  // (2^24 and a part more)
+  r.hi = min(r.lo + size, a.hi);
   return r;
 }
 
-// Sums of the sixteen parts of a range, one a wave, in LDS.
-template <class T>
-__device__ __forceinline__ double part_sums(const Residual<T>& r, Range all, double* lds, int lane, int wave) {
-  const Range mine = part_of(all, wave, kVerifyWaves, 64 * T::kWide);
+// Sums of the sixteen parts of a range, one a wave, in LDS; returns their sum.
+template <class T, bool DRAFT>
+__device__ __forceinline__ double part_sums(const Residual<T, DRAFT>& r, Range all, int32_t unit, double* lds, int lane, int wave) {
+  const Range mine = part_of(all, wave, unit);
   const double s = wave_sum(lane_sum(r, mine.lo, mine.hi, lane));
   __syncthreads();
   if (lane == 0) lds[wave] = s;
@@ -128,12 +148,14 @@ __device__ __forceinline__ double part_sums(const Residual<T>& r, Range all, dou
 __device__ __forceinline__ int32_t find_part(const double* lds, double& rest) {
   int32_t last = -1;
   double before = 0, last_before = 0;
+  bool passed = false;
+#pragma unroll
   for (int k = 0; k < kVerifyWaves; ++k) {
     const double v = lds[k];
-    if (v > 0) {
+    if (!passed && v > 0) {
       last = k;
       last_before = before;
-      if (before + v > rest) break;
+      passed = before + v > rest;
     }
     before += v;
   }
@@ -141,30 +163,24 @@ __device__ __forceinline__ int32_t find_part(const double* lds, double& rest) {
   return last;
 }
 
-// The lowest index at which the running sum of the weights passes u times their
-// total; -1 if they have none.  `total` and the sums of the row's parts, in LDS,
-// are known.
-template <class T>
-__device__ __forceinline__ int32_t sample(const Residual<T>& r, Range all, double rest, double* lds, int lane, int wave) {
-  // the part, a part of that, and in it by lanes
-  const int32_t k = find_part(lds, rest);
-  if (k < 0) return -1;
-  all = part_of(all, k, kVerifyWaves, 64 * T::kWide);
-  {
-    const Range mine = part_of(all, wave, kVerifyWaves, 64);
-    double s = 0;
-    for (int32_t i = mine.lo + lane; i < mine.hi; i += 64) s += r.at(i);
-    s = wave_sum(s);
-    __syncthreads();
-    if (lane == 0) lds[wave] = s;
-    __syncthreads();
+constexpr int32_t kPartUnit = 512;  // of the first parts, a multiple of what a wave loads at once
+
+// The lowest index at which the running sum of the weights passes `rest`; -1 if they
+// have none.  The sums of the row's sixteen parts, in LDS, are known: the part that
+// holds it, a sixteenth of that, and so on down to 64 values, a lane each.
+template <class T, bool DRAFT>
+__device__ __forceinline__ int32_t sample(const Residual<T, DRAFT>& r, Range all, double rest, double* lds, int lane, int wave) {
+  int32_t unit = kPartUnit;
+  for (;;) {
+    const int32_t k = find_part(lds, rest);
+    if (k < 0) return -1;
+    all = part_of(all, k, unit);
+    if (all.hi - all.lo <= 64) break;
+    unit = 64;
+    part_sums(r, all, unit, lds, lane, wave);
   }
-  const int32_t m = find_part(lds, rest);
-  if (m < 0) return -1;
-  all = part_of(all, m, kVerifyWaves, 64);
-  const Range mine = part_of(all, lane, 64, 1);
-  double own = 0;
-  for (int32_t i = mine.lo; i < mine.hi; ++i) own += r.at(i);
+  const int32_t i = all.lo + lane;
+  const double own = lane_sum(r, i, min(i + 1, all.hi), 0);
   double upto = own;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -173,23 +189,10 @@ __device__ __forceinline__ int32_t sample(const Residual<T>& r, Range all, doubl
   }
   const uint64_t any = __ballot(own > 0), past = __ballot(own > 0 && upto > rest);
   if (!any) return -1;
-  const int at = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(any);
-  rest -= lane_value(upto - own, at);
-  const Range last = part_of(all, at, 64, 1);
-  int32_t found = -1;
-  double sum = 0;
-  for (int32_t i = last.lo; i < last.hi; ++i) {
-    const double v = r.at(i);
-    sum += v;
-    if (v > 0) {
-      found = i;
-      if (sum > rest) break;
-    }
-  }
-  return found;
+  return all.lo + (past ? __builtin_ctzll(past) : 63 - __builtin_clzll(any));
 }
 
-template <class T>
+template <class T, bool DRAFT>
 __global__ void __launch_bounds__(kVerifyThreads) hlwq_verify_kernel(const VerifyArgs a) {
   typedef typename T::type type;
   __shared__ double sums[kVerifyWaves];
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kVerifyThreads) hlwq_verify_kernel(const Verif
   int32_t cur = 0, n_kept = 1, n_refused = 0;
   double mass = 1, taken = 0;
   bool summed = false;  // `sums` holds the parts' sums of the present residual
-  const auto residual = [&] { return Residual<T>{p_row(cur), draft && taken > 0 ? q_row(cur) : nullptr, taken, refused, n_refused}; };
+  const auto residual = [&] { return Residual<T, DRAFT>{p_row(cur), DRAFT ? q_row(cur) : nullptr, taken, refused, n_refused}; };
   if (threadIdx.x == 0) kept[0] = 0;
   for (int32_t base = 0; base < count; base += 64) {
     __syncthreads();
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kVerifyThreads) hlwq_verify_kernel(const Verif
         if (parent >= node || token < 0 || token >= a.vocab) parent = -1;
         if (parent >= 0) {
           p = T::value(p_row(parent)[token]);
-          q = draft ? T::value(q_row(parent)[token]) : 1.0f;
+          q = DRAFT ? T::value(q_row(parent)[token]) : 1.0f;
         }
       }
       node_parent[lane] = parent;
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(kVerifyThreads) hlwq_verify_kernel(const Verif
       const int32_t token = node_token[at];
       const double u = node_u[at], p = node_p[at], q = node_q[at];
       double value = p;
-      if (draft)
+      if constexpr (DRAFT)
         value = p - taken * q;
       else
         for (int32_t k = 0; k < n_refused; ++k) value = refused[k] == token ? 0.0 : value;
@@ -266,9 +269,9 @@ __global__ void __launch_bounds__(kVerifyThreads) hlwq_verify_kernel(const Verif
         taken = 0;
         n_refused = 0;
         summed = false;
-      } else if (draft) {
+      } else if (DRAFT) {
         taken += mass;
-        mass = part_sums(residual(), all, sums, lane, wave);
+        mass = part_sums(residual(), all, kPartUnit, sums, lane, wave);
         summed = true;
       } else {
         mass -= value > 0 ? value : 0.0;
@@ -280,12 +283,12 @@ __global__ void __launch_bounds__(kVerifyThreads) hlwq_verify_kernel(const Verif
     }
   }
 
-  Residual<T> r = residual();
-  double total = summed ? mass : part_sums(r, all, sums, lane, wave);
+  Residual<T, DRAFT> r = residual();
+  double total = summed ? mass : part_sums(r, all, kPartUnit, sums, lane, wave);
   if (!(total > 0)) {  // nothing left of p: p itself
-    r.q = nullptr;
+    r.s = 0;
     r.n_refused = 0;
-    total = part_sums(r, all, sums, lane, wave);
+    total = part_sums(r, all, kPartUnit, sums, lane, wave);
   }
   const int32_t next = sample(r, all, a.next_uniforms[b] * total, sums, lane, wave);
   if (threadIdx.x == 0) {
@@ -347,9 +350,12 @@ int run_verify(const hlwq_drafts* d, hipStream_t stream) {
   a.rows = static_cast<int32_t>(d->rows);
   a.vocab = static_cast<int32_t>(d->vocab);
   const dim3 grid(static_cast<uint32_t>(d->requests));
-  if (d->dtype == HLWQ_F32) return launch(hlwq_verify_kernel<F32>, grid, dim3(kVerifyThreads), stream, a);
-  if (d->dtype == HLWQ_BF16) return launch(hlwq_verify_kernel<Bf16>, grid, dim3(kVerifyThreads), stream, a);
-  return launch(hlwq_verify_kernel<F16>, grid, dim3(kVerifyThreads), stream, a);
+  const auto go = [&](auto type) {
+    using T = decltype(type);
+    return d->draft ? launch(hlwq_verify_kernel<T, true>, grid, dim3(kVerifyThreads), stream, a)
+                    : launch(hlwq_verify_kernel<T, false>, grid, dim3(kVerifyThreads), stream, a);
+  };
+  return d->dtype == HLWQ_F32 ? go(F32{}) : d->dtype == HLWQ_BF16 ? go(Bf16{}) : go(F16{});
 }
 
 }  // namespace
