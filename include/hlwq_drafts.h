@@ -41,7 +41,9 @@ extern "C" {
  * g = q_heads / kv_heads, T = kv_heads * min(rows * g / 16 + requests, rows * g).
  * HLWQ_ERR_LIMIT where T reaches 2^20, or T * max_pages * page_size / 128 reaches
  * 2^31.  `workspace`: hlwq_kv_tree_attention_workspace bytes, about 17 MB and 33
- * KB for each of the T tiles. */
+ * KB for each of the T tiles; where requests have 48 rows of a KV head and more on
+ * average (tiles of 64 rows, if the table is wide as well), up to 34 MB, 132 KB for
+ * each of those tiles and 516 bytes for each row and query head. */
 enum { HLWQ_TREE_NODES = 8192 };
 int hlwq_kv_tree_attention(const hlwq_kv_cache* cache, const void* q_bf16, int64_t q_stride, int64_t q_heads,
                            const void* k_new_bf16, int64_t k_stride, const void* v_new_bf16, int64_t v_stride,

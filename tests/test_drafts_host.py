@@ -59,8 +59,10 @@ def test_tree_workspace():
     w = wq.hlwq_kv_tree_attention_workspace
     tile = 2 * 16 * 258 * 4
     assert w(64, 64, 24, 4) == (512 + (64 * 6 // 16 + 64) * 4) * tile
-    # all rows are in tiles of sixteen, however many there are
-    assert w(1, 4096, 24, 4) == (512 + (4096 * 6 // 16 + 1) * 4) * tile
+    # many rows to a request: room for tiles of 64 too, whichever is more
+    assert w(1, 4096, 24, 4) == (256 + (4096 * 6 // 64 + 1) * 4) * 4 * tile + 4096 * 24 * 516
+    assert w(1, 31, 24, 4) == (512 + 12 * 4) * tile  # 186 rows of a KV head
+    assert w(4, 31, 24, 4) == (512 + (31 * 6 // 16 + 4) * 4) * tile
     assert w(1, 1, 24, 4) == 512 * tile  # four tiles' workgroups have places among the 512
     for bad in ((0, 5, 24, 4), (-1, 5, 24, 4), (1, 0, 24, 4), (1, 5, 23, 4), (1, 5, 24, 0), (2 ** 20 + 1, 5, 24, 4),
                 (1, 2 ** 27, 24, 4), (2 ** 20, 2 ** 20, 1, 1)):

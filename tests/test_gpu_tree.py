@@ -42,9 +42,9 @@ def check_tree(got, q, keys, values, held, parents, nodes, scale=1 / 16):
 
 
 def tree_case(wq, seed, ctx, new, q_heads, kv_heads, bits=3, page=64, residual=128, ring=128, wide=3, scale=1 / 16, extra=0,
-              pad=0, parents=None, sigma=1.0):
+              pad=0, parents=None, sigma=1.0, width=None):
     rng = np.random.default_rng(seed)
-    c = Cache(rng, ctx, kv_heads, bits, page, residual, ring)
+    c = Cache(rng, ctx, kv_heads, bits, page, residual, ring, width=width)
     n = sum(new) + pad
     q, kv = bf16_bits(rng, n, q_heads, D, sigma=sigma), [bf16_bits(rng, n, kv_heads, D) for _ in range(2)]
     cu = np.concatenate([[0], np.cumsum(new)])
@@ -220,6 +220,108 @@ def test_capture_and_replay(wq):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+# Tiles of 64 rows: tables of 4000 tokens and more, 192 rows of a KV head and 48 a request.
+def wide_case(wq, seed, ctx, new, q_heads, kv_heads, bits=3, page=64, **kw):
+    rows = (sum(new) + kw.get("pad", 0)) * q_heads // kv_heads
+    assert rows >= max(192, 48 * len(new))
+    tree_case(wq, seed, ctx, new, q_heads, kv_heads, bits, page, width=max(4096 // page, (max(ctx) + page - 1) // page), **kw)
+
+
+@pytest.mark.parametrize("ctx,new", [
+    ([0], [192]), ([1], [33]), ([128], [35]), ([129], [40]), ([500], [64]), ([2049], [44]), ([5000], [64]), ([9000], [33]),
+    ([0, 1, 15, 128, 129, 144, 145, 192, 193, 1000, 3000], [1, 2, 3, 4, 5, 60, 7, 8, 16, 17, 18]), ([1000, 30], [40, 0]),
+    ([4000, 0, 999], [33, 1, 0]), ([96, 97, 127], [32, 31, 33]), ([4096, 4097, 6000, 65], [10, 11, 43, 1]),
+])
+@pytest.mark.parametrize("q_heads,kv_heads,bits,page", [(24, 4, 3, 64), (12, 2, 2, 16)])
+def test_wide_lengths(wq, ctx, new, q_heads, kv_heads, bits, page):
+    wide_case(wq, sum(ctx) + len(new), ctx, new, q_heads, kv_heads, bits, page)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,new", [(1, 1, [200, 30]), (8, 8, [100, 92]), (8, 1, [9, 21]), (20, 4, [9, 31]), (17, 1, [9, 5])])
+@pytest.mark.parametrize("bits", [3, 2])
+def test_wide_heads(wq, q_heads, kv_heads, new, bits):
+    wide_case(wq, q_heads, [333, 40], new, q_heads, kv_heads, bits, 32, wide=5)
+
+
+@pytest.mark.parametrize("residual,ring", [(0, 0), (1, 1), (37, 37), (64, 100), (128, 1000)])
+@pytest.mark.parametrize("bits,page,new", [(3, 16, [1, 50, 13]), (2, 256, [50, 10, 6])])
+def test_wide_windows(wq, residual, ring, bits, page, new):
+    wide_case(wq, residual + page, [residual + 50, 700, 20], new, 6, 2, bits, page, residual=residual, ring=ring)
+
+
+@pytest.mark.parametrize("extra,pad", [(0, 5), (8, 0), (40, 30)])
+def test_wide_strides_and_padding(wq, extra, pad):
+    wide_case(wq, extra, [300, 3], [42, 27], 6, 2, extra=extra, pad=pad)
+
+
+@pytest.mark.parametrize("scale,sigma", [(0.0, 1.0), (-1 / 16, 1.0), (1.0, 1.0), (1 / 16, 8.0)])
+def test_wide_scales(wq, scale, sigma):
+    wide_case(wq, 3, [300], [70], 6, 2, scale=scale, sigma=sigma)
+
+
+@pytest.mark.parametrize("new,wide", [([1100, 257], 1), ([300], 1000)])
+def test_wide_large_trees(wq, new, wide):
+    wide_case(wq, wide, [200] * len(new), new, 2, 1, wide=wide)
+
+
+def test_wide_rows_left_alone_and_replayed(wq):
+    """Rows of a request of too many nodes, outputs on two streams at once, and a captured call."""
+    rng = np.random.default_rng(12)
+    ctx, new = [40, 300, 4100], [8193, 3, 50]
+    c = Cache(rng, ctx, 1, 3, 64, 128, 128)
+    n = sum(new)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q, kv = bf16_bits(rng, n, 1, D), [bf16_bits(rng, n, 1, D) for _ in range(2)]
+    parents = np.concatenate([np.arange(-1, 8192), trees(rng, new[1:], 3)])
+    t = [dev16(q), dev16(kv[0]), dev16(kv[1]), i32(parents), i32(cu), i32([x + m for x, m in zip(ctx, new)]), i32(c.table), *c.tensors()]
+    size = wq.hlwq_kv_tree_attention_workspace(3, n, 1, 1)
+    ws = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+    outs = [torch.full((n, 1, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i, s in enumerate(streams):
+        wq.hlwq_kv_tree_attention(*t, out=outs[i], workspace=ws[:size] if i == 0 else None, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(*outs) and bool((ws[size:] == 255).all())
+    got = outs[0].cpu().double().numpy()
+    assert np.all(got[:8193] == 7)
+    for b in (1, 2):
+        r = slice(cu[b], cu[b + 1])
+        check_tree(got[r], f64(q[r]), *sides(c, b, ctx[b], [x[r] for x in kv]), ctx[b], parents[r], range(0, new[b], 5))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = wq.hlwq_kv_tree_attention(*t, out=torch.full_like(outs[0], 7.0), workspace=ws)
+    for _ in range(3):
+        t[0].copy_(dev16(bf16_bits(rng, n, 1, D)))
+        want = wq.hlwq_kv_tree_attention(*t, out=outs[1])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_wide_nan_and_infinities_stay_with_the_rows_that_see_them(wq):
+    rng = np.random.default_rng(13)
+    new, ctx = [70, 30], [300, 20]
+    n = sum(new)
+    c = Cache(rng, ctx, 2, 3, 64, 128, 128, width=64)
+    q, kv = bf16_bits(rng, n, 4, D), [bf16_bits(rng, n, 2, D) for _ in range(2)]
+    parents = trees(rng, new, 4)
+    rest = (i32(parents), i32([0, new[0], n]), i32([t + m for t, m in zip(ctx, new)]), i32(c.table), *c.tensors())
+    clean = wq.hlwq_kv_tree_attention(dev16(q), dev16(kv[0]), dev16(kv[1]), *rest)
+    ways = [way(parents[:new[0]], i) for i in range(new[0])]
+    bad = max(range(1, new[0]), key=lambda x: sum(x in w for w in ways) % (new[0] - 1))
+    rows = [i for i in range(new[0]) if bad in ways[i]]
+    assert 1 < len(rows) < new[0] - 1
+    for i, what in ((0, 0x7FC0), (1, 0x7FC0), (1, 0x7F80)):
+        dirty = [x.copy() for x in kv]
+        dirty[i][bad, 1, 17] = what
+        got = wq.hlwq_kv_tree_attention(dev16(q), dev16(dirty[0]), dev16(dirty[1]), *rest)
+        hit = torch.zeros(n, 4, D, dtype=torch.bool, device="cuda")
+        hit[rows, 2:, slice(None) if i == 0 else 17] = True
+        assert torch.equal(got[~hit], clean[~hit]), (i, hex(what))
+        assert not torch.isfinite(got[hit]).any()
 
 
 def test_steps_of_drafted_tokens(wq):

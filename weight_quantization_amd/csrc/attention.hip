@@ -2,6 +2,7 @@
 // prompts (include/hlwq_attention.h).
 
 #include "attention_chunk.h"
+#include "attention_wide.h"
 
 #include <cmath>
 
@@ -69,13 +70,14 @@ int launch_prompt(const AttnArgs& a, hipStream_t stream) {
 // over 4000 in one of 32 slots 121 (105 alone).
 constexpr int64_t few_rows(int64_t requests) { return requests == 1 ? 256 : 64; }
 // Workgroups that the device holds at once: two to a CU of the split kernel
-// (256 registers a work-item), one of the chunk kernel.
-constexpr int64_t kSplitResident = 512, kChunkWorkers = 256;
+// (256 registers a work-item), one of the wide and of the chunk kernel (LDS).
+constexpr int64_t kSplitResident = 512, kWideResident = 256, kChunkWorkers = 256;
 struct PagedPlan {
   bool split, chunk;      // which kernels are called
+  bool wide;              // the split kernel's tiles are the wide one's
   int64_t split_tiles, split_workers;
   int64_t split_slots;    // of partial sums
-  size_t split_bytes, chunk_bytes;  // of workspace, each its own
+  size_t split_bytes, chunk_bytes, rotated_bytes;  // of workspace, each its own
 };
 // Sizes of the split kernel's part for its tiles.
 void size_split(PagedPlan& p) {
@@ -86,9 +88,10 @@ void size_split(PagedPlan& p) {
   // bits, 4000 tokens a request, us), with places kept and without: 4 requests
   // 19.8 and 22.5, 8 26.4 and 25.3, 16 35.8 and 33.6, 64 87 and 74, 128 183
   // and 154.
-  p.split_workers = kSplitResident - (p.split_tiles < kSplitResident / 16 ? p.split_tiles : 0);
+  const int64_t resident = p.wide ? kWideResident : kSplitResident;
+  p.split_workers = resident - (p.split_tiles < resident / (p.wide ? 4 : 16) ? p.split_tiles : 0);
   p.split_slots = 2 * (p.split_workers + p.split_tiles);
-  p.split_bytes = partial_floats(p.split_slots, kSplitRows) * sizeof(float);
+  p.split_bytes = partial_floats(p.split_slots, p.wide ? kWideRows : kSplitRows) * sizeof(float);
 }
 PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
   PagedPlan p{};
@@ -106,26 +109,41 @@ PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv
   return p;
 }
 
-// A call whose rows are trees: all the split kernel's.  (The chunk kernel would
-// unpack each code once for 256 rows instead of sixteen, but trees of so many
-// rows are not drafted.)
-PagedPlan tree_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads) {
+// A call whose rows are trees: the split kernel's, with tiles of sixteen rows, or
+// the wide one's, with 64, which unpacks each code once for all of them but takes
+// one more launch and starts later.  The host goes by the mean, as above, and by
+// the table's width.  Measured (3 bits, 24 query and 4 KV heads, us, split and
+// wide): one request with 32767 tokens and 22 rows (132 of a KV head) 80 and 86,
+// 32 rows 97 and 89, 64 rows 169 and 154; with 4000 tokens 32 rows 37 and 37, 64
+// rows 48 and 43; with 500 64 rows 27 and 39; sixteen requests of 4000 tokens, 6
+// rows each (36) 68 and 71, 9 rows 84 and 76, 33 rows 222 and 196.
+bool many_rows(int64_t requests, int64_t rows, int64_t group) { return rows * group >= std::max<int64_t>(48 * requests, 192); }
+constexpr int64_t kWideTokens = 4000;
+PagedPlan tree_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads, bool wide) {
   PagedPlan p{};
+  const int64_t group = q_heads / kv_heads;
   p.split = true;
-  p.split_tiles = tiles_of(requests, rows, q_heads / kv_heads, kv_heads, kSplitRows);
+  p.wide = wide;
+  p.split_tiles = tiles_of(requests, rows, group, kv_heads, p.wide ? kWideRows : kSplitRows);
   size_split(p);
+  if (p.wide) p.rotated_bytes = static_cast<size_t>(rows * q_heads) * (kRotatedRow + sizeof(float));
   return p;
 }
 
-// Tiles of the split kernel's launches: sixteen workgroups of 256 to a tile in
-// its join, 2^32 - 1 work-items to a launch.
+// Tiles of these launches: sixteen workgroups of 256 to a tile in the joins, 2^32 -
+// 1 work-items to a launch.
 constexpr int64_t kMaxSplitTiles = 0xffffff / kSplitRows;
+static_assert(kWideRows / kWideJoinRows == kSplitRows, "as many for both");
 
 size_t workspace_bytes_of(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads, bool tree) {
   bool nothing;
   if (requests <= 0 || requests > kMaxRequests || check_heads(rows, q_heads, kv_heads, &nothing) != HLWQ_OK || nothing) return 0;
-  const PagedPlan p = (tree ? tree_plan : paged_plan)(requests, rows, q_heads, kv_heads);
-  return p.split_tiles > kMaxSplitTiles ? 0 : p.split_bytes + p.chunk_bytes;
+  const PagedPlan p = tree ? tree_plan(requests, rows, q_heads, kv_heads, false) : paged_plan(requests, rows, q_heads, kv_heads);
+  if (p.split_tiles > kMaxSplitTiles) return 0;
+  const size_t bytes = p.split_bytes + p.chunk_bytes;
+  if (!tree || !many_rows(requests, rows, q_heads / kv_heads)) return bytes;
+  const PagedPlan w = tree_plan(requests, rows, q_heads, kv_heads, true);  // which of both depends on the table
+  return std::max(bytes, w.split_bytes + w.rotated_bytes);
 }
 
 template <int BITS, bool TREE>
@@ -133,6 +151,16 @@ int launch_split(const AttnArgs& a, int64_t tiles, hipStream_t stream) {
   const int st = launch(hlwq_split_attention_kernel<BITS, TREE>, dim3(static_cast<uint32_t>(a.workers + tiles)), dim3(kSplitThreads), stream, a);
   if (st != HLWQ_OK) return st;
   return launch(hlwq_split_join_kernel, dim3(static_cast<uint32_t>(tiles * kSplitRows)), dim3(kSplitThreads), stream, a);
+}
+
+template <int BITS>
+int launch_wide(const AttnArgs& a, int64_t tiles, hipStream_t stream) {
+  const int64_t groups = ceil_div(static_cast<int64_t>(a.rows) * a.q_heads, 4);
+  int st = launch(hlwq_rotate_queries_kernel<BITS>, dim3(static_cast<uint32_t>(groups)), dim3(256), stream, a);
+  if (st != HLWQ_OK) return st;
+  st = launch(hlwq_wide_attention_kernel<BITS>, dim3(static_cast<uint32_t>(a.workers + tiles)), dim3(kWideThreads), stream, a);
+  if (st != HLWQ_OK) return st;
+  return launch(hlwq_wide_join_kernel, dim3(static_cast<uint32_t>(tiles * (kWideRows / kWideJoinRows))), dim3(64 * kWideJoinRows), stream, a);
 }
 
 // The shift that keeps the sum of the costs of tiles of m rows and blocks of kt
@@ -160,6 +188,9 @@ int launch_paged(int bits, AttnArgs a, const PagedPlan& p, void* ws, hipStream_t
     if (p.chunk) a.most = few;
     if (a.parents) {
       a.most = static_cast<int32_t>(std::min<int64_t>(int64_t{HLWQ_TREE_NODES} * a.group, 0x7fffffff));
+      a.rotated = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + p.split_bytes);
+      a.rotated_factor = reinterpret_cast<float*>(a.rotated + static_cast<int64_t>(a.rows) * a.q_heads * (kRotatedRow / 2));
+      if (p.wide) return bits == 3 ? launch_wide<3>(a, p.split_tiles, stream) : launch_wide<2>(a, p.split_tiles, stream);
       return bits == 3 ? launch_split<3, true>(a, p.split_tiles, stream) : launch_split<2, true>(a, p.split_tiles, stream);
     }
     const int st = bits == 3 ? launch_split<3, false>(a, p.split_tiles, stream) : launch_split<2, false>(a, p.split_tiles, stream);
@@ -198,11 +229,13 @@ int run_paged(const hlwq_kv_cache* c, const void* q, int64_t q_stride, int64_t q
       (st = check_rows(k, k_stride, rows, c->kv_heads, &ke)) != HLWQ_OK ||
       (st = check_rows(v, v_stride, rows, c->kv_heads, &ve)) != HLWQ_OK)
     return st;
-  const PagedPlan plan = (tree ? tree_plan : paged_plan)(c->requests, rows, q_heads, c->kv_heads);
+  const bool wide = tree && many_rows(c->requests, rows, q_heads / c->kv_heads) && max_pages * c->page_size >= kWideTokens;
+  const PagedPlan plan = tree ? tree_plan(c->requests, rows, q_heads, c->kv_heads, wide) : paged_plan(c->requests, rows, q_heads, c->kv_heads);
   // (the split kernel counts its tiles' blocks in 32 bits)
-  if (plan.split_tiles > kMaxSplitTiles || plan.split_tiles * ceil_div(max_pages * c->page_size, kSplitBlock) > 0x7fffffff)
+  if (plan.split_tiles > kMaxSplitTiles || plan.split_tiles * ceil_div(max_pages * c->page_size, plan.wide ? kWideBlock : kSplitBlock) > 0x7fffffff)
     return HLWQ_ERR_LIMIT;
-  const size_t need = plan.split_bytes + plan.chunk_bytes;
+  const size_t need = tree ? workspace_bytes_of(c->requests, rows, q_heads, c->kv_heads, true) : plan.split_bytes + plan.chunk_bytes;
+  if (need == 0) return HLWQ_ERR_LIMIT;
   if (!cu || !lens || !out || !ws || (max_pages > 0 && !table) || (tree && !parents)) return HLWQ_ERR_NULL;
   if (ws_bytes < need) return HLWQ_ERR_SHAPE;
   if (misaligned(parents, 4) || misaligned(cu, 4) || misaligned(lens, 4) || misaligned(table, 4) || misaligned(out, 16) || misaligned(ws, 16))

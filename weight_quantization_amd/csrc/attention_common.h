@@ -44,6 +44,8 @@ struct AttnArgs {
   const int32_t* parents;  // of the rows, where they are trees
   uint16_t* out;
   float* partial;  // workspace: partial sums, then their statistics
+  uint16_t* rotated;      // and, where they are rotated beforehand, the queries
+  float* rotated_factor;
   int64_t n_res, ring;
   int32_t requests, rows, q_heads, kv_heads, group, n_pages, page_shift, width;
   int32_t workers;  // workgroups that share the work

@@ -244,26 +244,18 @@ __device__ __forceinline__ void weigh(SplitRows& r, float (&s)[8], float factor,
   }
 }
 
-// 32 encoded tokens; there: how many of each sixteen exist.
-template <int BITS>
-__device__ __forceinline__ void code_step(SplitRows& r, const u32x4 (&q)[8], float factor, const Codes<BITS>& c, int there_a,
-                                          int there_b, int lane) {
+// The weights of 32 encoded tokens from their products with the query, as the
+// operand of V's products: kn, vn: the lane's norms; there: how many of each
+// sixteen exist.
+__device__ __forceinline__ u32x4 code_weights(SplitRows& r, const f32x4 (&s)[2], float factor, const u32x2 (&k_norms)[2],
+                                              const u32x2 (&v_norms)[2], int there_a, int there_b, int lane) {
   const int h4 = lane >> 4;
-  const bool odd = lane & 1, masked = there_a < 16 || there_b < 16;
-  f32x4 s[2];
-#pragma unroll
-  for (int sub = 0; sub < 2; ++sub) {
-    u32x4 f[8];
-    k_fragments<BITS>(c, sub, f);
-    s[sub] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int x = 0; x < 8; ++x) s[sub] = mfma16<true>(f[x], q[x], s[sub]);
-  }
+  const bool masked = there_a < 16 || there_b < 16;
   float kn[8], vn[8];
   const auto gone = [&](int i) { return 4 * h4 + (i & 3) >= (i < 4 ? there_a : there_b); };
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t kw = c.kn[i >> 2][(i >> 1) & 1], vw = c.vn[i >> 2][(i >> 1) & 1];
+    const uint32_t kw = k_norms[i >> 2][(i >> 1) & 1], vw = v_norms[i >> 2][(i >> 1) & 1];
     kn[i] = f16_value(static_cast<uint16_t>(i & 1 ? kw >> 16 : kw));
     vn[i] = f16_value(static_cast<uint16_t>(i & 1 ? vw >> 16 : vw));
   }
@@ -296,6 +288,24 @@ __device__ __forceinline__ void code_step(SplitRows& r, const u32x4 (&q)[8], flo
   weigh(r, t, factor, masked, gone, p);
 #pragma unroll
   for (int i = 0; i < 4; ++i) pf[i] = pack_f16x2(p[2 * i] * (vn[2 * i] * over), p[2 * i + 1] * (vn[2 * i + 1] * over));
+  return pf;
+}
+
+// 32 encoded tokens.
+template <int BITS>
+__device__ __forceinline__ void code_step(SplitRows& r, const u32x4 (&q)[8], float factor, const Codes<BITS>& c, int there_a,
+                                          int there_b, int lane) {
+  const bool odd = lane & 1;
+  f32x4 s[2];
+#pragma unroll
+  for (int sub = 0; sub < 2; ++sub) {
+    u32x4 f[8];
+    k_fragments<BITS>(c, sub, f);
+    s[sub] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int x = 0; x < 8; ++x) s[sub] = mfma16<true>(f[x], q[x], s[sub]);
+  }
+  const u32x4 pf = code_weights(r, s, factor, c.kn, c.vn, there_a, there_b, lane);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t ca[8], cb[8];
@@ -476,15 +486,16 @@ __device__ __forceinline__ void join_waves(SplitRows& r, bool enc, int there, fl
   }
 }
 
-// What a request asks of the split kernel.
+// What a request asks of the split kernel, or of one with other tiles.
+template <int M = kSplitRows, int KT = kSplitBlock>
 struct SplitWork {
   Extent e;
   int32_t tiles, blocks;  // tiles of a KV head, page blocks of each
   __device__ __forceinline__ SplitWork(const AttnArgs& a, const Extent& x) {
     e = x;
     const int32_t r = e.n * a.group;
-    tiles = r >= a.least && r <= a.most ? static_cast<int32_t>(ceil_div(r, kSplitRows)) : 0;
-    blocks = static_cast<int32_t>(ceil_div(e.paged, kSplitBlock));
+    tiles = r >= a.least && r <= a.most ? static_cast<int32_t>(ceil_div(r, M)) : 0;
+    blocks = static_cast<int32_t>(ceil_div(e.paged, KT));
   }
 };
 // Slots of partial sums (attention_common.h): after the workers' come two to a
@@ -590,12 +601,13 @@ __device__ __forceinline__ void attend_pages(const AttnArgs& a, const Extent& e,
   join_waves(r, true, rows - r0, lds, lane, wave, write);
 }
 
-// Which of the step's own tokens the sixteen rows of a tile see, where these are
-// trees: a bit for each token that is the row's own or an ancestor of it.  Parents
-// come before their children, so the ways up end; sixteen lanes go them in LDS,
+// Which of the step's own tokens the rows of a tile see, where these are trees: a
+// bit for each token that is the row's own or an ancestor of it.  Parents come
+// before their children, so the ways up end; a lane for each row goes them in LDS,
 // where the sums of join_waves lie later.
 struct Kin {
   static constexpr int kWords = HLWQ_TREE_NODES / 32 + 1;  // of a row; the last stays 0
+  static constexpr int bytes(int rows) { return (HLWQ_TREE_NODES + rows * kWords) * 4; }
   const uint32_t* bits;
   int64_t near;
   // bit j: whether the lane's row sees token k0 + j
@@ -607,25 +619,27 @@ struct Kin {
     return __builtin_amdgcn_alignbit(bits[w + 1], bits[w], static_cast<uint32_t>(at & 31));
   }
 };
-static_assert((HLWQ_TREE_NODES + 16 * Kin::kWords) * 4 <= 4 * 16 * kSplitPitch * 4, "a tile's tree lies where its sums do");
+static_assert(Kin::bytes(kSplitRows) <= 4 * 16 * kSplitPitch * 4, "a tile's tree lies where its sums do");
 
-// (`count` tokens: up to the tile's last)
+// The kin of `mine`, a row of the tile of M from r0 on (`count` tokens: up to the
+// tile's last).
+template <int M, int THREADS>
 __device__ __forceinline__ Kin find_kin(const AttnArgs& a, const Extent& e, int64_t near, int32_t r0, int32_t rows, int32_t count,
-                                        float* lds, int lane) {
+                                        float* lds, int mine) {
   int32_t* parent = reinterpret_cast<int32_t*>(lds);
   uint32_t* bits = reinterpret_cast<uint32_t*>(lds) + HLWQ_TREE_NODES;
-  for (int32_t i = threadIdx.x; i < count; i += kSplitThreads) {
+  for (int32_t i = threadIdx.x; i < count; i += THREADS) {
     const int32_t p = a.parents[e.begin + static_cast<int64_t>(i)];
     parent[i] = p < i ? p : -1;
   }
   const int32_t words = (count + 31) / 32 + 1;
-  for (int32_t i = threadIdx.x; i < 16 * words; i += kSplitThreads) bits[i / words * Kin::kWords + i % words] = 0;
+  for (int32_t i = threadIdx.x; i < M * words; i += THREADS) bits[quotient(i, words) * Kin::kWords + i % words] = 0;
   __syncthreads();
-  if (threadIdx.x < 16)
+  if (threadIdx.x < M)
     for (int32_t t = token_of(min(r0 + static_cast<int32_t>(threadIdx.x), rows - 1), a.group); t >= 0; t = parent[t])
       bits[threadIdx.x * Kin::kWords + (t >> 5)] |= 1u << (t & 31);
   __syncthreads();
-  return Kin{bits + (lane & 15) * Kin::kWords, near};
+  return Kin{bits + mine * Kin::kWords, near};
 }
 
 // The window's and the step's own tokens of a tile.
@@ -649,7 +663,7 @@ __device__ __forceinline__ void attend_tokens(const AttnArgs& a, const Extent& e
   }
   SplitRows r;
   if constexpr (TREE) {
-    const Kin kin = find_kin(a, e, tokens.near, r0, rows, static_cast<int32_t>(last - tokens.near) + 1, lds, lane);
+    const Kin kin = find_kin<M, kSplitThreads>(a, e, tokens.near, r0, rows, static_cast<int32_t>(last - tokens.near) + 1, lds, c);
     clear(r);
     for (int64_t k0 = 32 * wave; k0 <= last; k0 += kSplitBlock) {
       const uint32_t seen = kin.word(k0);
@@ -673,9 +687,9 @@ hlwq_split_attention_kernel(const AttnArgs a) {
   constexpr int M = kSplitRows;
   __shared__ __attribute__((aligned(16))) float lds[4 * 16 * kSplitPitch + kSplitStats];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const auto tiles = [&](const Extent& e) { return SplitWork(a, e).tiles * a.kv_heads; };
+  const auto tiles = [&](const Extent& e) { return SplitWork<>(a, e).tiles * a.kv_heads; };
   const auto cost = [&](const Extent& e) {
-    const SplitWork w(a, e);
+    const SplitWork<> w(a, e);
     return w.tiles * w.blocks * a.kv_heads;
   };
   const auto to_slot = [&](int32_t slot) {
@@ -691,7 +705,7 @@ hlwq_split_attention_kernel(const AttnArgs a) {
     Finder<decltype(tiles), Nothing> finder(a, tiles, Nothing{});
     if (x >= finder.total) return;
     const Found f = finder.find(x);
-    const SplitWork w(a, f.e);
+    const SplitWork<> w(a, f.e);
     const int32_t head = quotient(f.rest, w.tiles), r0 = (f.rest - head * w.tiles) * M;
     const int32_t slot = tile_slot(a, x, 1);
     attend_tokens<TREE>(a, w.e, f.b, head, r0, lds, lane, wave, [&](int row, f32x4 o, float m, float l) {
@@ -711,7 +725,7 @@ hlwq_split_attention_kernel(const AttnArgs a) {
   int32_t left = share.bound(worker + 1) - share.bound(worker), b = first.b, rest = first.rest, before = first.before;
 #pragma clang loop unroll(disable)
   while (left > 0 && b < a.requests) {
-    const SplitWork w(a, b == first.b ? first.e : extent_of(a, b));
+    const SplitWork<> w(a, b == first.b ? first.e : extent_of(a, b));
     const int32_t tile = w.blocks ? quotient(rest, w.blocks) : 0;  // of all KV heads'
     if (w.blocks == 0 || tile >= w.tiles * a.kv_heads) {            // past the request's last
       before += w.tiles * a.kv_heads;
@@ -735,16 +749,16 @@ __global__ void __launch_bounds__(kSplitThreads) hlwq_split_join_kernel(const At
   constexpr int M = kSplitRows;
   __shared__ __attribute__((aligned(16))) float lds[4 * kSplitPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const auto tiles = [&](const Extent& e) { return SplitWork(a, e).tiles * a.kv_heads; };
+  const auto tiles = [&](const Extent& e) { return SplitWork<>(a, e).tiles * a.kv_heads; };
   const auto cost = [&](const Extent& e) {
-    const SplitWork w(a, e);
+    const SplitWork<> w(a, e);
     return w.tiles * w.blocks * a.kv_heads;
   };
   Finder<decltype(tiles), decltype(cost)> finder(a, tiles, cost);
   const int32_t x = blockIdx.x / M, row = blockIdx.x % M;
   if (x >= finder.total) return;
   const Found f = finder.find(x);
-  const SplitWork w(a, f.e);
+  const SplitWork<> w(a, f.e);
   const int32_t head = quotient(f.rest, w.tiles), r0 = (f.rest - head * w.tiles) * M;
   if (w.blocks == 0 || r0 + row >= w.e.n * a.group) return;
   const Share share(Finder<decltype(cost), Nothing>(a, cost, Nothing{}).total, a.workers, 1);
