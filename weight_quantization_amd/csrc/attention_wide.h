@@ -314,6 +314,8 @@ __device__ __forceinline__ void wide_pages(const AttnArgs& a, const Extent& e, i
         continue;
       }
       if (idle) continue;
+      // its chain of products and softmax is the longer one (3 us of 144)
+      __builtin_amdgcn_s_setprio(1);
       // kDeep operands on their way while one is multiplied
       constexpr int kDeep = 6;
       const u32x4* f = reinterpret_cast<const u32x4*>(stage + buffer * kWideStage) + lane;
@@ -331,11 +333,12 @@ __device__ __forceinline__ void wide_pages(const AttnArgs& a, const Extent& e, i
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
       }
-      const u32x4 pf = wide_weights(r, s, factor, sides[2 * buffer], h4);
-      __builtin_amdgcn_sched_barrier(0);
+      // V's first operands on their way during the softmax
 #pragma unroll
       for (int x = 0; x < kDeep; ++x) g[x] = f[64 * (16 + x)];
-      __builtin_amdgcn_sched_group_barrier(0x100, kDeep, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      const u32x4 pf = wide_weights(r, s, factor, sides[2 * buffer], h4);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         r.o[x] = mfma16<true>(g[x % kDeep], pf, r.o[x]);
@@ -345,6 +348,7 @@ __device__ __forceinline__ void wide_pages(const AttnArgs& a, const Extent& e, i
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
       }
+      __builtin_amdgcn_s_setprio(0);
     }
   }
   join_halves(r, true, rows - r0, lds, lane, wave, write);

@@ -715,136 +715,136 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
       barrier();
       listed = expert;
     }
-      for (int32_t c = wave; c < columns; c += kProductWaves) {
-        const int32_t pair = __builtin_amdgcn_readfirstlane(list[c0 + c]);
-        const uint16_t* from = a.act + static_cast<int64_t>(GATED ? quotient(pair, a.top_k) : pair) * pitch;
-        for (int32_t piece = lane; piece < a.nb * 16; piece += 64) {
-          const int32_t at_j = (piece & ~15) + (piece & 3) * 4 + (piece >> 2 & 3);  // pieces of 16 bytes: block, h4, j to block, j, h4
-          lds_put<u32x4>(base + L::act + (at_j * columns + c) * 16, *reinterpret_cast<const u32x4*>(from + 8 * piece));
-        }
+    for (int32_t c = wave; c < columns; c += kProductWaves) {
+      const int32_t pair = __builtin_amdgcn_readfirstlane(list[c0 + c]);
+      const uint16_t* from = a.act + static_cast<int64_t>(GATED ? quotient(pair, a.top_k) : pair) * pitch;
+      for (int32_t piece = lane; piece < a.nb * 16; piece += 64) {
+        const int32_t at_j = (piece & ~15) + (piece & 3) * 4 + (piece >> 2 & 3);  // pieces of 16 bytes: block, h4, j to block, j, h4
+        lds_put<u32x4>(base + L::act + (at_j * columns + c) * 16, *reinterpret_cast<const u32x4*>(from + 8 * piece));
       }
-      float pair_scale[4], pair_weight[4];  // of the lane's four
-      if constexpr (GATED)
+    }
+    float pair_scale[4], pair_weight[4];  // of the lane's four
+    if constexpr (GATED)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int32_t pair = list[c0 + min(4 * h4 + i, columns - 1)];
-          pair_scale[i] = a.act_scale[quotient(pair, a.top_k)];
-          pair_weight[i] = a.weights[pair];
-        }
-      if constexpr (!GATED)
-        for (int32_t i = threadIdx.x; i < a.nb * kTile; i += kProductThreads) {
-          const int32_t c = i & (kTile - 1);
-          inner[i] = c < columns ? a.act_scale[static_cast<int64_t>(list[c0 + c]) * a.nb + (i >> 4)] : 0.0f;
-        }
-      wait_lds();
-      barrier();
-      const uint32_t act = base + L::act + (h4 * columns + min(r, columns - 1)) * 16;
+      for (int i = 0; i < 4; ++i) {
+        const int32_t pair = list[c0 + min(4 * h4 + i, columns - 1)];
+        pair_scale[i] = a.act_scale[quotient(pair, a.top_k)];
+        pair_weight[i] = a.weights[pair];
+      }
+    if constexpr (!GATED)
+      for (int32_t i = threadIdx.x; i < a.nb * kTile; i += kProductThreads) {
+        const int32_t c = i & (kTile - 1);
+        inner[i] = c < columns ? a.act_scale[static_cast<int64_t>(list[c0 + c]) * a.nb + (i >> 4)] : 0.0f;
+      }
+    wait_lds();
+    barrier();
+    const uint32_t act = base + L::act + (h4 * columns + min(r, columns - 1)) * 16;
 
-      for (int32_t set = set0; set < set1; ++set) {
-        f32x4 acc[2] = {};
-        if (!idle(set)) {
-          uint32_t norm_at[2];
+    for (int32_t set = set0; set < set1; ++set) {
+      f32x4 acc[2] = {};
+      if (!idle(set)) {
+        uint32_t norm_at[2];
 #pragma unroll
-          for (int m = 0; m < 2; ++m) norm_at[m] = my + L::norms + m * 256 + r * 16 + 2 * ((row_of(set, m, r) * a.nb) & 1);
-          for (int32_t chunk = 0; chunk < chunks; ++chunk) {
-            wait_staged();
-            RowCodes<BITS> code[2][kChunk];
-            float norm[2][kChunk];
+        for (int m = 0; m < 2; ++m) norm_at[m] = my + L::norms + m * 256 + r * 16 + 2 * ((row_of(set, m, r) * a.nb) & 1);
+        for (int32_t chunk = 0; chunk < chunks; ++chunk) {
+          wait_staged();
+          RowCodes<BITS> code[2][kChunk];
+          float norm[2][kChunk];
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int k = 0; k < kChunk; ++k) {
+            for (int k = 0; k < kChunk; ++k) {
 #pragma unroll
-                for (int d = 0; d < BITS; ++d) set_word(code[m][k], d, lds_at<uint32_t>(place[k][d] + m * L::codes));
-                norm[m][k] = f16_value(lds_at<uint16_t>(norm_at[m] + 2 * k));
-              }
-            wait_lds();
-            if (chunk + 1 < chunks)
-              stage(set, chunk + 1);
-            else if (set + 1 < set1 && !idle(set + 1))
-              stage(set + 1, 0);
-            // Unit u: block u / 2, tile u % 2.  The look-ups of the next unit are under
-            // way while one is multiplied.
-            u32x4 x[2][4], w[2][4];
-            f32x4 scale[2];
-            const auto look = [&](int u) {
-              const int k = u >> 1;
-              if ((u & 1) == 0) {
-                const int32_t b = chunk * kChunk + k;
+              for (int d = 0; d < BITS; ++d) set_word(code[m][k], d, lds_at<uint32_t>(place[k][d] + m * L::codes));
+              norm[m][k] = f16_value(lds_at<uint16_t>(norm_at[m] + 2 * k));
+            }
+          wait_lds();
+          if (chunk + 1 < chunks)
+            stage(set, chunk + 1);
+          else if (set + 1 < set1 && !idle(set + 1))
+            stage(set + 1, 0);
+          // Unit u: block u / 2, tile u % 2.  The look-ups of the next unit are under
+          // way while one is multiplied.
+          u32x4 x[2][4], w[2][4];
+          f32x4 scale[2];
+          const auto look = [&](int u) {
+            const int k = u >> 1;
+            if ((u & 1) == 0) {
+              const int32_t b = chunk * kChunk + k;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[k & 1][j] = lds_at<u32x4>(act + (b * 4 + j) * 64 * columns);
-                if constexpr (!GATED) scale[k & 1] = *reinterpret_cast<const f32x4*>(inner + b * kTile + 4 * h4);
-              }
-              decode<BITS, BITS == 5 ? kWithoutBook : 0>(code[u & 1][k], lds + L::book, copy, w[u & 1]);
-              __builtin_amdgcn_sched_barrier(0);
-            };
-            const auto multiply = [&](int u) {
-              const int k = u >> 1, m = u & 1;
-              f32x4 d = {0, 0, 0, 0};
+              for (int j = 0; j < 4; ++j) x[k & 1][j] = lds_at<u32x4>(act + (b * 4 + j) * 64 * columns);
+              if constexpr (!GATED) scale[k & 1] = *reinterpret_cast<const f32x4*>(inner + b * kTile + 4 * h4);
+            }
+            decode<BITS, BITS == 5 ? kWithoutBook : 0>(code[u & 1][k], lds + L::book, copy, w[u & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+          };
+          const auto multiply = [&](int u) {
+            const int k = u >> 1, m = u & 1;
+            f32x4 d = {0, 0, 0, 0};
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x[k & 1][j]), __builtin_bit_cast(f16x8, w[m][j]), d, 0, 0, 0);
+            for (int j = 0; j < 4; ++j)
+              d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x[k & 1][j]), __builtin_bit_cast(f16x8, w[m][j]), d, 0, 0, 0);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[m][i] = __builtin_fmaf(d[i], GATED ? norm[m][k] : scale[k & 1][i] * norm[m][k], acc[m][i]);
-              __builtin_amdgcn_sched_barrier(0);
-            };
-            const int32_t there = min(a.nb - chunk * kChunk, kChunk);
-            if (there == kChunk) {
-              look(0);
+            for (int i = 0; i < 4; ++i) acc[m][i] = __builtin_fmaf(d[i], GATED ? norm[m][k] : scale[k & 1][i] * norm[m][k], acc[m][i]);
+            __builtin_amdgcn_sched_barrier(0);
+          };
+          const int32_t there = min(a.nb - chunk * kChunk, kChunk);
+          if (there == kChunk) {
+            look(0);
 #pragma unroll
-              for (int u = 0; u < 2 * kChunk; ++u) {
-                if (u + 1 < 2 * kChunk) look(u + 1);
+            for (int u = 0; u < 2 * kChunk; ++u) {
+              if (u + 1 < 2 * kChunk) look(u + 1);
+              multiply(u);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2 * (kChunk - 1); ++u)
+              if (u < 2 * there) {
+                look(u);
                 multiply(u);
               }
-            } else {
-#pragma unroll
-              for (int u = 0; u < 2 * (kChunk - 1); ++u)
-                if (u < 2 * there) {
-                  look(u);
-                  multiply(u);
-                }
-            }
           }
         }
-        const int32_t out0 = (set * kProductWaves + wave) * (GATED ? kTile : 2 * kTile);
-        if constexpr (GATED) {
-          barrier();
+      }
+      const int32_t out0 = (set * kProductWaves + wave) * (GATED ? kTile : 2 * kTile);
+      if constexpr (GATED) {
+        barrier();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t c = 4 * h4 + i;
+          float v = 0;
+          if (c < columns && out0 + r < a.n_out)
+            v = activate(acc[0][i] * pair_scale[i], a.activation) * (acc[1][i] * pair_scale[i]) * pair_weight[i];
+          inner[c * kPitch + wave * kTile + r] = v;
+        }
+        wait_lds();
+        barrier();
+        for (int32_t c = wave; c < columns; c += kProductWaves) {
+          const float2 v = *reinterpret_cast<const float2*>(inner + c * kPitch + 2 * lane);
+          float y[2] = {v.x, v.y};
+          const float y0 = fabsf(y[0]) <= FLT_MAX ? fabsf(y[0]) : 0.0f, y1 = fabsf(y[1]) <= FLT_MAX ? fabsf(y[1]) : 0.0f;
+          const int e = scale_exponent(wave_max(fmaxf(y0, y1)));
+          const float f = __builtin_ldexpf(1.0f, 7 - e);
+          y[0] *= f;
+          y[1] *= f;
+          block_fwht(y, lane);
+          const int64_t to = static_cast<int64_t>(list[c0 + c]) * sets + set;
+          *reinterpret_cast<uint32_t*>(a.rotated + to * kBlock + 2 * lane) = pack_f16x2(y[0], y[1]);
+          if (lane == 0) a.rotated_scale[to] = __builtin_ldexpf(1.0f, e - 14);
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int32_t o = out0 + m * kTile + r;
+          if (o >= a.n_out) continue;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int32_t c = 4 * h4 + i;
-            float v = 0;
-            if (c < columns && out0 + r < a.n_out)
-              v = activate(acc[0][i] * pair_scale[i], a.activation) * (acc[1][i] * pair_scale[i]) * pair_weight[i];
-            inner[c * kPitch + wave * kTile + r] = v;
-          }
-          wait_lds();
-          barrier();
-          for (int32_t c = wave; c < columns; c += kProductWaves) {
-            const float2 v = *reinterpret_cast<const float2*>(inner + c * kPitch + 2 * lane);
-            float y[2] = {v.x, v.y};
-            const float y0 = fabsf(y[0]) <= FLT_MAX ? fabsf(y[0]) : 0.0f, y1 = fabsf(y[1]) <= FLT_MAX ? fabsf(y[1]) : 0.0f;
-            const int e = scale_exponent(wave_max(fmaxf(y0, y1)));
-            const float f = __builtin_ldexpf(1.0f, 7 - e);
-            y[0] *= f;
-            y[1] *= f;
-            block_fwht(y, lane);
-            const int64_t to = static_cast<int64_t>(list[c0 + c]) * sets + set;
-            *reinterpret_cast<uint32_t*>(a.rotated + to * kBlock + 2 * lane) = pack_f16x2(y[0], y[1]);
-            if (lane == 0) a.rotated_scale[to] = __builtin_ldexpf(1.0f, e - 14);
-          }
-        } else {
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const int32_t o = out0 + m * kTile + r;
-            if (o >= a.n_out) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int32_t c = 4 * h4 + i;
-              if (c < columns) a.out[static_cast<int64_t>(list[c0 + c]) * a.n_out + o] = acc[m][i];
-            }
+            if (c < columns) a.out[static_cast<int64_t>(list[c0 + c]) * a.n_out + o] = acc[m][i];
           }
         }
       }
+    }
   }
 }
 
