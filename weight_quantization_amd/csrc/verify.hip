@@ -12,6 +12,8 @@
 
 #include "hlwq_drafts.h"
 
+#include <type_traits>
+
 namespace hlwq_kv {
 namespace {
 
@@ -69,7 +71,9 @@ struct Wide {
 // A lane's sum of weights of [lo, hi), over the wave's share of it, W values to a
 // load.  Sixteen waves keep enough loads on their way; several to a wave make the
 // code longer, and most of it runs once: four took 25 us for 250 rows of 100003
-// bf16 where one takes 19.
+// bf16 where one takes 19.  Where a draft's refusals read row after row, two at a
+// time are worth it: 39.4 us for 48 trees over 131072 where one takes 43.4 (four
+// 38.9).
 template <class T, bool DRAFT>
 __device__ __forceinline__ double lane_sum(const Residual<T, DRAFT>& r, int32_t lo, int32_t hi, int lane) {
   typedef typename Wide<T>::type wide;
@@ -77,15 +81,28 @@ __device__ __forceinline__ double lane_sum(const Residual<T, DRAFT>& r, int32_t 
   double sum = 0;
   const int32_t whole = lo + (hi - lo) / W * W;
   const auto over = [&](auto weight, bool both) {
-#pragma clang loop unroll(disable)
-    for (int32_t i = lo + lane * W; i < whole; i += 64 * W) {
-      const wide p = *reinterpret_cast<const wide*>(r.p + i);
-      wide q{};
-      if (both) q = *reinterpret_cast<const wide*>(r.q + i);
+    constexpr int kTogether = DRAFT ? 2 : 1;
+    int32_t i = lo + lane * W;
+    const auto step = [&](auto loads) {
+      wide p[loads], q[loads];
 #pragma unroll
-      for (int j = 0; j < W; ++j) sum += weight(i + j, T::value(p[j]), T::value(q[j]));
-    }
-    for (int32_t i = whole + lane; i < hi; i += 64) sum += weight(i, T::value(r.p[i]), both ? T::value(r.q[i]) : 0.0f);
+      for (int k = 0; k < loads; ++k) {
+        p[k] = *reinterpret_cast<const wide*>(r.p + i + 64 * W * k);
+        q[k] = wide{};
+        if (both) q[k] = *reinterpret_cast<const wide*>(r.q + i + 64 * W * k);
+      }
+#pragma unroll
+      for (int k = 0; k < loads; ++k)
+#pragma unroll
+        for (int j = 0; j < W; ++j) sum += weight(i + 64 * W * k + j, T::value(p[k][j]), T::value(q[k][j]));
+      i += 64 * W * loads;
+    };
+    if constexpr (kTogether > 1)
+#pragma clang loop unroll(disable)
+      while (i + 64 * W * (kTogether - 1) < whole) step(std::integral_constant<int, kTogether>{});
+#pragma clang loop unroll(disable)
+    while (i < whole) step(std::integral_constant<int, 1>{});
+    for (i = whole + lane; i < hi; i += 64) sum += weight(i, T::value(r.p[i]), both ? T::value(r.q[i]) : 0.0f);
   };
   const auto alone = [](int32_t, float p, float) { return static_cast<double>(fmaxf(p, 0.0f)); };
   if constexpr (DRAFT) {
