@@ -324,6 +324,23 @@ def test_wide_nan_and_infinities_stay_with_the_rows_that_see_them(wq):
         assert not torch.isfinite(got[hit]).any()
 
 
+@pytest.mark.parametrize("new,width", [([12, 3], None), ([70, 30], 64)])
+def test_a_bad_query_stays_in_its_row(wq, new, width):
+    rng = np.random.default_rng(14)
+    ctx, n = [300, 20], sum(new)
+    c = Cache(rng, ctx, 2, 3, 64, 128, 128, width=width)
+    q, kv = bf16_bits(rng, n, 4, D), [bf16_bits(rng, n, 2, D) for _ in range(2)]
+    rest = (i32(trees(rng, new, 4)), i32([0, new[0], n]), i32([t + m for t, m in zip(ctx, new)]), i32(c.table), *c.tensors())
+    clean = wq.hlwq_kv_tree_attention(dev16(q), dev16(kv[0]), dev16(kv[1]), *rest)
+    dirty = q.copy()
+    dirty[3, 1, 200], dirty[n - 2, 2, 0] = 0x7FC0, 0x7F80
+    got = wq.hlwq_kv_tree_attention(dev16(dirty), dev16(kv[0]), dev16(kv[1]), *rest)
+    hit = torch.zeros(n, 4, dtype=torch.bool, device="cuda")
+    hit[3, 1] = hit[n - 2, 2] = True
+    assert torch.isnan(got[3, 1]).all() and not torch.isfinite(got[n - 2, 2]).any()
+    assert torch.equal(got[~hit], clean[~hit])
+
+
 def test_steps_of_drafted_tokens(wq):
     """Trees through attention, an experts' layer and the verification; what is kept goes into the cache by plan and
     append, step after step, and every step's outputs are those of the definition on a cache built token by token."""

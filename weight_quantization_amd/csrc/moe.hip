@@ -588,7 +588,9 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
 
 constexpr int kWorkgroups = 256;
 constexpr int kMaxInnerBlocks = 64;  // whose scales a workgroup keeps
-constexpr int kActBytes = 48 << 10;  // of activations in LDS
+// Of activations in LDS.  (40 KB, and four copies of the pairs of 5-bit codes, took 2%
+// less for 64 and 192 tokens of 256 experts; but busier experts take passes more.)
+constexpr int kActBytes = 48 << 10;
 constexpr int kChunk = 4;            // blocks that are staged together
 constexpr int kWithoutBook = 1;      // fours of 32 5-bit codes whose centroids come from registers
 
