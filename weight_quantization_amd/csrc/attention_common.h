@@ -41,11 +41,8 @@ struct AttnArgs {
   const int32_t* cu;
   const int32_t* lens;  // null: nothing is cached
   const int32_t* table;
-  const int32_t* parents;  // of the rows, where they are trees
   uint16_t* out;
   float* partial;  // workspace: partial sums, then their statistics
-  uint16_t* rotated;      // and, where they are rotated beforehand, the queries
-  float* rotated_factor;
   int64_t n_res, ring;
   int32_t requests, rows, q_heads, kv_heads, group, n_pages, page_shift, width;
   int32_t workers;  // workgroups that share the work
@@ -54,6 +51,10 @@ struct AttnArgs {
   int32_t cost_shift;
   float scale;   // its sign is given to the queries
   float factor;  // |scale| log2 e, above 0: a masked score, minus infinity, stays that
+  // where the rows are trees
+  const int32_t* parents;
+  uint16_t* rotated;      // of the workspace, for tiles of 64 rows: the queries,
+  float* rotated_factor;  // and the factors of their scores
 };
 
 // One request's part of a step.

@@ -244,18 +244,26 @@ __device__ __forceinline__ void weigh(SplitRows& r, float (&s)[8], float factor,
   }
 }
 
-// The weights of 32 encoded tokens from their products with the query, as the
-// operand of V's products: kn, vn: the lane's norms; there: how many of each
-// sixteen exist.
-__device__ __forceinline__ u32x4 code_weights(SplitRows& r, const f32x4 (&s)[2], float factor, const u32x2 (&k_norms)[2],
-                                              const u32x2 (&v_norms)[2], int there_a, int there_b, int lane) {
+// 32 encoded tokens; there: how many of each sixteen exist.
+template <int BITS>
+__device__ __forceinline__ void code_step(SplitRows& r, const u32x4 (&q)[8], float factor, const Codes<BITS>& c, int there_a,
+                                          int there_b, int lane) {
   const int h4 = lane >> 4;
-  const bool masked = there_a < 16 || there_b < 16;
+  const bool odd = lane & 1, masked = there_a < 16 || there_b < 16;
+  f32x4 s[2];
+#pragma unroll
+  for (int sub = 0; sub < 2; ++sub) {
+    u32x4 f[8];
+    k_fragments<BITS>(c, sub, f);
+    s[sub] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int x = 0; x < 8; ++x) s[sub] = mfma16<true>(f[x], q[x], s[sub]);
+  }
   float kn[8], vn[8];
   const auto gone = [&](int i) { return 4 * h4 + (i & 3) >= (i < 4 ? there_a : there_b); };
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t kw = k_norms[i >> 2][(i >> 1) & 1], vw = v_norms[i >> 2][(i >> 1) & 1];
+    const uint32_t kw = c.kn[i >> 2][(i >> 1) & 1], vw = c.vn[i >> 2][(i >> 1) & 1];
     kn[i] = f16_value(static_cast<uint16_t>(i & 1 ? kw >> 16 : kw));
     vn[i] = f16_value(static_cast<uint16_t>(i & 1 ? vw >> 16 : vw));
   }
@@ -288,24 +296,6 @@ __device__ __forceinline__ u32x4 code_weights(SplitRows& r, const f32x4 (&s)[2],
   weigh(r, t, factor, masked, gone, p);
 #pragma unroll
   for (int i = 0; i < 4; ++i) pf[i] = pack_f16x2(p[2 * i] * (vn[2 * i] * over), p[2 * i + 1] * (vn[2 * i + 1] * over));
-  return pf;
-}
-
-// 32 encoded tokens.
-template <int BITS>
-__device__ __forceinline__ void code_step(SplitRows& r, const u32x4 (&q)[8], float factor, const Codes<BITS>& c, int there_a,
-                                          int there_b, int lane) {
-  const bool odd = lane & 1;
-  f32x4 s[2];
-#pragma unroll
-  for (int sub = 0; sub < 2; ++sub) {
-    u32x4 f[8];
-    k_fragments<BITS>(c, sub, f);
-    s[sub] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int x = 0; x < 8; ++x) s[sub] = mfma16<true>(f[x], q[x], s[sub]);
-  }
-  const u32x4 pf = code_weights(r, s, factor, c.kn, c.vn, there_a, there_b, lane);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t ca[8], cb[8];

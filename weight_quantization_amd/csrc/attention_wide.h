@@ -192,7 +192,7 @@ __device__ __forceinline__ void unpack_part(Codes<BITS>& c, int part, uint8_t* t
 }
 
 // The weights of 32 encoded tokens from their products with the query, as the
-// operand of V's products: as code_weights, with the norms that lie in LDS.
+// operand of V's products: as in code_step, with the norms that lie in LDS.
 __device__ __forceinline__ u32x4 wide_weights(SplitRows& r, f32x4 (&s)[2], float factor, const WideSide& side, int h4) {
   const int32_t exponent = __builtin_amdgcn_readfirstlane(side.exponent);
   if (exponent != r.exponent) {
@@ -273,7 +273,7 @@ __device__ __forceinline__ void wide_pages(const AttnArgs& a, const Extent& e, i
       const int mine = part ? there_b : there_a;
       if (lane < 16) side.k[16 * part + lane] = lane < mine ? n : -1.0f;
     } else if (part == 2) {
-      // as in code_weights: over a power of two that no norm met so far exceeds
+      // as in code_step: over a power of two that no norm met so far exceeds
       const bool in = c < (lane & 16 ? there_b : there_a);
       const float top = wave_max(in ? n : 0.0f);
       if (top > __builtin_ldexpf(1.0f, exponent)) exponent = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top));
