@@ -403,6 +403,22 @@ __device__ __forceinline__ u32x2 four_centroids(uint32_t v) {
   return u32x2{__builtin_amdgcn_perm(hi, lo, 0x05010400u), __builtin_amdgcn_perm(hi, lo, 0x07030602u)};
 }
 
+// Two 3-bit codes, the low six bits of v, to two centroids.
+struct Values3 {
+  static constexpr float c[8] = HLWQ_CENTROIDS_3;
+  static constexpr uint32_t word(int first, int shift) {
+    uint32_t w = 0;
+    for (int i = 0; i < 4; ++i) w |= ((__builtin_bit_cast(uint16_t, static_cast<_Float16>(c[first + i])) >> shift) & 0xffu) << (8 * i);
+    return w;
+  }
+};
+__device__ __forceinline__ uint32_t two_centroids(uint32_t v) {
+  const uint32_t at = (v & 7u) | (v << 5 & 0x700u);
+  const uint32_t hi = __builtin_amdgcn_perm(Values3::word(4, 8), Values3::word(0, 8), at);
+  const uint32_t lo = __builtin_amdgcn_perm(Values3::word(4, 0), Values3::word(0, 0), at);
+  return __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+}
+
 // 32 codes to four operands of eight centroids.
 template <int BITS, int WITHOUT = 0>
 __device__ __forceinline__ void decode(const RowCodes<BITS>& c, const uint8_t* book, uint32_t copy, u32x4 (&w)[4]) {
@@ -429,14 +445,20 @@ __device__ __forceinline__ float activate(float g, int32_t kind) {
   return sigmoid_times(g, kind == HLWQ_ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g));
 }
 
+// (From registers: with tables read from memory a kernel of five tokens took 0.4 us
+// more.)
 template <int BITS>
 __device__ __forceinline__ void fill_book(uint8_t* book) {
-  constexpr float c5[32] = HLWQ_CENTROIDS_5;
-  constexpr float c3[8] = HLWQ_CENTROIDS_3;
+  static_assert(Book<BITS>::kBytes == 16 * kProductThreads, "four words a thread");
+  if constexpr (BITS == 5) {
 #pragma unroll
-  for (uint32_t i = 0; i < Book<BITS>::kBytes / 4 / kProductThreads; ++i) {
-    const uint32_t at = i * kProductThreads + threadIdx.x, p = at >> Book<BITS>::kShift;
-    reinterpret_cast<uint32_t*>(book)[at] = BITS == 5 ? pack_f16x2(c5[p & 31], c5[p >> 5]) : pack_f16x2(c3[p & 7], c3[p >> 3 & 7]);
+    for (uint32_t i = 0; i < 2; ++i) {
+      const uint32_t p = i * kProductThreads + threadIdx.x, v = four_centroids(p)[0];
+      reinterpret_cast<u32x2*>(book)[p] = u32x2{v, v};
+    }
+  } else {
+    const uint32_t v = two_centroids(threadIdx.x >> 3);
+    reinterpret_cast<u32x4*>(book)[threadIdx.x] = u32x4{v, v, v, v};
   }
 }
 
