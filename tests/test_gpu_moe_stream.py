@@ -1,4 +1,4 @@
-"""GPU tests of the mixture-of-experts layer where many pairs meet large banks: banks streamed through LDS (128 blocks and
+"""GPU tests of the mixture-of-experts layer where many pairs meet large banks: banks streamed through LDS (160 blocks and
 more of the down projections' rows among the touched experts, more than 32 pairs), and the same sizes in banks that lie so
 that they are not."""
 import numpy as np
@@ -21,7 +21,7 @@ def moved(t, by):
 
 def given(wq, rng, tokens, experts, hidden, inner, k, bits, kind, among=None, put=dev):
     """A call with experts drawn from `among`, against the definition."""
-    assert tokens * k > 32 and min(experts, tokens * k) * -(-inner // 128) >= 128
+    assert tokens * k > 32 and min(experts, tokens * k) * -(-inner // 128) >= 160
     x, xf = bf16(rng, tokens, hidden)
     up, down = bank(rng, experts, 2 * inner, hidden, bits), bank(rng, experts, hidden, inner, bits)
     ids = rng.choice(np.arange(experts) if among is None else among, (tokens, k)).astype(np.int32)
@@ -33,9 +33,9 @@ def given(wq, rng, tokens, experts, hidden, inner, k, bits, kind, among=None, pu
 
 
 @pytest.mark.parametrize("tokens,experts,hidden,inner,k", [
-    (17, 128, 256, 128, 8), (130, 130, 128, 1, 1), (33, 128, 1, 130, 2), (40, 64, 300, 200, 8), (70, 43, 1000, 385, 8),
-    (16, 128, 1150, 72, 8), (300, 16, 514, 1030, 4), (65, 3, 140, 7000, 1), (150, 2, 100, 8192, 1), (1000, 150, 260, 100, 6),
-    (34, 13, 2050, 1300, 1), (64, 256, 640, 96, 32),
+    (20, 160, 256, 128, 8), (170, 170, 128, 1, 1), (40, 128, 1, 130, 2), (40, 80, 300, 200, 8), (70, 43, 1000, 385, 8),
+    (20, 160, 1150, 72, 8), (300, 18, 514, 1030, 4), (65, 3, 140, 7000, 1), (150, 3, 100, 8192, 1), (1000, 170, 260, 100, 6),
+    (34, 15, 2050, 1300, 1), (64, 256, 640, 96, 32),
 ])
 @pytest.mark.parametrize("bits,kind", [(5, "silu"), (3, "gelu_tanh")])
 def test_sizes(wq, tokens, experts, hidden, inner, k, bits, kind):
@@ -45,7 +45,7 @@ def test_sizes(wq, tokens, experts, hidden, inner, k, bits, kind):
 @pytest.mark.parametrize("bits", [5, 3])
 def test_the_widest_rows(wq, bits):
     # 192 blocks of a token's activations; few of many experts named
-    given(wq, np.random.default_rng(1), 33, 128, 24500, 20, 4, bits, "silu", among=[0, 77, 127])
+    given(wq, np.random.default_rng(1), 41, 160, 24500, 20, 4, bits, "silu", among=[0, 77, 127])
 
 
 @pytest.mark.parametrize("bits,kind", [(5, "gelu_tanh"), (3, "silu")])
@@ -58,17 +58,17 @@ def test_uneven_routings(wq, bits, kind, among):
 @pytest.mark.parametrize("bits", [5, 3])
 @pytest.mark.parametrize("by", [4, 8])
 def test_banks_that_lie_otherwise(wq, bits, by):
-    given(wq, np.random.default_rng(3), 40, 64, 300, 200, 4, bits, "silu", put=lambda b: [moved(t, by) for t in dev(b)])
+    given(wq, np.random.default_rng(3), 40, 80, 300, 200, 4, bits, "silu", put=lambda b: [moved(t, by) for t in dev(b)])
 
 
 def test_norms_at_odd_places(wq):
-    given(wq, np.random.default_rng(4), 40, 64, 300, 200, 4, 5, "silu", put=lambda b: [moved(t, i * 2) for i, t in enumerate(dev(b))])
+    given(wq, np.random.default_rng(4), 40, 80, 300, 200, 4, 5, "silu", put=lambda b: [moved(t, i * 2) for i, t in enumerate(dev(b))])
     # an odd number of norms to an expert
-    given(wq, np.random.default_rng(5), 40, 43, 301, 300, 4, 5, "silu")
+    given(wq, np.random.default_rng(5), 40, 55, 301, 300, 4, 5, "silu")
 
 
 def test_inner_sizes_past_what_streams(wq):
-    given(wq, np.random.default_rng(6), 34, 2, 130, 8193, 1, 3, "silu")
+    given(wq, np.random.default_rng(6), 34, 3, 130, 8193, 1, 3, "silu")
 
 
 @pytest.mark.parametrize("tokens,experts,hidden,inner,k", [(32, 300, 256, 200, 1), (2, 700, 300, 64, 16), (1, 1024, 8192, 10, 32),
@@ -86,10 +86,23 @@ def test_about_thirty_two_pairs(wq, tokens, experts, hidden, inner, k, bits):
     mr.check(f64(y.out), *mr.experts(xf, ids, y.weights.cpu().numpy(), up, down, bits, "silu"))
 
 
+@pytest.mark.parametrize("tokens,experts,hidden,inner,k", [(16, 8, 1024, 520, 2), (4, 40, 2048, 512, 8), (2, 40, 2048, 512, 8),
+                                                            (16, 64, 512, 256, 4), (40, 64, 300, 200, 8), (64, 8, 512, 500, 2)])
+@pytest.mark.parametrize("bits", [5, 3])
+def test_either_side_of_what_streams(wq, tokens, experts, hidden, inner, k, bits):
+    """Fewer sets of rows than the streaming asks for, and pairs that are few or not by what they read."""
+    rng = np.random.default_rng(tokens + inner)
+    x, xf = bf16(rng, tokens, hidden)
+    up, down = bank(rng, experts, 2 * inner, hidden, bits), bank(rng, experts, hidden, inner, bits)
+    ids, w = rng.integers(0, experts, (tokens, k)).astype(np.int32), rng.standard_normal((tokens, k)).astype(np.float32)
+    y = wq.hlwq_moe_experts(x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), *dev(up), *dev(down), bits=bits)
+    mr.check(f64(y), *mr.experts(xf, ids, w, up, down, bits, "silu"))
+
+
 @pytest.mark.parametrize("bits", [5, 3])
 def test_a_bad_row_stays_in_its_row(wq, bits):
     rng = np.random.default_rng(7)
-    tokens, experts, hidden, inner = 60, 128, 300, 150
+    tokens, experts, hidden, inner = 80, 128, 300, 150
     x, _ = bf16(rng, tokens, hidden)
     up, down = dev(bank(rng, experts, 2 * inner, hidden, bits)), dev(bank(rng, experts, hidden, inner, bits))
     ids = torch.tensor([[0, 2]] * tokens, dtype=torch.int32, device="cuda")
@@ -106,7 +119,7 @@ def test_a_bad_row_stays_in_its_row(wq, bits):
 @pytest.mark.parametrize("sigma", [1e-30, 1e17])
 def test_small_and_large_activations(wq, sigma):
     rng = np.random.default_rng(8)
-    experts, hidden, inner = 128, 256, 100
+    experts, hidden, inner = 160, 256, 100
     x, xf = bf16(rng, 40, hidden, sigma=sigma)
     up, down = bank(rng, experts, 2 * inner, hidden, 5), bank(rng, experts, hidden, inner, 5)
     ids, w = rng.integers(0, experts, (40, 4)).astype(np.int32), rng.random((40, 4)).astype(np.float32)

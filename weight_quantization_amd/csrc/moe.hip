@@ -193,7 +193,9 @@ __global__ void __launch_bounds__(kRotateThreads) hlwq_moe_prepare_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// The best experts of a token, a wave each: lane l holds experts l, l + 64, ..
+// The best experts of a token, a wave each: lane l holds experts l, l + 64, ..;
+// top_k times the largest of the wave's, by the upper halves of the logits first.
+// 4 to 5.4 us for 5 to 192 tokens, most of it a kernel's start.
 // ---------------------------------------------------------------------------
 
 struct TopArgs {
@@ -299,13 +301,15 @@ __global__ void __launch_bounds__(kTopThreads) hlwq_moe_top_kernel(const TopArgs
 }
 
 // ---------------------------------------------------------------------------
-// Products with an expert's codes.  A workgroup takes the a-th of the experts
-// that some pair names and some tiles of sixteen rows of its matrix (with GATED
-// the same tile of gate and up); its waves split the blocks of a row, KS ways,
-// or the tiles.  Per block and tile a lane holds 32 codes of one row, looks them
-// up two at a time, and they meet sixteen pairs' activations in four matrix
-// products; the norm of a row and block multiplies the result, where it is one
-// value to a lane.
+// Products with an expert's codes, where the named experts are not many.  A
+// workgroup takes the a-th of the experts that some pair names and some tiles of
+// sixteen rows of its matrix (with GATED the same tile of gate and up); its waves
+// split the blocks of a row, KS ways, or the tiles.  Per block and tile a lane
+// holds 32 codes of one row, looks them up two at a time, and they meet sixteen
+// pairs' activations in four matrix products; the norm of a row and block
+// multiplies the result, where it is one value to a lane.  What bounds it are the
+// loads, 20 bytes of another row to each lane, an address a cycle: all 256 experts of
+// 2048 x 512 would take 143 + 61 us (64 tokens), twice what streaming takes.
 // ---------------------------------------------------------------------------
 
 constexpr int kProductThreads = 512, kProductWaves = kProductThreads / 64;
@@ -606,6 +610,11 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
 // are turned by the row so that the dwords that the lanes then read lie in
 // different banks.  Inner values are rotated before they leave, over a power of
 // two for each block (act_scale [.][nb]).
+//
+// Measured (256 experts, hidden 2048, inner 512, 5 bits): gate and up 82 us for 64
+// tokens (298 MB of codes and norms) and 103 for 192 (344 MB), down 43 and 50: 5 TB/s
+// while every CU has a set, of which LDS look-ups take a third of the cycles and
+// VALU another; without work the kernel takes 4.  17 tokens at 3 bits 32 and 20.
 // ---------------------------------------------------------------------------
 
 constexpr int kWorkgroups = 256;
@@ -879,6 +888,11 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
 // does, the second rotates the inner values and joins a token's pairs.  A
 // workgroup takes sixteen rows; its waves split the blocks of one pair, or the
 // pairs.  All sixteen rows of the activations' operand are the same pair's.
+//
+// Measured (one token, 8 of 256 experts, hidden 2048, inner 512, 5 bits, 16 MB): 11.3
+// us, of which 2.9 are the choice and 4.1 the start, and 7.8.  What bounds them is
+// latency and the fetching of code that runs once: centroids from registers
+// instead of the book, and loops instead of unrolled blocks, change nothing.
 // ---------------------------------------------------------------------------
 
 constexpr int kFewPairs = 32, kFewBlocks = 64;
@@ -1157,9 +1171,19 @@ int launch_product(const ProductArgs& a, hipStream_t stream) {
   return go(hlwq_moe_product_kernel<BITS, 8, 3, GATED>, 1);
 }
 
-// Whether the pairs are few enough for the two kernels that do the most by themselves.
+// Whether the pairs are few enough for the two kernels that do the most by
+// themselves, but read an expert's codes again for each pair.  Measured (all kernels
+// of a layer with 5 bits, us; pairs, hidden x inner, blocks of codes they read):
+//   8 of 2048 x 512, 197 thousand    22.9, by the product kernels 29.5
+//   32 of 2048 x 128, 197 thousand   22.5, 31.2
+//   16 of 2048 x 512, 393 thousand   30.8, 34.7
+//   32 of 2048 x 512, 786 thousand   51.4, 39.1
+//   8 of 4096 x 1024, 786 thousand   38.1, 40.0
+//   32 of 4096 x 1024, 3.1 million   115, 47
+constexpr int64_t kFewCodes = 1 << 19;  // blocks
 bool few(const Sizes& s, int64_t pairs) {
-  return pairs <= kFewPairs && s.hidden_blocks <= kFewBlocks && s.inner_blocks <= kFewBlocks;
+  return pairs <= kFewPairs && s.hidden_blocks <= kFewBlocks && s.inner_blocks <= kFewBlocks &&
+         pairs * (2 * s.inner * s.hidden_blocks + s.hidden * s.inner_blocks) <= kFewCodes;
 }
 template <int BITS>
 int launch_few(const FewArgs& up, const ProductArgs& down, hipStream_t stream) {
@@ -1173,9 +1197,16 @@ int launch_few(const FewArgs& up, const ProductArgs& down, hipStream_t stream) {
 }
 
 // Whether the touched experts' sets of rows give the CUs work enough, and the
-// banks lie as the loads to LDS take them.
+// banks lie as the loads to LDS take them.  Measured (as above; sets of gate and up
+// if no expert is named twice):
+//   32 of 256 experts, 2048 x 512, 128 sets     47.1, by the product kernels 39.1
+//   64 of 64, 1024 x 256, 128                   37.1, 30.7
+//   64 of 8, 4096 x 2048, 128                   83.0, 84.6
+//   128 of 256, 2048 x 128, 128                 49.1, 48.6
+//   192 of 256, 2048 x 128, 192                 50.8, 56.3
+constexpr int64_t kStreamSets = 160;
 bool streams(const hlwq_moe_banks& b, const Sizes& s, int64_t pairs) {
-  return s.inner_blocks <= kMaxInnerBlocks && s.hidden_blocks <= kActBytes / 256 && std::min(s.experts, pairs) * s.inner_blocks >= 128 &&
+  return s.inner_blocks <= kMaxInnerBlocks && s.hidden_blocks <= kActBytes / 256 && std::min(s.experts, pairs) * s.inner_blocks >= kStreamSets &&
          !misaligned(b.gate_up_packed, 16) && !misaligned(b.down_packed, 16) && !misaligned(b.gate_up_norms, 4) &&
          !misaligned(b.down_norms, 4) && (s.hidden * s.inner_blocks) % 2 == 0;
 }
