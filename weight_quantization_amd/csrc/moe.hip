@@ -1172,18 +1172,21 @@ int launch_product(const ProductArgs& a, hipStream_t stream) {
 }
 
 // Whether the pairs are few enough for the two kernels that do the most by
-// themselves, but read an expert's codes again for each pair.  Measured (all kernels
-// of a layer with 5 bits, us; pairs, hidden x inner, blocks of codes they read):
-//   8 of 2048 x 512, 197 thousand    22.9, by the product kernels 29.5
-//   32 of 2048 x 128, 197 thousand   22.5, 31.2
-//   16 of 2048 x 512, 393 thousand   30.8, 34.7
-//   32 of 2048 x 512, 786 thousand   51.4, 39.1
-//   8 of 4096 x 1024, 786 thousand   38.1, 40.0
-//   32 of 4096 x 1024, 3.1 million   115, 47
-constexpr int64_t kFewCodes = 1 << 19;  // blocks
-bool few(const Sizes& s, int64_t pairs) {
+// themselves, but read an expert's codes again for each pair: those of one or two
+// tokens, or of little to read.  Measured (all kernels of a layer with 5 bits, us;
+// tokens x experts of each, hidden x inner, blocks of codes read for all pairs):
+//   1 x 8, 2048 x 512, 197 thousand     22.9, by the product kernels 29.5
+//   1 x 8, 4096 x 2048, 1.6 million     70.6, 84.3
+//   2 x 8, 2048 x 512, 393 thousand     30.8, 34.7
+//   2 x 8, 4096 x 1024, 1.6 million     68.3, 72.4
+//   3 x 8, 2048 x 512, 590 thousand     42.9, 37.9
+//   4 x 8, 2048 x 512, 786 thousand     51.4, 39.1
+//   8 x 4, 2048 x 128, 197 thousand     22.5, 31.2
+//   16 x 2, 4096 x 1024, 3.1 million    115, 47
+constexpr int64_t kFewCodes = 3 << 17;  // blocks
+bool few(const Sizes& s, int64_t tokens, int64_t pairs) {
   return pairs <= kFewPairs && s.hidden_blocks <= kFewBlocks && s.inner_blocks <= kFewBlocks &&
-         pairs * (2 * s.inner * s.hidden_blocks + s.hidden * s.inner_blocks) <= kFewCodes;
+         ((tokens <= 2 && pairs <= 16) || pairs * (2 * s.inner * s.hidden_blocks + s.hidden * s.inner_blocks) <= kFewCodes);
 }
 template <int BITS>
 int launch_few(const FewArgs& up, const ProductArgs& down, hipStream_t stream) {
@@ -1272,7 +1275,7 @@ int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t to
     pa.hidden = i32(s.hidden);
     pa.experts = i32(s.experts);
     pa.expert_groups = i32(ceil_div(s.experts, router_tile(n).experts * kRouterWaves));
-    const bool is_few = !empty && few(s, m);
+    const bool is_few = !empty && few(s, n, m);
     pa.rotating = empty || is_few ? 0 : i32(n);
     const int64_t preparing = pa.rotating + (route && m > 0 ? pa.expert_groups * ceil_div(n, router_tile(n).tokens) : 0);
     if (preparing > 0 &&
