@@ -161,3 +161,30 @@ def test_replays_streams_and_repeats(wq, tokens, bits):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(y, want))
+
+
+def test_two_graphs_share_a_workspace(wq):
+    """Captured calls of different sizes, kernels and bits on one workspace, replayed in turn between eager calls on it."""
+    rng = np.random.default_rng(10)
+    experts, hidden, inner, k = 64, 520, 260, 8
+    router = bf16(rng, experts, hidden)[0].cuda()
+    banks = {b: (*dev(bank(rng, experts, 2 * inner, hidden, b)), *dev(bank(rng, experts, hidden, inner, b))) for b in (5, 3)}
+    xs = [bf16(rng, n, hidden)[0].cuda() for n in (40, 1, 7)]
+    ws = torch.empty(wq.hlwq_moe_workspace(experts, hidden, inner, 40, k), dtype=torch.uint8, device="cuda")
+    call = lambda i, **kw: wq.hlwq_moe_layer(xs[i], router, *banks[3 if i == 2 else 5], top_k=k, bits=3 if i == 2 else 5, **kw)
+    graphs, outs = [], []
+    for i in range(3):
+        call(i, workspace=ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            outs.append(call(i, workspace=ws))
+    for _ in range(3):
+        for x in xs:
+            x.copy_(bf16(rng, *x.shape)[0])
+        wants = [call(i) for i in range(3)]
+        for i in (1, 0, 2, 0, 1):
+            for t in outs[i]:
+                t.zero_()
+            graphs[i].replay()
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], wants[i]))
+            ws.fill_(255)

@@ -341,6 +341,33 @@ def test_a_bad_query_stays_in_its_row(wq, new, width):
     assert torch.equal(got[~hit], clean[~hit])
 
 
+def test_two_graphs_share_a_workspace(wq):
+    """Captured calls with tiles of 64 rows and of 16 on one workspace, replayed in turn."""
+    rng = np.random.default_rng(15)
+    cases = []
+    for ctx, new, width in (([4200, 70], [60, 40], None), ([300, 70], [6, 4], 8)):
+        c, n = Cache(rng, ctx, 2, 3, 64, 128, 128, width=width), sum(new)
+        q, kv = bf16_bits(rng, n, 6, D), [bf16_bits(rng, n, 2, D) for _ in range(2)]
+        cases.append([dev16(q), dev16(kv[0]), dev16(kv[1]), i32(trees(rng, new, 3)), i32([0, new[0], n]),
+                      i32([t + m for t, m in zip(ctx, new)]), i32(c.table), *c.tensors()])
+    ws = torch.empty(max(wq.hlwq_kv_tree_attention_workspace(2, t[0].shape[0], 6, 2) for t in cases), dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for t in cases:
+        wq.hlwq_kv_tree_attention(*t, workspace=ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(wq.hlwq_kv_tree_attention(*t, workspace=ws))
+    for _ in range(3):
+        for t in cases:
+            t[0].copy_(dev16(bf16_bits(rng, t[0].shape[0], 6, D)))
+        wants = [wq.hlwq_kv_tree_attention(*t) for t in cases]
+        for i in (1, 0, 0, 1):
+            outs[i].zero_()
+            graphs[i].replay()
+            assert torch.equal(outs[i], wants[i])
+            ws.fill_(255)
+
+
 def test_steps_of_drafted_tokens(wq):
     """Trees through attention, an experts' layer and the verification; what is kept goes into the cache by plan and
     append, step after step, and every step's outputs are those of the definition on a cache built token by token."""
