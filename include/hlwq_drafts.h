@@ -90,9 +90,9 @@ typedef struct hlwq_drafts {
  * Without `draft` a child's q is one at its token: W_{j+1} = W_j - p(x), and p(x)
  * counts as 0 from then on.
  *
- * p need not sum to one.  Probabilities below 0 and NaN count as 0 in sums.  A
- * token outside [0, vocab) is passed over, as are a request's rows from the
- * 4096th on.  Sums and products are in 64 bits.  vocab from 1 to 2^24, at most
+ * p need not sum to one.  Probabilities below 0 and NaN, of target and draft,
+ * count as 0.  A token outside [0, vocab) is passed over, as are a request's rows
+ * from the 4096th on.  Sums and products are in 64 bits.  vocab from 1 to 2^24, at most
  * 2^20 requests, rows below 2^31, strides at most 2^40; target and draft aligned
  * to their type, the others to 4 bytes. */
 int hlwq_verify_drafts(const hlwq_drafts* drafts, void* hip_stream);

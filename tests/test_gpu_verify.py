@@ -237,3 +237,34 @@ def test_no_requests_and_refusals(wq):
         wq.hlwq_verify_drafts(t[:3], t, cu, p, u, un)
     with pytest.raises(ValueError):
         wq.hlwq_verify_drafts(t, t, cu, p[:, :0], u, un)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("vocab", [70, 1003])
+def test_a_draft_with_nan_and_negative_values(wq, vocab, dtype):
+    """Probabilities below 0 and NaN count as 0, the draft's too: in the decisions and in the sums after refusals."""
+    rng = np.random.default_rng(vocab)
+    tokens, parents, cu, p, q, u, un = inputs(rng, [9, 40, 30, 50, 12, 5], 30, vocab, dtype, True)
+    rows = np.repeat(cu[:-1], np.diff(cu)) + np.maximum(parents, 0)
+    good = [t[rows, tokens].clone() for t in (p, q)]
+    for t in (p, q):
+        what = torch.from_numpy(rng.integers(0, 12, t.shape))
+        t[what == 0] = float("nan")
+        t[what == 1] = -t[what == 1]
+    # a request's children as they were, most of them refused; of the others some kept over a q of 0
+    most = np.arange(len(tokens)) < cu[4]
+    for t, g in zip((p, q), good):
+        t[rows[most], tokens[most]] = g[most]
+    u[most] = 1 - 2.0 ** -10 * u[most]
+    # a row of q that is nothing but NaN, and children that p does not have either
+    q[0] = float("nan")
+    p[0, tokens[1:cu[1]][parents[1:cu[1]] == 0]] = 0
+    got = run(wq, tokens, parents, cu, p, q, u, un)
+    clean = [torch.where(t > 0, t, 0).double().numpy() for t in (p, q)]
+    want = vr.verify(tokens, parents, cu, *clean, u, un)
+    assert want[0][0] == 1 and max(want[0]) > 1
+    # children of a root that were refused before one was kept, or for good
+    ends = [want[2][cu[b] + 1] if want[0][b] > 1 else cu[b + 1] for b in range(6)]
+    assert sum(int(np.sum(parents[cu[b] + 1:ends[b]] == 0)) for b in range(1, 4)) > 2
+    for name, a, b in zip(("n_kept", "next_token", "kept"), got, want):
+        assert np.array_equal(a, b), (name, a, b)
