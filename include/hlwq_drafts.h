@@ -69,7 +69,7 @@ typedef struct hlwq_drafts {
   int32_t* n_kept;          /* [requests], written: rows kept, the root among them; 0 for a request of no rows */
   int32_t* next_token;      /* [requests], written: -1 for a request of no rows or a row of p without mass */
   int32_t* kept;            /* [rows], written: kept[cu_rows[b] + j] is the row of request b's j-th kept node, -1 past
-                               the last and past the last request */
+                               the last and in rows of no request (may be NULL where there are no requests) */
   int64_t requests, rows, vocab;
   int64_t target_stride, draft_stride; /* elements from row to row, at least vocab */
   int dtype;                /* of target and draft */

@@ -268,3 +268,21 @@ def test_a_draft_with_nan_and_negative_values(wq, vocab, dtype):
     assert sum(int(np.sum(parents[cu[b] + 1:ends[b]] == 0)) for b in range(1, 4)) > 2
     for name, a, b in zip(("n_kept", "next_token", "kept"), got, want):
         assert np.array_equal(a, b), (name, a, b)
+
+
+@pytest.mark.parametrize("counts,before,pad", [([], 0, 5), ([], 3, 2000), ([2, 3], 4, 3), ([0, 1], 1500, 0)])
+def test_rows_of_no_request_are_not_kept(wq, monkeypatch, counts, before, pad):
+    rng = np.random.default_rng(before + pad)
+    n, rows, vocab = len(counts), before + sum(counts) + pad, 40
+    cu = (before + np.concatenate([[0], np.cumsum(counts)])).astype(np.int32)
+    p = torch.from_numpy(softmax(rng.standard_normal((rows, vocab)))).float()
+    tokens, parents = rng.integers(0, vocab, rows).astype(np.int32), np.full(rows, -1, np.int32)
+    for b in range(n):
+        parents[cu[b] + 1:cu[b + 1]] = np.arange(counts[b] - 1) if counts[b] else 0
+    u, un = np.zeros(rows, np.float32), rng.random(n).astype(np.float32)  # everything is kept
+    monkeypatch.setattr(wq.drafts, "_empty", lambda shape, dtype, device, stream: torch.full((shape,), 7, dtype=dtype, device=device))
+    v = run(wq, tokens, parents, cu, p, None, u, un)
+    own = slice(before, before + sum(counts))
+    kept = np.full(rows, -1, np.int32)
+    kept[own] = np.arange(rows)[own]
+    assert np.array_equal(v[2], kept) and v[0].tolist() == counts

@@ -221,9 +221,15 @@ __global__ void __launch_bounds__(kVerifyThreads) hlwq_verify_kernel(const Verif
   __shared__ float node_u[64], node_p[64], node_q[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t b = blockIdx.x;
+  const auto not_kept = [&](int64_t from, int64_t to) {
+    for (int64_t i = from + threadIdx.x; i < to; i += kVerifyThreads) a.kept[i] = -1;
+  };
+  if (a.requests == 0) return not_kept(0, a.rows);
   const RowRange rr = row_range(a.cu, b, a.rows);
-  if (b == 0)  // rows past the last request
-    for (int64_t i = static_cast<int64_t>(row_range(a.cu, a.requests - 1, a.rows).end) + threadIdx.x; i < a.rows; i += kVerifyThreads) a.kept[i] = -1;
+  if (b == 0) {  // rows before the first request and past the last
+    not_kept(0, rr.begin);
+    not_kept(row_range(a.cu, a.requests - 1, a.rows).end, a.rows);
+  }
   const int32_t count = min(rr.end - rr.begin, kMaxNodes);
   if (count <= 0) {
     if (threadIdx.x == 0) {
@@ -326,10 +332,10 @@ int run_verify(const hlwq_drafts* d, hipStream_t stream) {
   if (d->requests > kMaxRequests || d->rows > 0x7fffffff || d->vocab > kMaxVocab || d->target_stride > kMaxRowStride ||
       (d->draft && d->draft_stride > kMaxRowStride))
     return HLWQ_ERR_LIMIT;
-  if (d->requests == 0) return HLWQ_OK;
+  if (d->requests == 0 && (d->rows == 0 || !d->kept)) return HLWQ_OK;
   const uintptr_t size = d->dtype == HLWQ_F32 ? 4 : 2;
-  if (!d->cu_rows || !d->n_kept || !d->next_token || !d->next_uniforms ||
-      (d->rows > 0 && (!d->tokens || !d->parents || !d->target || !d->uniforms || !d->kept)))
+  if (d->requests > 0 && (!d->cu_rows || !d->n_kept || !d->next_token || !d->next_uniforms ||
+                          (d->rows > 0 && (!d->tokens || !d->parents || !d->target || !d->uniforms || !d->kept))))
     return HLWQ_ERR_NULL;
   int64_t te, de, bytes;
   if (!mul_ok(d->rows, d->target_stride, &te) || !mul_ok(te, 4, &bytes) ||
@@ -369,7 +375,7 @@ int run_verify(const hlwq_drafts* d, hipStream_t stream) {
   a.requests = static_cast<int32_t>(d->requests);
   a.rows = static_cast<int32_t>(d->rows);
   a.vocab = static_cast<int32_t>(d->vocab);
-  const dim3 grid(static_cast<uint32_t>(d->requests));
+  const dim3 grid(static_cast<uint32_t>(std::max<int64_t>(d->requests, 1)));
   const auto go = [&](auto type) {
     using T = decltype(type);
     return d->draft ? launch(hlwq_verify_kernel<T, true>, grid, dim3(kVerifyThreads), stream, a)

@@ -37,7 +37,7 @@ class VerifiedDrafts(NamedTuple):
     """What hlwq_verify_drafts writes, int32 on the device."""
     n_kept: torch.Tensor      # [requests] rows kept, the root among them
     next_token: torch.Tensor  # [requests] the token that follows them
-    kept: torch.Tensor        # [rows] rows kept, a request's from its first row's place on; -1 past them
+    kept: torch.Tensor        # [rows] rows kept, a request's from its first row's place on; -1 elsewhere
 
 
 def hlwq_kv_tree_attention_workspace(requests: int, rows: int, q_heads: int, kv_heads: int) -> int:
