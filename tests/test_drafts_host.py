@@ -183,3 +183,14 @@ def test_python_refusals_without_a_device():
         wq.hlwq_verify_drafts(x, x, x, torch.zeros(2, 9), x, torch.zeros(1))
     with pytest.raises(TypeError):
         wq.hlwq_kv_tree_attention(None, None, None, None, None, None, None, None, None, None, None, None, None)
+
+
+def test_routing_of_rows_of_nothing_checks_what_it_writes(lib):
+    b = banks(hidden=0)
+    assert given(lib, b, xs=0, x=None, ids=None, w=None, out=None, ws=None) == OK
+    assert layer(lib, b, xs=0, k=0, x=None, ids=None, w=None, out=None, ws=None) == OK
+    assert layer(lib, b, xs=0, tokens=0, x=None, ids=None, w=None, out=None, ws=None) == OK
+    none = dict(xs=0, x=None, out=None, ws=None)
+    assert layer(lib, b, ids=None, **none) == ENULL and layer(lib, b, w=None, **none) == ENULL
+    assert layer(lib, b, ids=at(6) + 1, **none) == EALIGN and layer(lib, b, w=at(7) + 2, **none) == EALIGN
+    assert layer(lib, b, w=at(6) + 20, **none) == EOVERLAP and layer(lib, b, k=9, **none) == ESHAPE

@@ -270,3 +270,18 @@ def test_refusals_raise(wq):
         wq.hlwq_moe_layer(x, router, *up, *down, top_k=2, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(wq.HLWQError):
         wq.hlwq_moe_layer(x, router, *up, *down, top_k=2, out=x)
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("tokens,experts,k", [(1, 1, 1), (3, 7, 7), (200, 300, 5)])
+def test_rows_of_nothing_are_routed_all_the_same(wq, monkeypatch, tokens, experts, k, renormalize):
+    """No hidden values: every logit is 0, so the first experts are chosen, with equal weights."""
+    empty = torch.empty
+    monkeypatch.setattr(wq.moe, "_empty", lambda shape, dtype, device, stream: empty(shape, dtype=dtype, device=device).fill_(77))
+    rng = np.random.default_rng(0)
+    up, down = bank(rng, experts, 64, 0, 5), bank(rng, experts, 0, 32, 5)
+    x, router = (torch.zeros(n, 0, dtype=torch.bfloat16, device="cuda") for n in (tokens, experts))
+    y = wq.hlwq_moe_layer(x, router, *dev(up), *dev(down), top_k=k, renormalize=renormalize)
+    assert y.out.shape == (tokens, 0)
+    assert torch.equal(y.experts.cpu(), torch.arange(k, dtype=torch.int32).expand(tokens, k))
+    assert np.array_equal(y.weights.cpu().numpy(), np.full((tokens, k), np.float32(1 / (k if renormalize else experts))))

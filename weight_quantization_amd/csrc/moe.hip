@@ -300,6 +300,14 @@ __global__ void __launch_bounds__(kTopThreads) hlwq_moe_top_kernel(const TopArgs
   }
 }
 
+// Tokens of no hidden values: all logits are 0.
+__global__ void __launch_bounds__(kTopThreads) hlwq_moe_even_kernel(const TopArgs a) {
+  const int64_t p = static_cast<int64_t>(blockIdx.x) * kTopThreads + threadIdx.x;
+  if (p >= static_cast<int64_t>(a.tokens) * a.top_k) return;
+  a.ids[p] = static_cast<int32_t>(p % a.top_k);
+  a.weights[p] = static_cast<float>(1.0 / (a.renormalize ? a.top_k : a.experts));
+}
+
 // ---------------------------------------------------------------------------
 // Products with an expert's codes, where the named experts are not many.  A
 // workgroup takes the a-th of the experts that some pair names and some tiles of
@@ -1123,7 +1131,7 @@ struct Sizes {
   int64_t pass;  // tokens to a pass
 };
 
-// *nothing: valid, with no work.
+// *nothing: valid, with no work but the routing's.
 int check_sizes(Sizes& s, bool* nothing) {
   if (s.experts < 0 || s.hidden < 0 || s.inner < 0 || s.tokens < 0 || s.top_k < 0) return HLWQ_ERR_SHAPE;
   if (s.experts > kMaxExperts || s.hidden > kMaxSize || s.inner > kMaxSize || s.top_k > kMaxTopK || s.tokens > kMaxTokens)
@@ -1232,8 +1240,20 @@ int run_moe(const hlwq_moe_banks* b, const void* x, int64_t x_stride, int64_t to
   const int64_t block = 16 * b->bits;
   if (x_stride > kMaxSize || 2 * s.inner * s.hidden_blocks > 0x7fffffff / block || s.hidden * s.inner_blocks > 0x7fffffff / block)
     return HLWQ_ERR_LIMIT;
-  if (nothing) return HLWQ_OK;
-  const int64_t pairs = tokens * top_k, up = s.experts * 2 * s.inner * s.hidden_blocks, down = s.experts * s.hidden * s.inner_blocks;
+  const int64_t pairs = tokens * top_k;
+  if (nothing) {
+    if (!route || pairs == 0) return HLWQ_OK;
+    if (!ids || !weights) return HLWQ_ERR_NULL;
+    if (misaligned(ids, 4) || misaligned(weights, 4)) return HLWQ_ERR_ALIGN;
+    Spans spans;
+    add_span(spans, ids, pairs, 4, true);
+    add_span(spans, weights, pairs, 4, true);
+    if (check_disjoint(spans) != HLWQ_OK) return HLWQ_ERR_OVERLAP;
+    const TopArgs a{nullptr, ids, weights, static_cast<int32_t>(tokens), static_cast<int32_t>(s.experts), static_cast<int32_t>(top_k),
+                    renormalize != 0};
+    return launch(hlwq_moe_even_kernel, dim3(static_cast<uint32_t>(ceil_div(pairs, kTopThreads))), dim3(kTopThreads), stream, a);
+  }
+  const int64_t up = s.experts * 2 * s.inner * s.hidden_blocks, down = s.experts * s.hidden * s.inner_blocks;
   const Parts parts = parts_of(s);
   if (!x || !out || !ws || (route && s.experts > 0 && !router) || (pairs > 0 && (!ids || !weights)) ||
       (up > 0 && (!b->gate_up_packed || !b->gate_up_norms)) || (down > 0 && (!b->down_packed || !b->down_norms)))
