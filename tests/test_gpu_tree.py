@@ -266,6 +266,21 @@ def test_wide_large_trees(wq, new, wide):
     wide_case(wq, wide, [200] * len(new), new, 2, 1, wide=wide)
 
 
+@pytest.mark.parametrize("ctx", [20800, 45000])
+@pytest.mark.parametrize("bits,page", [(3, 16), (2, 64)])
+def test_wide_stretches_of_many_pages(wq, ctx, bits, page):
+    """Page ids are read 32 blocks of 64 tokens at a time: 24 tiles over 232 workgroups, 34 and 73 blocks each."""
+    wide_case(wq, ctx, [ctx], [64], 24, 1, bits, page)
+
+
+def test_wide_many_requests(wq):
+    # more of them than a wave looks through at once, empty ones among them
+    rng = np.random.default_rng(16)
+    ctx = [int(x) for x in rng.integers(0, 400, 75)]
+    new = [0 if b in (0, 30, 64, 74) else int(x) for b, x in enumerate(rng.integers(6, 14, 75))]
+    wide_case(wq, 16, ctx, new, 24, 4, 3, 32)
+
+
 def test_wide_rows_left_alone_and_replayed(wq):
     """Rows of a request of too many nodes, outputs on two streams at once, and a captured call."""
     rng = np.random.default_rng(12)
