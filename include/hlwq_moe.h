@@ -55,14 +55,14 @@ typedef struct hlwq_moe_banks {
 } hlwq_moe_banks;
 
 /* The experts of tokens whose routing is known: x bf16 [tokens][hidden], rows
- * x_stride elements apart (at least hidden), experts i32 and weights fp32
+ * x_stride elements apart (at least hidden, at most 2^20), experts i32 and weights fp32
  * [tokens][top_k], out bf16 [tokens][hidden].  top_k at most 32.  An expert
  * outside [0, banks->experts) adds nothing; one named twice adds twice.  NaN and
  * infinities in a token's row make only its own output NaN.
  *
  * `workspace`: hlwq_moe_workspace bytes, 16-byte aligned, contents immaterial
  * before and after.  x and out 2-byte aligned, experts and weights 4.
- * HLWQ_ERR_LIMIT: sizes past those stated, or 2^24 tokens. */
+ * HLWQ_ERR_LIMIT: sizes past those stated, or more than 2^24 tokens. */
 int hlwq_moe_experts(const hlwq_moe_banks* banks, const void* x_bf16, int64_t x_stride, int64_t tokens, int64_t top_k,
                      const int32_t* experts, const float* weights, void* out_bf16, void* workspace,
                      size_t workspace_bytes, void* hip_stream);

@@ -285,3 +285,22 @@ def test_rows_of_nothing_are_routed_all_the_same(wq, monkeypatch, tokens, expert
     assert y.out.shape == (tokens, 0)
     assert torch.equal(y.experts.cpu(), torch.arange(k, dtype=torch.int32).expand(tokens, k))
     assert np.array_equal(y.weights.cpu().numpy(), np.full((tokens, k), np.float32(1 / (k if renormalize else experts))))
+
+
+def test_row_strides_up_to_the_limit(wq):
+    # a token of each of two sequences of 512 x 2048: rows 2^20 elements apart, and of 513 x 2048, which is refused
+    rng = np.random.default_rng(14)
+    up, down = dev(bank(rng, 4, 64, 2048, 5)), dev(bank(rng, 4, 2048, 32, 5))
+    x, router = bf16(rng, 2, 2048)[0].cuda(), bf16(rng, 4, 2048)[0].cuda()
+    want = wq.hlwq_moe_layer(x, router, *up, *down, top_k=2)
+    h = torch.zeros(2, 513, 2048, dtype=torch.bfloat16, device="cuda")
+    h[:, -1] = x
+    near = h.view(-1)[:2 * 512 * 2048].view(2, 512, 2048)
+    near[:, -1] = x
+    assert near[:, -1].stride() == (2 ** 20, 1)
+    assert all(torch.equal(a, b) for a, b in zip(wq.hlwq_moe_layer(near[:, -1], router, *up, *down, top_k=2), want))
+    h[:, -1] = x
+    with pytest.raises(wq.HLWQError):
+        wq.hlwq_moe_layer(h[:, -1], router, *up, *down, top_k=2)
+    assert torch.equal(wq.hlwq_moe_layer(h[:, -1].contiguous(), router, *up, *down, top_k=2).out, want.out)
+    assert torch.equal(wq.hlwq_moe_layer(h[1:, -1], router, *up, *down, top_k=2).out, want.out[1:])  # there is no next row
