@@ -80,7 +80,6 @@ __device__ __forceinline__ void rotate_row(F at, int32_t n, uint16_t* __restrict
   const float f = __builtin_ldexpf(1.0f, 7 - e);
   if (threadIdx.x == 0) *scale = __builtin_ldexpf(1.0f, e - 7 - 7);  // and the blocks' 1 / 128
   const int32_t nb = static_cast<int32_t>(ceil_div(n, kBlock));
-#pragma unroll 2
   for (int32_t b = wave; b < nb; b += kRotateThreads / 64) {
     const int32_t i = b * kBlock + 2 * lane;
     const f32x2 v = i < n ? at(i) : f32x2{0, 0};
@@ -1167,16 +1166,30 @@ Parts parts_of(const Sizes& s) {
   return p;
 }
 
+// Four waves to a row's blocks, or eight with two blocks each at a time.  Measured
+// (5 bits, us, a kernel's time for gate and up, four waves and eight; x1: a pair or
+// two to an expert, 16 tokens x 2 of 32 experts, 1024 values out from 20 blocks on):
+//   2 blocks of a row, x1     5.6, 6.5      12, x1    23, 32
+//   4, x1                     7.4, 10.7     16, x1    40, 53
+//   6, x1                     8.6, 13.4     24, x1    33, 36
+//   8, x1                    14.6, 19.4     40, x1    51, 46
+// and the whole layer, all blocks with four or all with eight:
+//   100 tokens x 4 of 8, 2048 x 512 (16 and 4 blocks)      73, 59
+//   100 x 2 of 8, 4096 x 1408 (32 and 11)                 134, 118
+//   33 x 1 of 2, 768 x 2048 (6 and 16)                     42, 34
+//   1 x 2 of 8, 4096 x 14336 (32 and 112)                 132, 113
+//   12 x 4 of 12, 640 x 1920 (5 and 15)                    31, 37
+// Long rows are those of few large experts as a rule, to which many pairs come;
+// where they are not, eight waves lose.  (Four with two blocks at a time and
+// eight with three took as long or longer at every size.)
 template <int BITS, bool GATED>
 int launch_product(const ProductArgs& a, hipStream_t stream) {
   const auto go = [&](auto kernel, int groups) {
     const uint32_t wide = static_cast<uint32_t>(ceil_div(a.tiles, groups));
     return launch(kernel, dim3(wide, static_cast<uint32_t>(std::min(a.experts, a.pairs))), dim3(kProductThreads), stream, a);
   };
-  if (a.nb <= 4) return go(hlwq_moe_product_kernel<BITS, 4, 1, GATED>, 2);
-  if (a.nb <= 8) return go(hlwq_moe_product_kernel<BITS, 4, 2, GATED>, 2);
-  if (a.nb <= 16) return go(hlwq_moe_product_kernel<BITS, 8, 2, GATED>, 1);
-  return go(hlwq_moe_product_kernel<BITS, 8, 3, GATED>, 1);
+  if (a.nb <= 8) return go(hlwq_moe_product_kernel<BITS, 4, 1, GATED>, 2);
+  return go(hlwq_moe_product_kernel<BITS, 8, 2, GATED>, 1);
 }
 
 // Whether the pairs are few enough for the two kernels that do the most by
