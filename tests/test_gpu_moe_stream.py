@@ -188,3 +188,14 @@ def test_two_graphs_share_a_workspace(wq):
             graphs[i].replay()
             assert all(torch.equal(a, b) for a, b in zip(outs[i], wants[i]))
             ws.fill_(255)
+
+
+@pytest.mark.parametrize("tokens,experts,hidden,inner,k", [
+    # several passes over one bank or both, few enough to be streamed ..
+    (40, 20, 140, 7000, 1), (60, 20, 140, 7000, 2), (80, 20, 100, 8192, 2), (100, 16, 2100, 1270, 4), (70, 80, 5120, 130, 4),
+    # .. and too many
+    (200, 80, 5120, 130, 8), (150, 24, 8200, 840, 5), (130, 3, 130, 8190, 2),
+])
+@pytest.mark.parametrize("bits", [5, 3])
+def test_either_side_of_what_passes_cost(wq, tokens, experts, hidden, inner, k, bits):
+    given(wq, np.random.default_rng(tokens + hidden), tokens, experts, hidden, inner, k, bits, "silu")

@@ -629,6 +629,9 @@ constexpr int kMaxInnerBlocks = 64;  // whose scales a workgroup keeps
 // Of activations in LDS.  (40 KB, and four copies of the pairs of 5-bit codes, took 2%
 // less for 64 and 192 tokens of 256 experts; but busier experts take passes more.)
 constexpr int kActBytes = 48 << 10;
+// Pairs of a pass over an expert's codes, of rows of nb blocks: sixteen up to 1536
+// values, 12 at 2048, 6 at 4096, 4 at 5120, one past 12288.
+__host__ __device__ inline int32_t pass_pairs(int64_t nb) { return static_cast<int32_t>(nb * 256 * kTile <= kActBytes ? kTile : kActBytes / (nb * 256)); }
 constexpr int kChunk = 4;            // blocks that are staged together
 constexpr int kWithoutBook = 1;      // fours of 32 5-bit codes whose centroids come from registers
 
@@ -656,7 +659,7 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
   const uint32_t copy = book_copy<BITS>(lane);
 
   const int32_t sets = a.tiles;  // of 128 or 256 rows
-  const int32_t capacity = min(kTile, kActBytes / (a.nb * 256));
+  const int32_t capacity = pass_pairs(a.nb);
 
   // The experts' pairs, and this workgroup's run of (expert, pass over as many of
   // its pairs as fit, set): passes cost the same whatever their pairs.
@@ -1220,19 +1223,48 @@ int launch_few(const FewArgs& up, const ProductArgs& down, hipStream_t stream) {
   return launch(hlwq_moe_few_down_kernel<BITS>, dim3(static_cast<uint32_t>(ceil_div(up.hidden, kTile))), dim3(kProductThreads), stream, a);
 }
 
-// Whether the touched experts' sets of rows give the CUs work enough, and the
-// banks lie as the loads to LDS take them.  Measured (as above; sets of gate and up
-// if no expert is named twice):
-//   32 of 256 experts, 2048 x 512, 128 sets     47.1, by the product kernels 39.1
-//   64 of 64, 1024 x 256, 128                   37.1, 30.7
-//   64 of 8, 4096 x 2048, 128                   83.0, 84.6
-//   128 of 256, 2048 x 128, 128                 49.1, 48.6
-//   192 of 256, 2048 x 128, 192                 50.8, 56.3
+// Whether the touched experts' sets of rows give the CUs work enough, the banks lie
+// as the loads to LDS take them, and these do not go through the codes much more
+// often than the product kernels, which take sixteen pairs of an expert at a time.
+// Measured (as above; streamed, by the product kernels; sets of gate and up, if no
+// expert is named twice):
+//   4 tokens x 8 of 256, 2048 x 512, 128 sets     48.5, 47.3
+//   8 x 8 of 64, 1024 x 256, 128                  34.9, 31.4
+//   32 x 2 of 8, 4096 x 2048, 128                 80.4, 78.6
+//   16 x 8 of 256, 2048 x 128, 128                51.8, 56.6
+//   40 x 8 of 160, 512 x 128, 160                 35.5, 33.2
+//   40 x 2 of 20, 2048 x 1024, 160                50.7, 55.4
+//   24 x 8 of 256, 2048 x 128, 192                55.6, 71.7
+//   64 x 8 of 256, 2048 x 512, 1024                141, 225
+// Passes: a touched expert has pairs / touched pairs, more or less, so what is left
+// over takes half a pass of its own; two thirds of the codes are gate and up.  A
+// pass here is worth half of one of theirs.  Pairs of an expert, pairs of a pass
+// over either bank, us as above:
+//   512 x 4 of 16, 2048 x 2048: 128, 12 and 12     350, 575
+//   200 x 4 of 32, 4096 x 1408: 25, 6 and 16       323, 378
+//   256 x 8 of 64, 3584 x 512: 32, 6 and 16        261, 280
+//   100 x 4 of 16, 1024 x 4096: 25, 16 and 6       142, 139
+//   64 x 4 of 8, 2880 x 2880: 32, 8 and 8          173, 150
+//   32 x 4 of 32, 5120 x 1000: 4, 4 and 16         140, 139
+// and past it:
+//   300 x 2 of 16, 4096 x 2048: 38, 6 and 12       332, 376
+//   100 x 2 of 8, 4096 x 2560: 25, 6 and 9         186, 183
+//   200 x 2 of 8, 4096 x 4096: 50, 6 and 6         477, 448
+//   100 x 8 of 32, 5120 x 1000: 25, 4 and 16       365, 331; with 3 bits 257, 256
+//   100 x 4 of 16, 6144 x 2560: 25, 4 and 9        572, 467
+//   100 x 4 of 16, 1024 x 8192: 25, 16 and 3       297, 261
+//   100 x 2 of 8, 8192 x 4096: 25, 3 and 6         752, 495
+//   256 x 8 of 64, 7168 x 2048: 32, 3 and 12      3117, 1978
 constexpr int64_t kStreamSets = 160;
 bool streams(const hlwq_moe_banks& b, const Sizes& s, int64_t pairs) {
-  return s.inner_blocks <= kMaxInnerBlocks && s.hidden_blocks <= kActBytes / 256 && std::min(s.experts, pairs) * s.inner_blocks >= kStreamSets &&
-         !misaligned(b.gate_up_packed, 16) && !misaligned(b.down_packed, 16) && !misaligned(b.gate_up_norms, 4) &&
-         !misaligned(b.down_norms, 4) && (s.hidden * s.inner_blocks) % 2 == 0;
+  const int64_t touched = std::min(s.experts, pairs);
+  if (s.inner_blocks > kMaxInnerBlocks || s.hidden_blocks > kActBytes / 256 || touched * s.inner_blocks < kStreamSets ||
+      misaligned(b.gate_up_packed, 16) || misaligned(b.down_packed, 16) || misaligned(b.gate_up_norms, 4) ||
+      misaligned(b.down_norms, 4) || (s.hidden * s.inner_blocks) % 2 != 0)
+    return false;
+  const double each = static_cast<double>(pairs) / static_cast<double>(touched);
+  const auto passes = [each](int32_t of) { return std::max(1.0, each / of + 0.5); };
+  return 2 * passes(pass_pairs(s.hidden_blocks)) + passes(pass_pairs(s.inner_blocks)) < 2 * 3 * passes(kTile);
 }
 template <int BITS, bool GATED>
 int launch_stream(ProductArgs a, hipStream_t stream) {
