@@ -199,3 +199,21 @@ def test_two_graphs_share_a_workspace(wq):
 @pytest.mark.parametrize("bits", [5, 3])
 def test_either_side_of_what_passes_cost(wq, tokens, experts, hidden, inner, k, bits):
     given(wq, np.random.default_rng(tokens + hidden), tokens, experts, hidden, inner, k, bits, "silu")
+
+
+@pytest.mark.parametrize("tokens,experts,hidden,inner,k", [
+    # one token's pairs, up to eight, and inner values of up to 16 blocks ..
+    (1, 9, 4000, 2048, 8), (1, 9, 4000, 2048, 9), (1, 5, 300, 2049, 2), (2, 9, 4000, 700, 4),
+    # .. and 393216 blocks in all
+    (32, 40, 1024, 256, 1), (8, 20, 2048, 256, 4), (8, 20, 2048, 257, 4),
+])
+@pytest.mark.parametrize("bits", [5, 3])
+def test_either_side_of_what_is_little(wq, tokens, experts, hidden, inner, k, bits):
+    rng = np.random.default_rng(hidden + inner)
+    x, xf = bf16(rng, tokens, hidden)
+    router, rf = bf16(rng, experts, hidden, sigma=1.5 / np.sqrt(hidden))
+    up, down = bank(rng, experts, 2 * inner, hidden, bits), bank(rng, experts, hidden, inner, bits)
+    y = wq.hlwq_moe_layer(x.cuda(), router.cuda(), *dev(up), *dev(down), top_k=k, bits=bits)
+    ids, _ = mr.route(xf, rf, k, True)
+    assert np.array_equal(y.experts.cpu().numpy(), ids)
+    mr.check(f64(y.out), *mr.experts(xf, ids, y.weights.cpu().numpy(), up, down, bits, "silu"))

@@ -1196,21 +1196,40 @@ int launch_product(const ProductArgs& a, hipStream_t stream) {
 }
 
 // Whether the pairs are few enough for the two kernels that do the most by
-// themselves, but read an expert's codes again for each pair: those of one or two
-// tokens, or of little to read.  Measured (all kernels of a layer with 5 bits, us;
-// tokens x experts of each, hidden x inner, blocks of codes read for all pairs):
-//   1 x 8, 2048 x 512, 197 thousand     22.9, by the product kernels 29.5
-//   1 x 8, 4096 x 2048, 1.6 million     70.6, 84.3
-//   2 x 8, 2048 x 512, 393 thousand     30.8, 34.7
-//   2 x 8, 4096 x 1024, 1.6 million     68.3, 72.4
-//   3 x 8, 2048 x 512, 590 thousand     42.9, 37.9
-//   4 x 8, 2048 x 512, 786 thousand     51.4, 39.1
-//   8 x 4, 2048 x 128, 197 thousand     22.5, 31.2
-//   16 x 2, 4096 x 1024, 3.1 million    115, 47
-constexpr int64_t kFewCodes = 3 << 17;  // blocks
+// themselves, but read an expert's codes again for each pair, and whose second one
+// gives a pair's row of inner values to a wave: up to 16 blocks of them, and one
+// token's pairs, a wave each, or of little to read.  Measured (all kernels of a
+// layer with 5 bits, us; tokens x experts of each, hidden x inner, blocks of codes
+// read for all pairs; by these, by the kernels of many pairs):
+//   1 x 8 of 256, 2048 x 512, 197 thousand     22.4, 28.0
+//   8 x 4 of 256, 2048 x 128, 197 thousand     22.1, 30.0
+//   32 x 1 of 128, 1024 x 256, 197 thousand    22.7, 23.2
+//   1 x 8 of 128, 2816 x 704, 383 thousand     28.1, 34.4
+//   2 x 8 of 256, 2048 x 512, 393 thousand     30.1, 32.8
+//   8 x 4 of 64, 2048 x 256, 393 thousand      28.9, 32.8
+//   1 x 2 of 8, 4096 x 2048, 393 thousand      35.1, 33.0
+//   16 x 2 of 64, 1024 x 512, 393 thousand     37.3, 27.3
+//   1 x 8 of 64, 4096 x 1024, 786 thousand     38.1, 45.1
+//   1 x 4 of 16, 4096 x 2048, 786 thousand     44.0, 44.6
+//   1 x 8 of 64, 4096 x 2048, 1.6 million      69.3, 70.4
+//   1 x 8 of 256, 7168 x 2048, 2.8 million      102, 108
+// more pairs or tokens, which may name the same experts:
+//   2 x 10 of 512, 2048 x 512, 492 thousand    49.5, 44.2
+//   3 x 8 of 256, 2048 x 512, 590 thousand     42.6, 39.3
+//   2 x 8 of 128, 2816 x 704, 766 thousand     43.0, 41.6
+//   1 x 16 of 256, 2048 x 1024, 786 thousand   53.5, 49.7
+//   2 x 4 of 32, 4096 x 1408, 1.1 million      49.5, 53.9
+//   2 x 4 of 8, 4096 x 2048, 1.6 million       64.1, 57.9
+//   2 x 8 of 8, 4096 x 2048, 3.1 million        120, 71
+//   2 x 8 of 256, 7168 x 2048, 5.5 million      186, 127
+// more than 16 blocks of inner values:
+//   1 x 2 of 8, 1024 x 4096, 197 thousand      40.7, 30.5
+//   1 x 1 of 8, 4096 x 4096, 393 thousand      47.0, 36.6
+//   1 x 2 of 8, 4096 x 8192, 1.6 million        108, 73
+constexpr int64_t kFewCodes = 3 << 17, kFewInner = 16;  // blocks
 bool few(const Sizes& s, int64_t tokens, int64_t pairs) {
-  return pairs <= kFewPairs && s.hidden_blocks <= kFewBlocks && s.inner_blocks <= kFewBlocks &&
-         ((tokens <= 2 && pairs <= 16) || pairs * (2 * s.inner * s.hidden_blocks + s.hidden * s.inner_blocks) <= kFewCodes);
+  return pairs <= kFewPairs && s.hidden_blocks <= kFewBlocks && s.inner_blocks <= kFewInner &&
+         ((tokens == 1 && pairs <= kProductWaves) || pairs * (2 * s.inner * s.hidden_blocks + s.hidden * s.inner_blocks) <= kFewCodes);
 }
 template <int BITS>
 int launch_few(const FewArgs& up, const ProductArgs& down, hipStream_t stream) {
