@@ -26,8 +26,10 @@
  * streams may run concurrently (each with a workspace of its own).  Nothing on
  * the device is read by the host, so a call can be captured into a graph.
  *
- * Made for decode steps: up to some hundreds of tokens each touched expert's
- * codes are read from memory once.  Tokens are taken 4096 / top_k at a time.
+ * Made for decode steps.  Tokens are taken 4096 / top_k at a time, and an expert's
+ * codes are gone through once for so many of its pairs (tokens that chose it) among
+ * these: 16, or, where large banks are streamed, min(16, 192 / blocks of a row), 12
+ * at 2048 values, 6 at 4096; for a handful of pairs in all once for each.
  */
 #ifndef HLWQ_MOE_H
 #define HLWQ_MOE_H
@@ -68,7 +70,7 @@ int hlwq_moe_experts(const hlwq_moe_banks* banks, const void* x_bf16, int64_t x_
                      size_t workspace_bytes, void* hip_stream);
 
 /* The whole layer: logits = router x with router bf16 [banks->experts][hidden],
- * summed in 64 bits; the top_k experts of each token (top_k at most
+ * summed in 64 bits in a fixed order; the top_k experts of each token (top_k at most
  * banks->experts) by falling logit, equal ones by rising index, NaN below all;
  * their weights softmax(logits), over all experts, or, with renormalize, over
  * the chosen ones; then as hlwq_moe_experts, which gets them in experts and

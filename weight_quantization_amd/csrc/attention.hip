@@ -87,7 +87,11 @@ void size_split(PagedPlan& p) {
   // that they follow the first pages' workgroups.  Measured (4 KV heads, 3
   // bits, 4000 tokens a request, us), with places kept and without: 4 requests
   // 19.8 and 22.5, 8 26.4 and 25.3, 16 35.8 and 33.6, 64 87 and 74, 128 183
-  // and 154.
+  // and 154.  Of the wide kernel (24 heads on 4; tiles by the host's count): one
+  // tree of 32 rows, 16 tiles, 33 and 47; two of 64, 56 tiles, 58 and 70; four of
+  // 32, 64 tiles, 59 and 65; eight of 16, 80 tiles, 71 and 72, and over 16000
+  // tokens 222 and 173; four of 64, 112 tiles, 112 and 98; eight of 64, 224 tiles,
+  // 779 and 157.
   const int64_t resident = p.wide ? kWideResident : kSplitResident;
   p.split_workers = resident - (p.split_tiles < resident / (p.wide ? 4 : 16) ? p.split_tiles : 0);
   p.split_slots = 2 * (p.split_workers + p.split_tiles);
@@ -112,11 +116,24 @@ PagedPlan paged_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv
 // A call whose rows are trees: the split kernel's, with tiles of sixteen rows, or
 // the wide one's, with 64, which unpacks each code once for all of them but takes
 // one more launch and starts later.  The host goes by the mean, as above, and by
-// the table's width.  Measured (3 bits, 24 query and 4 KV heads, us, split and
-// wide): one request with 32767 tokens and 22 rows (132 of a KV head) 80 and 86,
-// 32 rows 97 and 89, 64 rows 169 and 154; with 4000 tokens 32 rows 37 and 37, 64
-// rows 48 and 43; with 500 64 rows 27 and 39; sixteen requests of 4000 tokens, 6
-// rows each (36) 68 and 71, 9 rows 84 and 76, 33 rows 222 and 196.
+// the table's width.  Measured (24 query and 4 KV heads, us, split and wide):
+//   one request, 3 bits    22 rows (132 of a KV head)   32 rows    64 rows
+//     over 1000 tokens              22  32               23  34     33  38
+//          2000                     26  33               30  34     39  38
+//          3000                     31  33               33  33     44  39
+//          4000                     33  34               36  33     46  40
+//         16000                     50  52               59  53     92  81
+//         32767                     76  78               90  79    154 135
+//   the same, 2 bits
+//          4000                     31  34               35  34     44  39
+//         32767                     66  76               80  77    134 131
+//   requests of 4000 tokens, 3 bits   6 rows (36)   9 rows (54)  16 rows (96)  33 rows
+//      8                               47  43        52  46        69  71     117 107
+//     16                               66  67        81  72       113 106     207 179
+//     32                              109 110       125 118       195 196     389 359
+//   8 of 16000                         93 103       106 108       158 170
+// (Rows a little past a multiple of 64 leave most of a tile empty, which is where
+// the wide one loses.)
 bool many_rows(int64_t requests, int64_t rows, int64_t group) { return rows * group >= std::max<int64_t>(48 * requests, 192); }
 constexpr int64_t kWideTokens = 4000;
 PagedPlan tree_plan(int64_t requests, int64_t rows, int64_t q_heads, int64_t kv_heads, bool wide) {

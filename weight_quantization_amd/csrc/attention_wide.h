@@ -12,10 +12,12 @@
 // A block takes 256 KB of LDS reads and 64 KB of writes (2500 cycles at 128 bytes
 // each) and about 300 VALU instructions and 32 products a wave (2400 and 1000
 // cycles of a SIMD that holds two): what bounds it is LDS and VALU alike.  One
-// request of 64 rows over 32767 tokens (3 bits, 24 query and 4 KV heads): 144 us
-// with the rotation and the joining (the split kernel's 171), of which about 54 are
-// the unpacking's, 47 the products' and the softmax's, 15 what a launch takes
-// without its blocks; 24 ragged requests of up to 16384 tokens (2 bits) 186 (238).
+// request of 64 rows over 32767 tokens (3 bits, 24 query and 4 KV heads) takes 135
+// us (on another card 144) with the rotation and the joining, tiles of sixteen rows
+// 154 to 167; 24 ragged requests of up to 16384 tokens (2 bits) 177 and 226.  Of
+// the 144 the unpacking is 51 (so much less without it), the products and the
+// softmax 37; with a single block to a workgroup 40 are left: the launches, and the
+// window's and the step's own tokens, which otherwise are done beside the pages.
 #pragma once
 
 #include "attention_split.h"

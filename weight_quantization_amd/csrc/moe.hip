@@ -149,11 +149,20 @@ __device__ __forceinline__ void router_logits(const PrepareArgs& a, int32_t e0, 
     }
 }
 // Experts and tokens to a wave: more of them read and widen each value less often,
-// fewer make more waves.  Measured (256 experts, the whole kernel, us):
-//   tokens     17    64   192
-//   1 x 2     6.1   8.9  20.2
-//   2 x 2     6.4   7.6  16.4
-//   4 x 4     7.9   8.4  13.4
+// fewer make more waves.  Measured (hidden 2048, the whole kernel, us; a layer of
+// few experts loses up to 2.5 from 97 tokens on):
+//   256 experts, tokens    2    8   17   32   48   64    96   128   192   512
+//   1 x 2                3.6  4.3  4.8  6.4  7.9 10.0  13.0  15.8  21.9  51.8
+//   2 x 2                4.1  4.4  5.0  5.7  6.8  8.7  10.7  13.0  17.4  38.7
+//   4 x 4                6.8  7.1  7.0  7.2  7.9  8.3  10.1  10.5  13.7  27.9
+//   128 experts
+//   1 x 2                3.5  4.2  4.2  4.8  5.4  6.6   8.3  10.7  12.9  29.2
+//   2 x 2                4.2  4.2  4.4  5.1  5.5  6.0   7.4   8.8  10.6  23.1
+//   4 x 4                6.6  7.0  7.1  7.1  7.8  7.8   8.1   8.5  11.0  17.9
+//   8 experts
+//   1 x 2                3.6  4.3  4.1  4.2  4.2  4.3   4.5   4.4   4.5   5.8
+//   2 x 2                3.6  4.3  4.5  4.3  4.2  4.2   5.0   4.4   4.8   6.2
+//   4 x 4                5.8  6.2  6.6  6.7  6.7  6.8   6.8   6.9   6.8   9.0
 struct RouterTile {
   int experts, tokens;
 };
@@ -311,12 +320,12 @@ __global__ void __launch_bounds__(kTopThreads) hlwq_moe_even_kernel(const TopArg
 // Products with an expert's codes, where the named experts are not many.  A
 // workgroup takes the a-th of the experts that some pair names and some tiles of
 // sixteen rows of its matrix (with GATED the same tile of gate and up); its waves
-// split the blocks of a row, KS ways, or the tiles.  Per block and tile a lane
+// split the blocks of a row, KS ways with BW at a time, or the tiles.  Per block and tile a lane
 // holds 32 codes of one row, looks them up two at a time, and they meet sixteen
 // pairs' activations in four matrix products; the norm of a row and block
 // multiplies the result, where it is one value to a lane.  What bounds it are the
 // loads, 20 bytes of another row to each lane, an address a cycle: all 256 experts of
-// 2048 x 512 would take 143 + 61 us (64 tokens), twice what streaming takes.
+// 2048 x 512 would take 143 + 62 us (64 tokens), where streaming takes 83 + 44.
 // ---------------------------------------------------------------------------
 
 constexpr int kProductThreads = 512, kProductWaves = kProductThreads / 64;
@@ -618,10 +627,10 @@ __global__ void __launch_bounds__(kProductThreads) hlwq_moe_product_kernel(const
 // different banks.  Inner values are rotated before they leave, over a power of
 // two for each block (act_scale [.][nb]).
 //
-// Measured (256 experts, hidden 2048, inner 512, 5 bits): gate and up 82 us for 64
-// tokens (298 MB of codes and norms) and 103 for 192 (344 MB), down 43 and 50: 5 TB/s
+// Measured (256 experts, hidden 2048, inner 512, 5 bits): gate and up 83 us for 64
+// tokens (298 MB of codes and norms) and 104 for 192 (344 MB), down 44 and 50: 5 TB/s
 // while every CU has a set, of which LDS look-ups take a third of the cycles and
-// VALU another; without work the kernel takes 4.  17 tokens at 3 bits 32 and 20.
+// VALU another; without work the kernel takes 4.  17 tokens at 3 bits 33 and 20.
 // ---------------------------------------------------------------------------
 
 constexpr int kWorkgroups = 256;
@@ -899,8 +908,8 @@ __global__ void __launch_bounds__(kProductThreads, 2) hlwq_moe_stream_kernel(con
 // workgroup takes sixteen rows; its waves split the blocks of one pair, or the
 // pairs.  All sixteen rows of the activations' operand are the same pair's.
 //
-// Measured (one token, 8 of 256 experts, hidden 2048, inner 512, 5 bits, 16 MB): 11.3
-// us, of which 2.9 are the choice and 4.1 the start, and 7.8.  What bounds them is
+// Measured (one token, 8 of 256 experts, hidden 2048, inner 512, 5 bits, 16 MB): 11.7
+// us, of which 2.9 are the choice and 4.1 the start, and 7.5.  What bounds them is
 // latency and the fetching of code that runs once: centroids from registers
 // instead of the book, and loops instead of unrolled blocks, change nothing.
 // ---------------------------------------------------------------------------
