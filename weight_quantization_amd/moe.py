@@ -56,7 +56,8 @@ def _banks(torch, gate_up_packed, gate_up_norms, down_packed, down_norms, hidden
 
 
 def _x(t, bf16):
-    """Tokens [tokens, hidden] in bf16, whole rows at any stride (the C function takes strides up to 2^20).  Returns the address and the stride."""
+    """Tokens [tokens, hidden] in bf16, whole rows at any stride (the C function takes strides up to 2^20).  Returns the
+    address and the stride."""
     tokens, hidden = _shape(t, 2, "x")
     if t.dtype is not bf16 or not t.is_cuda:
         _fail(t, bf16, "x")
@@ -86,9 +87,10 @@ def hlwq_moe_workspace(experts: int, hidden: int, inner: int, tokens: int, top_k
 def hlwq_moe_experts(x, experts, weights, gate_up_packed, gate_up_norms, down_packed, down_norms, bits: int = 5,
                      activation: str = "silu", out=None, workspace=None, stream=None):
     """The weighted sum of the experts' outputs for tokens whose routing is known: x bf16 [tokens, hidden] (rows at most
-    2^20 elements apart), experts int32 and weights fp32 [tokens, top_k], the banks' codes as hlwq_quantize returns them for [experts, 2 * inner, hidden]
-    (gate rows, then up rows) and [experts, hidden, inner]; activation "silu" or "gelu_tanh".  Returns bf16
-    [tokens, hidden].  workspace: uint8, hlwq_moe_workspace bytes; allocated for the call by default."""
+    2^20 elements apart), experts int32 and weights fp32 [tokens, top_k], the banks' codes as hlwq_quantize returns them
+    for [experts, 2 * inner, hidden] (gate rows, then up rows) and [experts, hidden, inner]; activation "silu" or
+    "gelu_tanh".  Returns bf16 [tokens, hidden].  workspace: uint8, hlwq_moe_workspace bytes; allocated for the call by
+    default."""
     torch = _torch()
     xp, xs, tokens, hidden = _x(x, torch.bfloat16)
     banks, n, inner = _banks(torch, gate_up_packed, gate_up_norms, down_packed, down_norms, hidden, bits, activation)
